@@ -1,4 +1,4 @@
-"""Python binding of libmxfp4.so (the C ABI in include/mxfp4.h and include/q4k.h).
+"""Python binding of libmxfp4.so (the C ABI in include/mxfp4.h, include/q4k.h and include/mx4.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of the library.  Tensors are torch CUDA tensors (device memory and
@@ -21,6 +21,9 @@ __all__ = [
     "mxfp4_moe_down_ex", "mxfp4_moe_cold_pairs", "mxfp4_moe_gate_up_seg", "mxfp4_moe_down_seg",
     "MOE_MODE_F32", "MOE_MODE_V41", "q4k_nbytes", "q4k_dequant", "q4k_mv", "q4k_mm",
     "mxfp4_status_string", "MM_SMALL_MAX", "EXPORTED_SYMBOLS",
+    "mxfp4_quant", "mxfp4_swiglu_quant", "mxfp4_mm_mx", "mxfp4_moe_mm_mx", "mxfp4_moe_sort",
+    "mxfp4_moe_dispatch", "mxfp4_moe_dispatch_grad", "mxfp4_moe_combine",
+    "mxfp4_moe_combine_grad", "TYPE_F32", "TYPE_BF16", "TYPE_F16", "MOE_MAX_SORTED_EXPERTS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -28,10 +31,15 @@ library_path = os.path.join(_PKG, "libmxfp4.so")
 MM_SMALL_MAX = 64
 MOE_MODE_F32 = 0
 MOE_MODE_V41 = 1
+TYPE_F32 = 0
+TYPE_BF16 = 1
+TYPE_F16 = 2
+MOE_MAX_SORTED_EXPERTS = 1024
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
 _SIG = {
     "mxfp4_status_string": (ctypes.c_char_p, [_I]),
     "mxfp4_last_cuda_error": (_I, []),
@@ -64,6 +72,16 @@ _SIG = {
     "q4k_dequant": (_I, [_P, _I, _I, _P, _P]),
     "q4k_mv": (_I, [_P, _I, _I, _P, _P, _P]),
     "q4k_mm": (_I, [_P, _I, _I, _P, _I, _P, _P]),
+    # microscaled 4-bit activations and their routing (include/mx4.h)
+    "mxfp4_quant": (_I, [_P, _I, _I, _I, _LL, _P, _I, _P, _P, _P]),
+    "mxfp4_swiglu_quant": (_I, [_P, _P, _I, _I, _I, _LL, ctypes.c_float, _P, _P, _P]),
+    "mxfp4_mm_mx": (_I, [_P, _I, _I, _P, _I, _P, _I, _P]),
+    "mxfp4_moe_mm_mx": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _I, _P]),
+    "mxfp4_moe_sort": (_I, [_P, _I, _I, _I, _P, _P, _P, _P]),
+    "mxfp4_moe_dispatch": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "mxfp4_moe_dispatch_grad": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "mxfp4_moe_combine": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "mxfp4_moe_combine_grad": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
 }
 EXPORTED_SYMBOLS = tuple(_SIG)
 _lib = None
@@ -318,3 +336,83 @@ def q4k_mv(w, rows, cols, x, y, stream=None):
 def q4k_mm(w, rows, cols, X, nb, Y, stream=None):
     _check("q4k_mm", lib().q4k_mm(_addr(w), rows, cols, _addr(X), nb, _addr(Y),
                                   _stream(stream)))
+
+
+# --- microscaled 4-bit activations and their routing (include/mx4.h) -------------
+
+_TYPE_OF = {}
+
+
+def _type(given, *tensors):
+    """The element type code of a call's dense arguments: as given, else the one dtype its
+    tensors share (different ones, one the library does not take, or addresses alone: refused)."""
+    if given is not None:
+        return given
+    if not _TYPE_OF:
+        import torch
+        _TYPE_OF.update({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
+                         torch.float16: TYPE_F16})
+    codes = {_TYPE_OF.get(t.dtype, -1) for t in tensors if hasattr(t, "dtype")}
+    return codes.pop() if len(codes) == 1 else -1
+
+
+def mxfp4_quant(x, x_rows, cols, ld, row_of, rows, out, values=None, type=None, stream=None):
+    """x (x_rows rows, ld elements apart) or its rows row_of -> the MXFP4 matrix out [rows, cols];
+    type (TYPE_*) defaults to x's dtype, which values shares."""
+    _check("mxfp4_quant", lib().mxfp4_quant(
+        _addr(x), _type(type, x, values), x_rows, cols, ld, _addr(row_of), rows, _addr(out),
+        _addr(values), _stream(stream)))
+
+
+def mxfp4_swiglu_quant(gate, up, rows, cols, ld, out, values=None, swiglu_limit=0.0, type=None,
+                       stream=None):
+    """silu(gate) * up -> the MXFP4 matrix out [rows, cols]."""
+    _check("mxfp4_swiglu_quant", lib().mxfp4_swiglu_quant(
+        _addr(gate), _addr(up), _type(type, gate, up, values), rows, cols, ld, float(swiglu_limit),
+        _addr(out), _addr(values), _stream(stream)))
+
+
+def mxfp4_mm_mx(w, rows, cols, xq, nb, Y, y_type=None, stream=None):
+    """Y [nb, rows] = X W^T of two MXFP4 matrices; y_type defaults to Y's dtype."""
+    _check("mxfp4_mm_mx", lib().mxfp4_mm_mx(_addr(w), rows, cols, _addr(xq), nb, _addr(Y),
+                                            _type(y_type, Y), _stream(stream)))
+
+
+def mxfp4_moe_mm_mx(bank, n_experts, rows, cols, xq, n_rows, offsets, Y, y_type=None,
+                    stream=None):
+    """Each expert's rows offsets[e] .. offsets[e+1] of xq with that expert's matrix."""
+    _check("mxfp4_moe_mm_mx", lib().mxfp4_moe_mm_mx(
+        _addr(bank), n_experts, rows, cols, _addr(xq), n_rows, _addr(offsets), _addr(Y),
+        _type(y_type, Y), _stream(stream)))
+
+
+def mxfp4_moe_sort(expert_ids, n_tokens, top_k, n_experts, token_at, pos_of, offsets,
+                   stream=None):
+    _check("mxfp4_moe_sort", lib().mxfp4_moe_sort(
+        _addr(expert_ids), n_tokens, top_k, n_experts, _addr(token_at), _addr(pos_of),
+        _addr(offsets), _stream(stream)))
+
+
+def mxfp4_moe_dispatch(x, n_tokens, top_k, width, token_at, xs, type=None, stream=None):
+    _check("mxfp4_moe_dispatch", lib().mxfp4_moe_dispatch(
+        _addr(x), _type(type, x, xs), n_tokens, top_k, width, _addr(token_at), _addr(xs),
+        _stream(stream)))
+
+
+def mxfp4_moe_dispatch_grad(dxs, n_tokens, top_k, width, pos_of, dx, type=None, stream=None):
+    _check("mxfp4_moe_dispatch_grad", lib().mxfp4_moe_dispatch_grad(
+        _addr(dxs), _type(type, dxs, dx), n_tokens, top_k, width, _addr(pos_of), _addr(dx),
+        _stream(stream)))
+
+
+def mxfp4_moe_combine(o, n_tokens, top_k, width, pos_of, route_w, y, type=None, stream=None):
+    _check("mxfp4_moe_combine", lib().mxfp4_moe_combine(
+        _addr(o), _type(type, o, y), n_tokens, top_k, width, _addr(pos_of), _addr(route_w),
+        _addr(y), _stream(stream)))
+
+
+def mxfp4_moe_combine_grad(dy, o, n_tokens, top_k, width, pos_of, route_w, d_o, d_route_w,
+                           type=None, stream=None):
+    _check("mxfp4_moe_combine_grad", lib().mxfp4_moe_combine_grad(
+        _addr(dy), _addr(o), _type(type, dy, o, d_o), n_tokens, top_k, width, _addr(pos_of),
+        _addr(route_w), _addr(d_o), _addr(d_route_w), _stream(stream)))

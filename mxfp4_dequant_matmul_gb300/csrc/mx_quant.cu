@@ -1,0 +1,166 @@
+// mx_quant.cu -- quantisation to MXFP4 (include/mx4.h mxfp4_quant,
+// mxfp4_swiglu_quant).
+//
+// Per group of 32 elements with largest magnitude amax: scale byte k =
+// max(0, E(amax) - 2), E the biased FP32 exponent (floor(log2 amax) + 127; 0 for
+// zeros and subnormals), code = E2M1 of x * 2^(127-k) by the hardware pair
+// conversion (nearest even, saturating at 6).  The scaling by a power of two is
+// exact unless it underflows far below half of E2M1's smallest step, so the
+// code is the only rounding.
+//
+// Bound by HBM: each element is read once and 17/32 byte (and the rounded value)
+// written.  A thread takes 8 elements (one 16-byte load in 16-bit types), four
+// lanes a group: amax by two shuffles, one 32-bit word of codes per lane (128
+// bytes per warp) and the group's scale byte from the first of the four.
+#include <cstdint>
+
+#include "common.cuh"
+#include "elem.cuh"
+#include "kernels.h"
+#include "mx4_kernels.h"
+
+namespace mxk {
+namespace {
+
+constexpr int kQThreads = 256;
+
+// Two floats -> the byte of their E2M1 codes, `lo` in the low nibble; four such
+// bytes -> a code word (elements 0..7 of v in nibbles 0..7).
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8]) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return w;
+}
+
+// 8 elements at p; kVec: p is aligned to 8 * sizeof(T) or 16 bytes.
+template <typename T, bool kVec>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+    if constexpr (kVec) {
+        constexpr int kN = 16 / sizeof(T);
+#pragma unroll
+        for (int q = 0; q < 8 / kN; ++q) {
+            const uint4 raw = ldg_stream(reinterpret_cast<const uint4*>(p) + q);
+            const Pack<T, kN> a = *reinterpret_cast<const Pack<T, kN>*>(&raw);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) v[q * kN + i] = to_f32(a.v[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+    constexpr int kN = 16 / sizeof(T);
+#pragma unroll
+    for (int q = 0; q < 8 / kN; ++q) {
+        Pack<T, kN> a;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) a.v[i] = from_f32<T>(v[q * kN + i]);
+        *reinterpret_cast<Pack<T, kN>*>(p + q * kN) = a;
+    }
+}
+
+// silu(g) * u in FP32 with the limit of the routed-expert passes.
+__device__ __forceinline__ float swiglu(float g, float u, float limit) {
+    return moe_act(g, u, MoeAct{nullptr, limit, 0}, 0);
+}
+
+template <typename T, bool kAct, bool kVec>
+__global__ void __launch_bounds__(kQThreads)
+    k_mx_quant(const T* __restrict__ x, const T* __restrict__ up, int x_rows, int cols,
+               long long ld, const int32_t* __restrict__ row_of, float limit, int rows,
+               uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
+               T* __restrict__ values) {
+    const int per_row = cols / 8;
+    const size_t n = static_cast<size_t>(rows) * per_row;   // a multiple of 4
+    for (size_t base = static_cast<size_t>(blockIdx.x) * kQThreads; base < n;
+         base += static_cast<size_t>(gridDim.x) * kQThreads) {
+        const size_t i = base + threadIdx.x;
+        const bool in = i < n;   // the same for the four lanes of a group
+        float v[8] = {};
+        if (in) {
+            const size_t r = i / per_row;
+            const int c = static_cast<int>(i - r * per_row) * 8;
+            long long src = static_cast<long long>(r);
+            if (row_of != nullptr) {
+                src = __ldg(row_of + r);
+                if (src >= x_rows) src = -1;
+            }
+            if (src >= 0) {
+                load8<T, kVec>(x + src * ld + c, v);
+                if constexpr (kAct) {
+                    float u[8];
+                    load8<T, kVec>(up + src * ld + c, u);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = swiglu(v[q], u[q], limit);
+                }
+            }
+        }
+        // largest magnitude as bits: a NaN or infinity has exponent 255
+        uint32_t top = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const uint32_t e = top >> 23;
+        const bool bad = e == 255u;
+        const uint32_t k = bad ? 255u : (e > 2u ? e - 2u : 0u);
+        const float inv = __uint_as_float((254u - (bad ? 127u : k)) << 23);   // 2^(127-k)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = bad ? 0.0f : __fmul_rn(v[q], inv);
+        const uint32_t word = f32x8_to_e2m1x8(v);
+        if (!in) continue;
+        codes[i] = word;
+        if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(k);
+        if (values != nullptr) {
+            const float sc = e8m0_to_f32(k);
+            e2m1x8_to_f32(word, v);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], sc);
+            store8<T>(values + i * 8, v);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, long long ld,
+                         const int32_t* row_of, float limit, int rows, uint8_t* out, void* values,
+                         cudaStream_t s) {
+    const size_t n = static_cast<size_t>(rows) * (cols / 8);
+    const size_t blocks = (n + kQThreads - 1) / kQThreads;
+    const unsigned grid = static_cast<unsigned>(blocks < (1u << 30) ? blocks : (1u << 30));
+    auto* codes = reinterpret_cast<uint32_t*>(out);
+    uint8_t* scales = out + static_cast<size_t>(rows) * cols / 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(up) |
+                      (static_cast<uintptr_t>(ld) * sizeof(T))) % 16 == 0;
+    auto go = [&](auto kernel) {
+        kernel<<<grid, kQThreads, 0, s>>>(static_cast<const T*>(x), static_cast<const T*>(up),
+                                          x_rows, cols, ld, row_of, limit, rows, codes, scales,
+                                          static_cast<T*>(values));
+        return cudaGetLastError();
+    };
+    if (up != nullptr) return vec ? go(k_mx_quant<T, true, true>) : go(k_mx_quant<T, true, false>);
+    return vec ? go(k_mx_quant<T, false, true>) : go(k_mx_quant<T, false, false>);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quant(const void* x, const void* up, int type, int x_rows, int cols,
+                            long long ld, const int32_t* row_of, float limit, int rows,
+                            uint8_t* out, void* values, cudaStream_t s) {
+    if (type == kTypeF32)
+        return launch_typed<float>(x, up, x_rows, cols, ld, row_of, limit, rows, out, values, s);
+    if (type == kTypeBF16)
+        return launch_typed<__nv_bfloat16>(x, up, x_rows, cols, ld, row_of, limit, rows, out,
+                                           values, s);
+    return launch_typed<__half>(x, up, x_rows, cols, ld, row_of, limit, rows, out, values, s);
+}
+
+}  // namespace mxk
