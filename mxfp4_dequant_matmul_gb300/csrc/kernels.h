@@ -145,6 +145,7 @@ cudaError_t read_fault_mma(int* value, bool reset);
 cudaError_t read_fault_prefill(int* value, bool reset);
 cudaError_t read_fault_mvtc(int* value, bool reset);
 cudaError_t read_fault_moetc(int* value, bool reset);
+cudaError_t read_fault_mx(int* value, bool reset);
 
 // Records a CUDA error for mxfp4_last_cuda_error() (this thread).
 void record_cuda_error(int err);

@@ -1,12 +1,35 @@
-// mx_mm.cu -- products of two MXFP4 matrices (include/mx4.h mxfp4_mm_mx,
-// mxfp4_moe_mm_mx).
+// mx_mm.cu -- products of two MXFP4 matrices on the block-scaled 4-bit tensor cores
+// (include/mx4.h mxfp4_mm_mx, mxfp4_moe_mm_mx; tcgen05 kind::mxf4, sm_103a).
 //
-// Y[i][r] = sum_g 2^(kw-127) 2^(kx-127) sum_{c in g} e2m1(W[r][c]) e2m1(X[i][c]).
-// A group's 32 products are multiples of 1/4 below 36, so their sum is exact in
-// FP32; both scales are applied in one step, so that neither alone overflows.
+// Y[i][r] = sum_g 2^(kw-127) 2^(kx-127) sum_{c in g} e2m1(W[r][c]) e2m1(X[i][c]): the
+// tensor core multiplies the codes, applies both groups' scale bytes and adds in FP32.
+// The weights are the MMA's 128-row operand A and the tokens its N columns, so one
+// kernel serves one token (N = 16) and a prompt (N up to 208), and a warp's 32 TMEM
+// lanes are 32 consecutive outputs of one token: stores are coalesced without a
+// transpose.
 //
-// One warp per (weight row, 4 rows of X): lanes take groups, a warp tree adds.
+// Code planes arrive by TMA as they lie in memory (128-byte swizzled rows of 256
+// elements: one ring stage, four MMAs of K = 64).  Scale bytes lie row-major with a
+// row stride of cols/32 bytes, which no copy engine can turn into the layout the
+// tensor core wants (32 lanes x 16 bytes: byte 4j + b of lane l is group b of row l +
+// 32j), so two warps load them 8 bytes a row and store them in that layout, and
+// tcgen05.cp moves them to tensor memory ahead of the stage's MMAs.
+//
+// Warp 0 issues the copies, warp 1 the MMAs, warps 2 and 3 the scales of W and X, warps
+// 4..7 read finished accumulators (two, in turn) and store them.  Persistent: CTA c
+// takes tiles c, c + grid, ...  With few tokens the tiles are too few to fill the SMs;
+// then a cluster of CTAs shares a tile, each a slice of K, and adds the partial sums
+// through distributed shared memory in rank order.
+//
+// Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land,
+// frees its tensor memory and returns.
+#include <cooperative_groups.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
 #include <cstdint>
+#include <mutex>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -16,58 +39,571 @@
 namespace mxk {
 namespace {
 
-constexpr int kTok = 4;
+namespace cg = cooperative_groups;
 
-template <typename T>
-__global__ void __launch_bounds__(256)
-    k_mx_mm(const uint8_t* __restrict__ bank, size_t stride, int n_experts, int rows, int cols,
-            const uint8_t* __restrict__ xq, int n_rows, const int32_t* __restrict__ offsets,
-            T* __restrict__ Y) {
-    const int gpr = cols / kGroup;
-    const int lane = threadIdx.x & 31;
-    const uint8_t* xs = xq + static_cast<size_t>(n_rows) * cols / 2;
-    for (int e = blockIdx.y; e < n_experts; e += gridDim.y) {
-        const int b0 = offsets == nullptr ? 0 : min(max(__ldg(offsets + e), 0), n_rows);
-        const int b1 = offsets == nullptr ? n_rows : min(__ldg(offsets + e + 1), n_rows);
-        const uint8_t* w = bank + static_cast<size_t>(e) * stride;
-        const uint8_t* ws = w + static_cast<size_t>(rows) * cols / 2;
-        const int n_tok = (b1 - b0 + kTok - 1) / kTok;
-        const long long units = static_cast<long long>(rows) * max(n_tok, 0);
-        for (long long u = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < units;
-             u += static_cast<long long>(gridDim.x) * 8) {
-            const int r = static_cast<int>(u / n_tok);
-            const int t0 = b0 + static_cast<int>(u % n_tok) * kTok;
-            float acc[kTok] = {};
-            for (int g = lane; g < gpr; g += 32) {
-                const uint4 wc = __ldg(group_codes(w, gpr, r, g));
-                const int kw = static_cast<int>(group_scale_byte(ws, gpr, r, g));
+constexpr int kM = 128;                     // weight rows per tile
+constexpr int kK = 256;                     // elements per ring stage: 128 code bytes a row
+constexpr int kGroupsStage = kK / kGroup;   // 8 scale bytes a row
+constexpr int kThreadsMx = 256;
+constexpr int kEpiWarpMx = 4;               // first epilogue warp
+constexpr uint32_t kABytes = kM * kK / 2;
+constexpr uint32_t kSfChunk = 512;          // scale bytes of 128 rows x 4 groups
+constexpr int kMaxStages = 10;
+constexpr int kMaxTokens = 208;             // two accumulators and the scales in 512 columns
+constexpr uint32_t kWaitMx = 1u << 24;
+
+__device__ int g_fault_mx;
+
+// One launch's shape.  tn: most tokens of a tile (a multiple of 16); box: token rows of
+// one TMA copy (divides the stage's token rows); n_acc accumulators of tn columns.
+struct MxArgs {
+    const uint8_t* w_scales;      // scale plane of expert 0
+    size_t bank_stride;
+    size_t w_plane;               // bytes of a scale plane, padded to 16
+    const uint8_t* x_scales;
+    size_t x_plane;
+    const int32_t* offsets;       // nullptr: one matrix
+    int n_experts, rows, gpr, n_rows;
+    int n_steps;                  // ring stages per tile
+    int tn, box, n_stages, n_acc, sf_blocks;   // sf_blocks: 128-token blocks of a stage's scales
+    uint32_t stage_bytes, tmem_cols;
+    int n_rt, n_tt;               // row tiles; token tiles (one matrix)
+};
+
+struct Tile {
+    int e, r0, t0, t1;
+};
+
+__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                      uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                      uint64_t* bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
+// Shared-memory matrix descriptors: operands K-major with 128-byte swizzle (8-row groups
+// 1024 bytes apart); scale chunks unswizzled 8 x 16-byte core matrices 128 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
+           (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+
+// Instruction descriptor of kind::mxf4: A = B = E2M1 (1), K-major, UE8M0 scales, M = 128,
+// N; sf: which half of a 4-byte scale cell (0 or 2) holds the two groups of this K = 64.
+__device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t sf) {
+    return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (1u << 23) | (1u << 27) | (sf << 29);
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+        "[%6], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+        : "memory");
+}
+
+// 512 bytes of scales -> 4 TMEM columns, the 32 lanes repeated in every lane quarter.
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_mx(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_after_mx() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_before_mx() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+// 16 accumulator columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void sts128_mx(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                          uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+// The 8 scale bytes g0 .. g0 + 7 of rows row0 + lane + 32 j, j < 4, of a plane with gpr
+// bytes a row; bytes past a row's end and rows at or past row_end are 0 (2^-127: their
+// codes are 0 or their results are not stored).  Unaligned rows: three aligned words
+// shifted together, none of them past the padded plane.
+struct Scales {
+    uint32_t lo[4], hi[4];
+};
+__device__ __forceinline__ void load_scales(Scales& s, const uint8_t* plane, size_t plane_bytes,
+                                            int gpr, int g0, int row0, int row_end, int lane) {
+    const bool wide = (gpr & 7) == 0;
+    const int nv = min(kGroupsStage, gpr - g0);
+    const uint32_t mlo = nv >= 4 ? 0xFFFFFFFFu : (1u << (8 * nv)) - 1u;
+    const uint32_t mhi = nv >= 8 ? 0xFFFFFFFFu : nv <= 4 ? 0u : (1u << (8 * (nv - 4))) - 1u;
 #pragma unroll
-                for (int t = 0; t < kTok; ++t) {
-                    const int row = min(t0 + t, b1 - 1);
-                    const uint4 xc = __ldg(group_codes(xq, gpr, row, g));
-                    const int kx = static_cast<int>(group_scale_byte(xs, gpr, row, g));
-                    float d = 0.0f;
+    for (int j = 0; j < 4; ++j) {
+        const int row = row0 + lane + 32 * j;
+        s.lo[j] = s.hi[j] = 0u;
+        if (row >= row_end) continue;
+        const size_t at = static_cast<size_t>(row) * gpr + g0;
+        if (wide) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(plane + at));
+            s.lo[j] = v.x;
+            s.hi[j] = v.y;
+        } else {
+            const size_t a = at & ~static_cast<size_t>(3);
+            const uint32_t sh = 8u * static_cast<uint32_t>(at & 3);
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(plane + a);
+            const uint32_t w0 = __ldg(p);
+            const uint32_t w1 = a + 4 < plane_bytes ? __ldg(p + 1) : 0u;
+            const uint32_t w2 = a + 8 < plane_bytes ? __ldg(p + 2) : 0u;
+            s.lo[j] = __funnelshift_r(w0, w1, sh) & mlo;
+            s.hi[j] = __funnelshift_r(w1, w2, sh) & mhi;
+        }
+    }
+}
+
+// Both chunks (groups 0..3 and 4..7) of 128 rows; chunk 1 is `second` bytes on.
+__device__ __forceinline__ void store_scales(const Scales& s, uint32_t saddr, uint32_t second,
+                                             int lane) {
+    sts128_mx(saddr + lane * 16, s.lo[0], s.lo[1], s.lo[2], s.lo[3]);
+    sts128_mx(saddr + second + lane * 16, s.hi[0], s.hi[1], s.hi[2], s.hi[3]);
+}
+
+template <typename T, bool kSplit>
+__global__ void __launch_bounds__(kThreadsMx, 1)
+    k_mx_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+            const MxArgs a, T* __restrict__ Y) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_word, n_tiles_sh;
+    volatile int* abort_flag = &abort_word;
+    // after the ring: the experts' row offsets and first tiles (experts), or the
+    // partial sums of a split tile
+    uint8_t* after = smem + static_cast<size_t>(a.n_stages) * a.stage_bytes;
+    int32_t* off = reinterpret_cast<int32_t*>(after);
+    int32_t* first = off + a.n_experts + 1;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kSplit ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+    const int n_rank = kSplit ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
+
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&tmem_base)),
+                     "r"(a.tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < a.n_stages; ++i) {
+            mbar_init(&full[i], 3);   // the copies, W's scales, X's scales
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 4);
+        }
+        mbar_init(&drain, 1);
+        abort_word = 0;
+        n_tiles_sh = a.n_rt * a.n_tt;
+        fence_mbar_init();
+    }
+    if (a.offsets != nullptr) {
+        for (int e = tid; e <= a.n_experts; e += kThreadsMx)
+            off[e] = min(max(__ldg(a.offsets + e), 0), a.n_rows);
+        __syncthreads();
+        if (warp == 0) {   // first[e]: tiles of the experts before e
+            int base = 0;
+            for (int e0 = 0; e0 < a.n_experts; e0 += 32) {
+                const int e = e0 + lane;
+                int n = 0;
+                if (e < a.n_experts)
+                    n = a.n_rt * ((max(off[e + 1] - off[e], 0) + a.tn - 1) / a.tn);
+                int sum = n;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float a[8], b[8];
-                        e2m1x8_to_f32(k == 0 ? wc.x : k == 1 ? wc.y : k == 2 ? wc.z : wc.w, a);
-                        e2m1x8_to_f32(k == 0 ? xc.x : k == 1 ? xc.y : k == 2 ? xc.z : xc.w, b);
-#pragma unroll
-                        for (int q = 0; q < 8; ++q) d = fmaf(a[q], b[q], d);
-                    }
-                    acc[t] += kw == 255 || kx == 255 ? __uint_as_float(0x7FC00000u)
-                                                     : ldexpf(d, kw + kx - 254);
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                    if (lane >= d) sum += o;
                 }
+                if (e < a.n_experts) first[e] = base + sum - n;
+                base += __shfl_sync(0xFFFFFFFFu, sum, 31);
             }
-#pragma unroll
-            for (int t = 0; t < kTok; ++t) {
-#pragma unroll
-                for (int m = 16; m > 0; m >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], m);
-                if (lane == 0 && t0 + t < b1)
-                    Y[static_cast<size_t>(t0 + t) * rows + r] = from_f32<T>(acc[t]);
+            if (lane == 0) {
+                first[a.n_experts] = base;
+                n_tiles_sh = base;
             }
         }
     }
+    fence_before_mx();
+    __syncthreads();
+    fence_after_mx();
+    const uint32_t tmem = tmem_base;
+    const int n_tiles = n_tiles_sh;
+    const int s_lo = kSplit ? static_cast<int>(static_cast<long long>(a.n_steps) * rank / n_rank) : 0;
+    const int s_hi =
+        kSplit ? static_cast<int>(static_cast<long long>(a.n_steps) * (rank + 1) / n_rank) : a.n_steps;
+    const int tile0 = kSplit ? static_cast<int>(blockIdx.x) / n_rank : static_cast<int>(blockIdx.x);
+    const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x);   // (split: one tile)
+    const uint32_t sf_cols = tmem + a.n_acc * a.tn;
+    const uint32_t sf_stage = 8u + 8u * a.sf_blocks;
+    const uint32_t sf_off = kABytes + static_cast<uint32_t>(a.tn) * 128u;   // within a stage
+
+    // A tile's token tiles come first, so that the weights of a row tile are read again
+    // from L2; an expert's rows are cut into equal tiles of a multiple of 16.
+    auto tile_at = [&](int tile) {
+        Tile t;
+        if (a.offsets == nullptr) {
+            t.e = 0;
+            const int rt = tile / a.n_tt;
+            t.r0 = rt * kM;
+            t.t0 = (tile - rt * a.n_tt) * a.tn;
+            t.t1 = min(t.t0 + a.tn, a.n_rows);
+        } else {
+            int lo = 0, hi = a.n_experts;   // first[lo] <= tile < first[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= tile) lo = mid;
+                else hi = mid;
+            }
+            t.e = lo;
+            const int n = off[lo + 1] - off[lo];
+            const int n_tt = (n + a.tn - 1) / a.tn;
+            const int per = ((n + n_tt - 1) / n_tt + 15) & ~15;
+            const int local = tile - first[lo], rt = local / n_tt;
+            t.r0 = rt * kM;
+            t.t0 = off[lo] + (local - rt * n_tt) * per;
+            t.t1 = min(t.t0 + per, off[lo + 1]);
+        }
+        return t;
+    };
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(&g_fault_mx, 1);
+    };
+    int issued = 0;   // (warp 0) stages started
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // --- copies
+            const uint64_t keep = l2_evict_last();
+            const uint64_t w_policy = kSplit || a.tn <= 16 ? l2_evict_first() : keep;
+            for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step) {
+                const Tile t = tile_at(tile);
+                const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
+                const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box * a.box) * 128u;
+                for (int s = s_lo; s < s_hi; ++s, ++issued) {
+                    const int st = issued % a.n_stages;
+                    if (issued >= a.n_stages &&
+                        !mbar_wait(&empty[st],
+                                   static_cast<uint32_t>(issued / a.n_stages - 1) & 1u, kWaitMx)) {
+                        fail();
+                        break;
+                    }
+                    const uint32_t dst = smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes);
+                    mbar_arrive_expect_tx(&full[st], bytes);
+                    tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[st], w_policy);
+                    for (int b = 0; b < n_box; ++b)
+                        tma2d(dst + kABytes + static_cast<uint32_t>(b * a.box) * 128u, &xmap,
+                              s * (kK / 2), t.t0 + b * a.box, &full[st], keep);
+                }
+                if (*abort_flag) break;
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // --- MMAs
+            int used = 0, j = 0;
+            for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step, ++j) {
+                const Tile t = tile_at(tile);
+                const int n = (t.t1 - t.t0 + 15) & ~15;
+                const int ab = j % a.n_acc;
+                if (j >= a.n_acc &&
+                    !mbar_wait(&acc_empty[ab], static_cast<uint32_t>(j / a.n_acc - 1) & 1u,
+                               kWaitMx)) {
+                    fail();
+                    break;
+                }
+                fence_after_mx();
+                const uint32_t d = tmem + ab * a.tn;
+                for (int s = s_lo; s < s_hi; ++s, ++used) {
+                    const int st = used % a.n_stages;
+                    if (!mbar_wait(&full[st], static_cast<uint32_t>(used / a.n_stages) & 1u,
+                                   kWaitMx)) {
+                        fail();
+                        break;
+                    }
+                    fence_after_mx();
+                    const uint32_t base = smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes);
+                    const uint32_t sfa = sf_cols + st * sf_stage, sfb = sfa + 8u;
+                    const uint32_t sfs = base + sf_off;
+                    cp_scales(sfa, scale_desc(sfs));
+                    cp_scales(sfa + 4u, scale_desc(sfs + kSfChunk));
+                    for (int c = 0; c < 2; ++c)
+                        for (int b = 0; b < a.sf_blocks; ++b) {
+                            const int q = c * a.sf_blocks + b;
+                            cp_scales(sfb + 4u * q, scale_desc(sfs + (2 + q) * kSfChunk));
+                        }
+                    // K = 64 at a time; the last stage of a row may hold fewer
+                    const int kk_end = min(4, (a.gpr - s * kGroupsStage + 1) / 2);
+                    for (int kk = 0; kk < kk_end; ++kk)
+                        umma_mxf4(d, operand_desc(base + kk * 32),
+                                  operand_desc(base + kABytes + kk * 32),
+                                  idesc_mxf4(n, (kk & 1) * 2u), sfa + 4u * (kk >> 1),
+                                  sfb + 4u * (kk >> 1) * a.sf_blocks,
+                                  (s > s_lo || kk > 0) ? 1u : 0u);
+                    umma_commit_mx(&empty[st]);
+                }
+                if (*abort_flag) break;
+                umma_commit_mx(&acc_full[ab]);
+            }
+            if (*abort_flag) {
+                umma_commit_mx(&drain);
+                mbar_wait(&drain, 0u, kWaitMx);
+            }
+        }
+    } else if (warp < kEpiWarpMx) {
+        // --- scales of W (warp 2) or X (warp 3)
+        const bool is_w = warp == 2;
+        int done = 0;
+        for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step) {
+            const Tile t = tile_at(tile);
+            const uint8_t* plane = is_w ? a.w_scales + static_cast<size_t>(t.e) * a.bank_stride
+                                        : a.x_scales;
+            const size_t plane_bytes = is_w ? a.w_plane : a.x_plane;
+            const int row0 = is_w ? t.r0 : t.t0, row_end = is_w ? a.rows : t.t1;
+            const int blocks = is_w ? 1 : a.sf_blocks;
+            const uint32_t at = sf_off + (is_w ? 0u : 2u * kSfChunk);
+            const uint32_t second = kSfChunk * static_cast<uint32_t>(blocks);
+            Scales cur[2], nxt[2];
+            for (int b = 0; b < 2; ++b)
+                if (b < blocks)
+                    load_scales(cur[b], plane, plane_bytes, a.gpr, s_lo * kGroupsStage,
+                                row0 + 128 * b, row_end, lane);
+            for (int s = s_lo; s < s_hi; ++s, ++done) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (b < blocks && s + 1 < s_hi)
+                        load_scales(nxt[b], plane, plane_bytes, a.gpr, (s + 1) * kGroupsStage,
+                                    row0 + 128 * b, row_end, lane);
+                const int st = done % a.n_stages;
+                if (done >= a.n_stages &&
+                    !__all_sync(0xFFFFFFFFu,
+                                mbar_wait(&empty[st],
+                                          static_cast<uint32_t>(done / a.n_stages - 1) & 1u,
+                                          kWaitMx))) {
+                    fail();
+                    break;
+                }
+                const uint32_t dst =
+                    smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes) + at;
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                    if (b < blocks) store_scales(cur[b], dst + b * kSfChunk, second, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_m(&full[st]);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) cur[b] = nxt[b];
+            }
+            if (*abort_flag) break;
+        }
+    } else {
+        // --- epilogue
+        const int quarter = warp & 3;   // TMEM lanes 32 * quarter .. + 31
+        int j = 0;
+        for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step, ++j) {
+            const Tile t = tile_at(tile);
+            const int ab = j % a.n_acc;
+            if (!__all_sync(0xFFFFFFFFu,
+                            mbar_wait(&acc_full[ab], static_cast<uint32_t>(j / a.n_acc) & 1u,
+                                      kWaitMx))) {
+                fail();
+                break;
+            }
+            fence_after_mx();
+            const int n = t.t1 - t.t0;
+            const int r = t.r0 + quarter * 32 + lane;
+            const uint32_t src =
+                tmem + ab * a.tn + (static_cast<uint32_t>(quarter * 32) << 16);
+            if constexpr (kSplit) {
+                // [token][128 rows] partial sums of this rank
+                float* part = reinterpret_cast<float*>(after);
+                for (int c = 0; c < n; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(src + c, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        part[(c + i) * kM + quarter * 32 + lane] =
+                            s_hi > s_lo ? __uint_as_float(v[i]) : 0.0f;
+                }
+            } else {
+                for (int c = 0; c < n; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(src + c, v);
+                    T* dst = Y + static_cast<size_t>(t.t0 + c) * a.rows + r;
+                    if (r < a.rows) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < n)
+                                dst[static_cast<size_t>(i) * a.rows] =
+                                    from_f32<T>(__uint_as_float(v[i]));
+                    }
+                }
+            }
+            fence_before_mx();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_m(&acc_empty[ab]);
+        }
+    }
+
+    __syncthreads();
+    if constexpr (kSplit) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();   // every rank's partial sums are written
+        const Tile t = tile_at(tile0);
+        float* part = reinterpret_cast<float*>(after);
+        const int n_out = (t.t1 - t.t0) * kM;
+        for (int i = rank * kThreadsMx + tid; i < n_out && !*abort_flag;
+             i += n_rank * kThreadsMx) {
+            const int r = t.r0 + (i & (kM - 1)), tok = t.t0 + i / kM;
+            float sum = 0.0f;
+            for (int q = 0; q < n_rank; ++q) sum += cluster.map_shared_rank(part, q)[i];
+            if (r < a.rows) Y[static_cast<size_t>(tok) * a.rows + r] = from_f32<T>(sum);
+        }
+        cluster.sync();   // no rank leaves while its sums are being read
+    }
+    __syncthreads();
+    if (*abort_flag && tid == 0) {
+        // a CTA that gave up: let the copies it started land before it exits
+        for (int i = issued - a.n_stages; i < issued; ++i)
+            if (i >= 0)
+                mbar_wait(&full[i % a.n_stages], static_cast<uint32_t>(i / a.n_stages) & 1u,
+                          kWaitMx);
+    }
+    fence_before_mx();
+    __syncthreads();
+    if (warp == 1) {
+        fence_after_mx();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(a.tmem_cols)
+                     : "memory");
+    }
+}
+
+// --- host side --------------------------------------------------------------------------
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// Code planes of `experts` matrices [rows][cols/2] bytes, `stride` bytes apart; copies of
+// 128 bytes x box_rows.
+bool code_map(CUtensorMap* map, const void* base, int cols, int rows, int experts, size_t stride,
+              int box_rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols / 2), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(experts)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols / 2),
+                                   static_cast<cuuint64_t>(stride)};
+    const cuuint32_t box[3] = {kK / 2, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, experts > 0 ? 3 : 2, const_cast<void*>(base),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int sm_count() {
+    static PerDevice memo;
+    return memo.get([] {
+        int dev = 0, n = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+            n = 1;
+        return n;
+    });
+}
+
+constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 2048;   // alignment and static arrays
+
+template <typename T, bool kSplit>
+cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxArgs& a, T* Y,
+                     unsigned grid, unsigned cluster, size_t smem, cudaStream_t s) {
+    static PerDevice memo;
+    const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
+        return static_cast<int>(cudaFuncSetAttribute(k_mx_mm<T, kSplit>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(kSmemMax - 1024)));
+    }));
+    if (attr_err != cudaSuccess) return attr_err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreadsMx);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kSplit ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_mx_mm<T, kSplit>, wmap, xmap, a, Y);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+uint32_t tmem_columns(int need) {
+    uint32_t c = 32;
+    while (c < static_cast<uint32_t>(need)) c *= 2;
+    return c;
 }
 
 }  // namespace
@@ -75,16 +611,91 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
                          const uint8_t* xq, int n_rows, const int32_t* offsets, void* Y,
                          int y_type, cudaStream_t s) {
+    const size_t w_codes = static_cast<size_t>(rows) * cols / 2;
+    const size_t x_codes = static_cast<size_t>(n_rows) * cols / 2;
     const size_t stride = padded_nbytes(rows, cols);
-    const dim3 grid(2048, static_cast<unsigned>(n_experts));
-    if (y_type == kTypeF32)
-        k_mx_mm<float><<<grid, 256, 0, s>>>(bank, stride, n_experts, rows, cols, xq, n_rows,
-                                            offsets, static_cast<float*>(Y));
-    else
-        k_mx_mm<__nv_bfloat16><<<grid, 256, 0, s>>>(bank, stride, n_experts, rows, cols, xq,
-                                                    n_rows, offsets,
-                                                    static_cast<__nv_bfloat16*>(Y));
-    return cudaGetLastError();
+    const int sms = sm_count();
+    MxArgs a{};
+    a.w_scales = bank + w_codes;
+    a.bank_stride = stride;
+    a.w_plane = stride - w_codes;
+    a.x_scales = xq + x_codes;
+    a.x_plane = padded_nbytes(n_rows, cols) - x_codes;
+    a.offsets = offsets;
+    a.n_experts = n_experts;
+    a.rows = rows;
+    a.gpr = cols / kGroup;
+    a.n_rows = n_rows;
+    a.n_steps = (cols + kK - 1) / kK;
+    a.n_rt = (rows + kM - 1) / kM;
+    int split = 1, per_sm = 1;
+    if (offsets != nullptr) {
+        const int mean = (n_rows + n_experts - 1) / n_experts;
+        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 80 ? 96
+               : mean <= 112 ? 128 : 192;
+        a.box = a.tn < 32 ? a.tn : 32;
+        a.n_tt = 0;
+    } else {
+        a.tn = std::min((n_rows + 15) / 16 * 16, kMaxTokens);
+        if (n_rows > 64) {
+            // token tiles: the fewest rounds of tiles over the SMs x columns per tile
+            long best = -1;
+            for (int tn = 32; tn <= kMaxTokens; tn += 16) {
+                const long tiles = static_cast<long>(a.n_rt) * ((n_rows + tn - 1) / tn);
+                const long cost = (tiles + sms - 1) / sms * (tn + 32);
+                if (best < 0 || cost <= best) {
+                    best = cost;
+                    a.tn = tn;
+                }
+            }
+        } else {
+            // few tokens: slices of K over a cluster until the SMs are full twice over
+            while (split < 8 && a.n_rt * split * 2 <= 2 * sms && a.n_steps / (split * 2) >= 2)
+                split *= 2;
+            per_sm = std::min(4, (a.n_rt * split + sms - 1) / sms);
+        }
+        a.box = a.tn;
+        a.n_tt = (n_rows + a.tn - 1) / a.tn;
+    }
+    a.sf_blocks = (a.tn + 127) / 128;
+    a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * 128u + 2u * kSfChunk * (1 + a.sf_blocks);
+    a.n_acc = split > 1 ? 1 : 2;
+    const size_t extra = split > 1 ? static_cast<size_t>(a.tn) * kM * 4
+                                   : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0;
+    const size_t budget = kSmemMax / (split > 1 ? per_sm : 1) - kSmemSlack - 1024 - extra;
+    a.n_stages = std::min(kMaxStages, static_cast<int>(budget / a.stage_bytes));
+    if (split > 1) a.n_stages = std::min(a.n_stages, (a.n_steps + split - 1) / split);
+    const int sf_cols = 8 + 8 * a.sf_blocks;
+    a.n_stages = std::min(a.n_stages, (512 / (split > 1 ? per_sm : 1) - a.n_acc * a.tn) / sf_cols);
+    a.tmem_cols = tmem_columns(a.n_acc * a.tn + a.n_stages * sf_cols);
+    if (a.n_stages < 1) return cudaErrorNotSupported;
+    // A CTA that waits for tensor memory must not hold up a cluster: an unsplit CTA takes
+    // its SM's whole shared memory (and all 512 columns), and a split CTA at least 40 KB,
+    // so that the columns of those that fit an SM together never exceed 512 (2.2 columns
+    // per KB at most) and none shares an SM with a kernel that takes them all.
+    const size_t ring = static_cast<size_t>(a.n_stages) * a.stage_bytes + extra + 1024;
+    const size_t smem = split > 1 ? max(ring, static_cast<size_t>(40 * 1024)) : kSmemMax - 1024;
+    CUtensorMap wmap, xmap;
+    if (!code_map(&wmap, bank, cols, rows, n_experts, stride, kM) ||
+        !code_map(&xmap, xq, cols, n_rows, 0, 16, a.box))
+        return cudaErrorNotSupported;
+    const long tiles = static_cast<long>(a.n_rt) * (offsets != nullptr ? 1 : a.n_tt);
+    const unsigned grid = split > 1 ? static_cast<unsigned>(a.n_rt * split)
+                          : offsets != nullptr || tiles > sms ? static_cast<unsigned>(sms)
+                                                              : static_cast<unsigned>(tiles);
+    auto go = [&](auto* y) {
+        using T = std::remove_pointer_t<decltype(y)>;
+        return split > 1 ? launch_k<T, true>(wmap, xmap, a, y, grid, split, smem, s)
+                         : launch_k<T, false>(wmap, xmap, a, y, grid, 1, smem, s);
+    };
+    return y_type == kTypeF32 ? go(static_cast<float*>(Y)) : go(static_cast<__nv_bfloat16*>(Y));
+}
+
+cudaError_t read_fault_mx(int* value, bool reset) {
+    cudaError_t e = cudaMemcpyFromSymbol(value, g_fault_mx, sizeof(int));
+    if (e != cudaSuccess || !reset) return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_fault_mx, &zero, sizeof(int));
 }
 
 }  // namespace mxk
