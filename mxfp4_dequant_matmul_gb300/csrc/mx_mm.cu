@@ -12,7 +12,7 @@
 // elements: one ring stage, four MMAs of K = 64).  Scale bytes lie row-major with a
 // row stride of cols/32 bytes, which no copy engine can turn into the layout the
 // tensor core wants (32 lanes x 16 bytes: byte 4j + b of lane l is group b of row l +
-// 32j), so two warps load them 8 bytes a row and store them in that layout, and
+// 32j), so two warps load them 32 bytes a row and store them in that layout, and
 // tcgen05.cp moves them to tensor memory ahead of the stage's MMAs.
 //
 // Warp 0 issues the copies, warp 1 the MMAs, warps 2 and 3 the scales of W and X, warps
@@ -59,9 +59,7 @@ __device__ int g_fault_mx;
 struct MxArgs {
     const uint8_t* w_scales;      // scale plane of expert 0
     size_t bank_stride;
-    size_t w_plane;               // bytes of a scale plane, padded to 16
     const uint8_t* x_scales;
-    size_t x_plane;
     const int32_t* offsets;       // nullptr: one matrix
     int n_experts, rows, gpr, n_rows;
     int n_steps;                  // ring stages per tile
@@ -141,6 +139,14 @@ __device__ __forceinline__ void fence_before_mx() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // 16 accumulator columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -160,47 +166,58 @@ __device__ __forceinline__ void sts128_mx(uint32_t addr, uint32_t a, uint32_t b,
                  : "memory");
 }
 
-// The 8 scale bytes g0 .. g0 + 7 of rows row0 + lane + 32 j, j < 4, of a plane with gpr
-// bytes a row; bytes past a row's end and rows at or past row_end are 0 (2^-127: their
-// codes are 0 or their results are not stored).  Unaligned rows: three aligned words
-// shifted together, none of them past the padded plane.
+// The scale bytes of kAhead stages (32 groups from g0) of rows row0 + lane + 32 j, j < 4, of
+// a plane with gpr bytes a row; bytes past a row's end and rows at or past row_end are 0
+// (2^-127: their codes are 0 or their results are not stored).  Rows that are not 16-byte
+// aligned: aligned words shifted together, none of them past the row's last byte's word.
+constexpr int kAhead = 4;
 struct Scales {
-    uint32_t lo[4], hi[4];
+    uint32_t w[4][2 * kAhead];
 };
-__device__ __forceinline__ void load_scales(Scales& s, const uint8_t* plane, size_t plane_bytes,
-                                            int gpr, int g0, int row0, int row_end, int lane) {
-    const bool wide = (gpr & 7) == 0;
-    const int nv = min(kGroupsStage, gpr - g0);
-    const uint32_t mlo = nv >= 4 ? 0xFFFFFFFFu : (1u << (8 * nv)) - 1u;
-    const uint32_t mhi = nv >= 8 ? 0xFFFFFFFFu : nv <= 4 ? 0u : (1u << (8 * (nv - 4))) - 1u;
+__device__ __forceinline__ void load_scales(Scales& s, const uint8_t* plane, int gpr, int g0,
+                                            int row0, int row_end, int lane) {
+    constexpr int kWords = 2 * kAhead;
+    const bool wide = ((gpr | g0) & 15) == 0;
+    const int nv = min(4 * kWords, gpr - g0);   // bytes of the row that count
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int row = row0 + lane + 32 * j;
-        s.lo[j] = s.hi[j] = 0u;
-        if (row >= row_end) continue;
         const size_t at = static_cast<size_t>(row) * gpr + g0;
         if (wide) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(plane + at));
-            s.lo[j] = v.x;
-            s.hi[j] = v.y;
+#pragma unroll
+            for (int q = 0; q < kWords / 4; ++q) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (row < row_end && 16 * q < nv)
+                    v = __ldg(reinterpret_cast<const uint4*>(plane + at) + q);
+                s.w[j][4 * q] = v.x;
+                s.w[j][4 * q + 1] = v.y;
+                s.w[j][4 * q + 2] = v.z;
+                s.w[j][4 * q + 3] = v.w;
+            }
         } else {
-            const size_t a = at & ~static_cast<size_t>(3);
-            const uint32_t sh = 8u * static_cast<uint32_t>(at & 3);
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(plane + a);
-            const uint32_t w0 = __ldg(p);
-            const uint32_t w1 = a + 4 < plane_bytes ? __ldg(p + 1) : 0u;
-            const uint32_t w2 = a + 8 < plane_bytes ? __ldg(p + 2) : 0u;
-            s.lo[j] = __funnelshift_r(w0, w1, sh) & mlo;
-            s.hi[j] = __funnelshift_r(w1, w2, sh) & mhi;
+            const int skew = static_cast<int>(at & 3);
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(plane + (at - skew));
+            uint32_t raw[kWords + 1];
+#pragma unroll
+            for (int i = 0; i <= kWords; ++i)
+                raw[i] = row < row_end && 4 * i < nv + skew ? __ldg(p + i) : 0u;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const int left = nv - 4 * i;   // bytes of this word that count
+                const uint32_t keep =
+                    left >= 4 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+                s.w[j][i] = __funnelshift_r(raw[i], raw[i + 1], 8u * skew) & keep;
+            }
         }
     }
 }
 
-// Both chunks (groups 0..3 and 4..7) of 128 rows; chunk 1 is `second` bytes on.
-__device__ __forceinline__ void store_scales(const Scales& s, uint32_t saddr, uint32_t second,
-                                             int lane) {
-    sts128_mx(saddr + lane * 16, s.lo[0], s.lo[1], s.lo[2], s.lo[3]);
-    sts128_mx(saddr + second + lane * 16, s.hi[0], s.hi[1], s.hi[2], s.hi[3]);
+// Both chunks (groups 0..3 and 4..7) of stage q's 128 rows; chunk 1 is `second` bytes on.
+__device__ __forceinline__ void store_scales(const Scales& s, int q, uint32_t saddr,
+                                             uint32_t second, int lane) {
+    sts128_mx(saddr + lane * 16, s.w[0][2 * q], s.w[1][2 * q], s.w[2][2 * q], s.w[3][2 * q]);
+    sts128_mx(saddr + second + lane * 16, s.w[0][2 * q + 1], s.w[1][2 * q + 1],
+              s.w[2][2 * q + 1], s.w[3][2 * q + 1]);
 }
 
 template <typename T, bool kSplit>
@@ -274,11 +291,15 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
     fence_before_mx();
     __syncthreads();
     fence_after_mx();
-    const uint32_t tmem = tmem_base;
-    const int n_tiles = n_tiles_sh;
-    const int s_lo = kSplit ? static_cast<int>(static_cast<long long>(a.n_steps) * rank / n_rank) : 0;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
+    const int n_tiles = __shfl_sync(0xFFFFFFFFu, n_tiles_sh, 0);
+    // (split) slices of whole pairs of stages, so that 16-byte scale loads stay aligned
+    const int pairs = (a.n_steps + 1) / 2;
+    const int s_lo = kSplit ? 2 * static_cast<int>(static_cast<long long>(pairs) * rank / n_rank) : 0;
     const int s_hi =
-        kSplit ? static_cast<int>(static_cast<long long>(a.n_steps) * (rank + 1) / n_rank) : a.n_steps;
+        kSplit ? min(a.n_steps,
+                     2 * static_cast<int>(static_cast<long long>(pairs) * (rank + 1) / n_rank))
+               : a.n_steps;
     const int tile0 = kSplit ? static_cast<int>(blockIdx.x) / n_rank : static_cast<int>(blockIdx.x);
     const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x);   // (split: one tile)
     const uint32_t sf_cols = tmem + a.n_acc * a.tn;
@@ -347,103 +368,128 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // --- MMAs
-            int used = 0, j = 0;
-            for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step, ++j) {
-                const Tile t = tile_at(tile);
-                const int n = (t.t1 - t.t0 + 15) & ~15;
-                const int ab = j % a.n_acc;
-                if (j >= a.n_acc &&
-                    !mbar_wait(&acc_empty[ab], static_cast<uint32_t>(j / a.n_acc - 1) & 1u,
-                               kWaitMx)) {
-                    fail();
-                    break;
-                }
+        // --- MMAs: the whole warp walks the stages, so that descriptors and addresses stay
+        // in uniform registers (computed by one lane alone they cost several hundred cycles
+        // a stage); one elected lane issues
+        const bool leader = elect_one();
+        const uint32_t ring = smem_u32(smem);
+        const uint64_t op0 = operand_desc(ring), sf0 = scale_desc(ring + sf_off);
+        const uint32_t stage16 = a.stage_bytes >> 4;   // descriptors count 16 bytes
+        uint32_t st = 0, phase = 0;
+        int j = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
+            const Tile t = tile_at(tile);
+            const int n = __shfl_sync(0xFFFFFFFFu, (t.t1 - t.t0 + 15) & ~15, 0);
+            const uint32_t id0 = idesc_mxf4(n, 0u), id2 = idesc_mxf4(n, 2u);
+            const int ab = j % a.n_acc;
+            if (j >= a.n_acc)
+                ok = mbar_wait(&acc_empty[ab], static_cast<uint32_t>(j / a.n_acc - 1) & 1u,
+                               kWaitMx);
+            fence_after_mx();
+            const uint32_t d = tmem + ab * a.tn;
+            for (int s = s_lo; s < s_hi && ok; ++s) {
+                ok = mbar_wait(&full[st], phase, kWaitMx);
+                if (!ok) break;
                 fence_after_mx();
-                const uint32_t d = tmem + ab * a.tn;
-                for (int s = s_lo; s < s_hi; ++s, ++used) {
-                    const int st = used % a.n_stages;
-                    if (!mbar_wait(&full[st], static_cast<uint32_t>(used / a.n_stages) & 1u,
-                                   kWaitMx)) {
-                        fail();
-                        break;
+                const uint32_t sfa = sf_cols + st * sf_stage, sfb = sfa + 8u;
+                const uint64_t ad = op0 + st * stage16, bd = ad + (kABytes >> 4);
+                const uint64_t sd = sf0 + st * stage16;
+                const uint32_t more = s > s_lo ? 1u : 0u;
+                // K = 64 at a time; the last stage of a row may hold fewer
+                const int kk_end = (a.gpr - s * kGroupsStage + 1) / 2;
+                if (leader) {
+                    cp_scales(sfa, sd);
+                    cp_scales(sfa + 4u, sd + (kSfChunk >> 4));
+                    cp_scales(sfb, sd + 2 * (kSfChunk >> 4));
+                    cp_scales(sfb + 4u, sd + 3 * (kSfChunk >> 4));
+                    if (a.sf_blocks == 2) {
+                        cp_scales(sfb + 8u, sd + 4 * (kSfChunk >> 4));
+                        cp_scales(sfb + 12u, sd + 5 * (kSfChunk >> 4));
                     }
-                    fence_after_mx();
-                    const uint32_t base = smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes);
-                    const uint32_t sfa = sf_cols + st * sf_stage, sfb = sfa + 8u;
-                    const uint32_t sfs = base + sf_off;
-                    cp_scales(sfa, scale_desc(sfs));
-                    cp_scales(sfa + 4u, scale_desc(sfs + kSfChunk));
-                    for (int c = 0; c < 2; ++c)
-                        for (int b = 0; b < a.sf_blocks; ++b) {
-                            const int q = c * a.sf_blocks + b;
-                            cp_scales(sfb + 4u * q, scale_desc(sfs + (2 + q) * kSfChunk));
-                        }
-                    // K = 64 at a time; the last stage of a row may hold fewer
-                    const int kk_end = min(4, (a.gpr - s * kGroupsStage + 1) / 2);
-                    for (int kk = 0; kk < kk_end; ++kk)
-                        umma_mxf4(d, operand_desc(base + kk * 32),
-                                  operand_desc(base + kABytes + kk * 32),
-                                  idesc_mxf4(n, (kk & 1) * 2u), sfa + 4u * (kk >> 1),
-                                  sfb + 4u * (kk >> 1) * a.sf_blocks,
-                                  (s > s_lo || kk > 0) ? 1u : 0u);
+                    const uint32_t sfb2 = sfb + 4u * a.sf_blocks;
+                    umma_mxf4(d, ad, bd, id0, sfa, sfb, more);
+                    if (kk_end > 1) umma_mxf4(d, ad + 2, bd + 2, id2, sfa, sfb, 1u);
+                    if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
+                    if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
                     umma_commit_mx(&empty[st]);
                 }
-                if (*abort_flag) break;
-                umma_commit_mx(&acc_full[ab]);
+                __syncwarp();
+                if (++st == static_cast<uint32_t>(a.n_stages)) {
+                    st = 0;
+                    phase ^= 1u;
+                }
             }
-            if (*abort_flag) {
-                umma_commit_mx(&drain);
-                mbar_wait(&drain, 0u, kWaitMx);
-            }
+            if (ok && leader) umma_commit_mx(&acc_full[ab]);
+            ok = ok && !*abort_flag;
         }
+        if (!ok) {
+            fail();
+            if (leader) umma_commit_mx(&drain);
+            mbar_wait(&drain, 0u, kWaitMx);
+        }
+        __syncwarp();
     } else if (warp < kEpiWarpMx) {
-        // --- scales of W (warp 2) or X (warp 3)
+        // --- scales of W (warp 2) or X (warp 3), loaded four to eight stages ahead of
+        // their use and across tiles
         const bool is_w = warp == 2;
-        int done = 0;
-        for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step) {
-            const Tile t = tile_at(tile);
-            const uint8_t* plane = is_w ? a.w_scales + static_cast<size_t>(t.e) * a.bank_stride
-                                        : a.x_scales;
-            const size_t plane_bytes = is_w ? a.w_plane : a.x_plane;
-            const int row0 = is_w ? t.r0 : t.t0, row_end = is_w ? a.rows : t.t1;
-            const int blocks = is_w ? 1 : a.sf_blocks;
-            const uint32_t at = sf_off + (is_w ? 0u : 2u * kSfChunk);
-            const uint32_t second = kSfChunk * static_cast<uint32_t>(blocks);
-            Scales cur[2], nxt[2];
+        const int blocks = is_w ? 1 : a.sf_blocks;
+        const uint32_t at = sf_off + (is_w ? 0u : 2u * kSfChunk);
+        const uint32_t second = kSfChunk * static_cast<uint32_t>(blocks);
+        int f_tile = tile0, f_step = s_lo;   // what to load next
+        Tile ft{};
+        if (f_tile < n_tiles) ft = tile_at(f_tile);
+        auto fetch = [&](Scales(&r)[2]) {
+            if (f_tile >= n_tiles) return;
+            const uint8_t* plane =
+                is_w ? a.w_scales + static_cast<size_t>(ft.e) * a.bank_stride : a.x_scales;
+            const int row0 = is_w ? ft.r0 : ft.t0, row_end = is_w ? a.rows : ft.t1;
+#pragma unroll
             for (int b = 0; b < 2; ++b)
                 if (b < blocks)
-                    load_scales(cur[b], plane, plane_bytes, a.gpr, s_lo * kGroupsStage,
-                                row0 + 128 * b, row_end, lane);
-            for (int s = s_lo; s < s_hi; ++s, ++done) {
+                    load_scales(r[b], plane, a.gpr, f_step * kGroupsStage, row0 + 128 * b,
+                                row_end, lane);
+            f_step += kAhead;
+            if (f_step >= s_hi) {
+                f_step = s_lo;
+                f_tile += tile_step;
+                if (f_tile < n_tiles) ft = tile_at(f_tile);
+            }
+        };
+        int done = 0;
+        bool ok = true;
+        Scales cur[2], nxt[2];
+        fetch(cur);
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
+            for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead) {
+                fetch(nxt);
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (b < blocks && s + 1 < s_hi)
-                        load_scales(nxt[b], plane, plane_bytes, a.gpr, (s + 1) * kGroupsStage,
-                                    row0 + 128 * b, row_end, lane);
-                const int st = done % a.n_stages;
-                if (done >= a.n_stages &&
-                    !__all_sync(0xFFFFFFFFu,
-                                mbar_wait(&empty[st],
-                                          static_cast<uint32_t>(done / a.n_stages - 1) & 1u,
-                                          kWaitMx))) {
-                    fail();
-                    break;
+                for (int q = 0; q < kAhead; ++q) {
+                    if (s0 + q >= s_hi || !ok) break;
+                    const int st = done % a.n_stages;
+                    if (done >= a.n_stages)
+                        ok = __all_sync(0xFFFFFFFFu,
+                                        mbar_wait(&empty[st],
+                                                  static_cast<uint32_t>(done / a.n_stages - 1) & 1u,
+                                                  kWaitMx));
+                    if (!ok) break;
+                    const uint32_t dst =
+                        smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes) + at;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        if (b < blocks) store_scales(cur[b], q, dst + b * kSfChunk, second, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_m(&full[st]);
+                    ++done;
                 }
-                const uint32_t dst =
-                    smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes) + at;
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    if (b < blocks) store_scales(cur[b], dst + b * kSfChunk, second, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_m(&full[st]);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) cur[b] = nxt[b];
+                if (*abort_flag) break;
             }
             if (*abort_flag) break;
         }
+        if (!ok) fail();
     } else {
         // --- epilogue
         const int quarter = warp & 3;   // TMEM lanes 32 * quarter .. + 31
@@ -618,9 +664,7 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     MxArgs a{};
     a.w_scales = bank + w_codes;
     a.bank_stride = stride;
-    a.w_plane = stride - w_codes;
     a.x_scales = xq + x_codes;
-    a.x_plane = padded_nbytes(n_rows, cols) - x_codes;
     a.offsets = offsets;
     a.n_experts = n_experts;
     a.rows = rows;
@@ -664,7 +708,7 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
                                    : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0;
     const size_t budget = kSmemMax / (split > 1 ? per_sm : 1) - kSmemSlack - 1024 - extra;
     a.n_stages = std::min(kMaxStages, static_cast<int>(budget / a.stage_bytes));
-    if (split > 1) a.n_stages = std::min(a.n_stages, (a.n_steps + split - 1) / split);
+    if (split > 1) a.n_stages = std::min(a.n_stages, (a.n_steps + 1) / 2 / split * 2 + 2);
     const int sf_cols = 8 + 8 * a.sf_blocks;
     a.n_stages = std::min(a.n_stages, (512 / (split > 1 ? per_sm : 1) - a.n_acc * a.tn) / sf_cols);
     a.tmem_cols = tmem_columns(a.n_acc * a.tn + a.n_stages * sf_cols);
