@@ -50,7 +50,7 @@ constexpr uint32_t kABytes = kM * kK / 2;
 constexpr uint32_t kSfChunk = 512;          // scale bytes of 128 rows x 4 groups
 constexpr int kMaxStages = 10;
 constexpr int kMaxTokens = 208;             // two accumulators and the scales in 512 columns
-constexpr uint32_t kWaitMx = 1u << 24;
+constexpr uint32_t kWaitMx = 1u << 24, kDrainMx = 1u << 14;
 
 __device__ int g_fault_mx;
 
@@ -63,7 +63,7 @@ struct MxArgs {
     const int32_t* offsets;       // nullptr: one matrix
     int n_experts, rows, gpr, n_rows;
     int n_steps;                  // ring stages per tile
-    int tn, box, n_stages, n_acc, sf_blocks;   // sf_blocks: 128-token blocks of a stage's scales
+    int tn, box, n_stages, n_acc;
     uint32_t stage_bytes, tmem_cols;
     int n_rt, n_tt;               // row tiles; token tiles (one matrix)
 };
@@ -166,15 +166,16 @@ __device__ __forceinline__ void sts128_mx(uint32_t addr, uint32_t a, uint32_t b,
                  : "memory");
 }
 
-// The scale bytes of kAhead stages (32 groups from g0) of rows row0 + lane + 32 j, j < 4, of
+// The scale bytes of kAhead stages (8 groups each, from g0) of rows row0 + lane + 32 j, j < 4, of
 // a plane with gpr bytes a row; bytes past a row's end and rows at or past row_end are 0
 // (2^-127: their codes are 0 or their results are not stored).  Rows that are not 16-byte
 // aligned: aligned words shifted together, none of them past the row's last byte's word.
-constexpr int kAhead = 4;
+template <int kAhead>
 struct Scales {
     uint32_t w[4][2 * kAhead];
 };
-__device__ __forceinline__ void load_scales(Scales& s, const uint8_t* plane, int gpr, int g0,
+template <int kAhead>
+__device__ __forceinline__ void load_scales(Scales<kAhead>& s, const uint8_t* plane, int gpr, int g0,
                                             int row0, int row_end, int lane) {
     constexpr int kWords = 2 * kAhead;
     const bool wide = ((gpr | g0) & 15) == 0;
@@ -213,15 +214,18 @@ __device__ __forceinline__ void load_scales(Scales& s, const uint8_t* plane, int
 }
 
 // Both chunks (groups 0..3 and 4..7) of stage q's 128 rows; chunk 1 is `second` bytes on.
-__device__ __forceinline__ void store_scales(const Scales& s, int q, uint32_t saddr,
+template <int kAhead>
+__device__ __forceinline__ void store_scales(const Scales<kAhead>& s, int q, uint32_t saddr,
                                              uint32_t second, int lane) {
     sts128_mx(saddr + lane * 16, s.w[0][2 * q], s.w[1][2 * q], s.w[2][2 * q], s.w[3][2 * q]);
     sts128_mx(saddr + second + lane * 16, s.w[0][2 * q + 1], s.w[1][2 * q + 1],
               s.w[2][2 * q + 1], s.w[3][2 * q + 1]);
 }
 
-template <typename T, bool kSplit>
-__global__ void __launch_bounds__(kThreadsMx, 1)
+// NB: 128-token blocks of a stage's scales.  Split tiles (few tokens) leave registers for
+// two CTAs on an SM.
+template <typename T, bool kSplit, int NB>
+__global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
     k_mx_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
             const MxArgs a, T* __restrict__ Y) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -303,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
     const int tile0 = kSplit ? static_cast<int>(blockIdx.x) / n_rank : static_cast<int>(blockIdx.x);
     const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x);   // (split: one tile)
     const uint32_t sf_cols = tmem + a.n_acc * a.tn;
-    const uint32_t sf_stage = 8u + 8u * a.sf_blocks;
+    constexpr uint32_t sf_stage = 8u + 8u * NB;   // TMEM columns of a stage's scales
     const uint32_t sf_off = kABytes + static_cast<uint32_t>(a.tn) * 128u;   // within a stage
 
     // A tile's token tiles come first, so that the weights of a row tile are read again
@@ -345,27 +349,32 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
             // --- copies
             const uint64_t keep = l2_evict_last();
             const uint64_t w_policy = kSplit || a.tn <= 16 ? l2_evict_first() : keep;
-            for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step) {
+            const uint32_t ring = smem_u32(smem);
+            int st = 0;
+            uint32_t phase = 1;   // of the empty barriers: the first round passes at once
+            bool ok = true;
+            for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
                 const Tile t = tile_at(tile);
                 const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
-                const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box * a.box) * 128u;
+                const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
+                const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box) * box_bytes;
                 for (int s = s_lo; s < s_hi; ++s, ++issued) {
-                    const int st = issued % a.n_stages;
-                    if (issued >= a.n_stages &&
-                        !mbar_wait(&empty[st],
-                                   static_cast<uint32_t>(issued / a.n_stages - 1) & 1u, kWaitMx)) {
-                        fail();
-                        break;
-                    }
-                    const uint32_t dst = smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes);
+                    ok = mbar_wait(&empty[st], phase, kWaitMx);
+                    if (!ok) break;
+                    const uint32_t dst = ring + static_cast<uint32_t>(st) * a.stage_bytes;
                     mbar_arrive_expect_tx(&full[st], bytes);
                     tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[st], w_policy);
                     for (int b = 0; b < n_box; ++b)
-                        tma2d(dst + kABytes + static_cast<uint32_t>(b * a.box) * 128u, &xmap,
+                        tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
                               s * (kK / 2), t.t0 + b * a.box, &full[st], keep);
+                    if (++st == a.n_stages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
                 }
-                if (*abort_flag) break;
+                ok = ok && !*abort_flag;
             }
+            if (!ok) fail();
         }
     } else if (warp == 1) {
         // --- MMAs: the whole warp walks the stages, so that descriptors and addresses stay
@@ -403,11 +412,11 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
                     cp_scales(sfa + 4u, sd + (kSfChunk >> 4));
                     cp_scales(sfb, sd + 2 * (kSfChunk >> 4));
                     cp_scales(sfb + 4u, sd + 3 * (kSfChunk >> 4));
-                    if (a.sf_blocks == 2) {
+                    if (NB == 2) {
                         cp_scales(sfb + 8u, sd + 4 * (kSfChunk >> 4));
                         cp_scales(sfb + 12u, sd + 5 * (kSfChunk >> 4));
                     }
-                    const uint32_t sfb2 = sfb + 4u * a.sf_blocks;
+                    const uint32_t sfb2 = sfb + 4u * NB;
                     umma_mxf4(d, ad, bd, id0, sfa, sfb, more);
                     if (kk_end > 1) umma_mxf4(d, ad + 2, bd + 2, id2, sfa, sfb, 1u);
                     if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
@@ -433,19 +442,20 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
         // --- scales of W (warp 2) or X (warp 3), loaded four to eight stages ahead of
         // their use and across tiles
         const bool is_w = warp == 2;
-        const int blocks = is_w ? 1 : a.sf_blocks;
-        const uint32_t at = sf_off + (is_w ? 0u : 2u * kSfChunk);
+        const int blocks = is_w ? 1 : NB;
         const uint32_t second = kSfChunk * static_cast<uint32_t>(blocks);
+        const uint32_t ring = smem_u32(smem) + sf_off + (is_w ? 0u : 2u * kSfChunk);
+        constexpr int kAhead = kSplit ? 2 : 4;
         int f_tile = tile0, f_step = s_lo;   // what to load next
         Tile ft{};
         if (f_tile < n_tiles) ft = tile_at(f_tile);
-        auto fetch = [&](Scales(&r)[2]) {
+        auto fetch = [&](Scales<kAhead>(&r)[NB]) {
             if (f_tile >= n_tiles) return;
             const uint8_t* plane =
                 is_w ? a.w_scales + static_cast<size_t>(ft.e) * a.bank_stride : a.x_scales;
             const int row0 = is_w ? ft.r0 : ft.t0, row_end = is_w ? a.rows : ft.t1;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < NB; ++b)
                 if (b < blocks)
                     load_scales(r[b], plane, a.gpr, f_step * kGroupsStage, row0 + 128 * b,
                                 row_end, lane);
@@ -456,38 +466,35 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
                 if (f_tile < n_tiles) ft = tile_at(f_tile);
             }
         };
-        int done = 0;
+        int st = 0;
+        uint32_t phase = 1;
         bool ok = true;
-        Scales cur[2], nxt[2];
+        Scales<kAhead> cur[NB], nxt[NB];
         fetch(cur);
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead) {
                 fetch(nxt);
 #pragma unroll
                 for (int q = 0; q < kAhead; ++q) {
-                    if (s0 + q >= s_hi || !ok) break;
-                    const int st = done % a.n_stages;
-                    if (done >= a.n_stages)
-                        ok = __all_sync(0xFFFFFFFFu,
-                                        mbar_wait(&empty[st],
-                                                  static_cast<uint32_t>(done / a.n_stages - 1) & 1u,
-                                                  kWaitMx));
+                    if (s0 + q >= s_hi) break;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase, kWaitMx));
                     if (!ok) break;
-                    const uint32_t dst =
-                        smem_u32(smem + static_cast<size_t>(st) * a.stage_bytes) + at;
+                    const uint32_t dst = ring + static_cast<uint32_t>(st) * a.stage_bytes;
 #pragma unroll
-                    for (int b = 0; b < 2; ++b)
+                    for (int b = 0; b < NB; ++b)
                         if (b < blocks) store_scales(cur[b], q, dst + b * kSfChunk, second, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_m(&full[st]);
-                    ++done;
+                    if (++st == a.n_stages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
                 }
 #pragma unroll
-                for (int b = 0; b < 2; ++b) cur[b] = nxt[b];
-                if (*abort_flag) break;
+                for (int b = 0; b < NB; ++b) cur[b] = nxt[b];
             }
-            if (*abort_flag) break;
+            ok = ok && !*abort_flag;
         }
         if (!ok) fail();
     } else {
@@ -561,7 +568,7 @@ __global__ void __launch_bounds__(kThreadsMx, 1)
         for (int i = issued - a.n_stages; i < issued; ++i)
             if (i >= 0)
                 mbar_wait(&full[i % a.n_stages], static_cast<uint32_t>(i / a.n_stages) & 1u,
-                          kWaitMx);
+                          kDrainMx);   // (its scales may never arrive)
     }
     fence_before_mx();
     __syncthreads();
@@ -620,12 +627,12 @@ int sm_count() {
 
 constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 2048;   // alignment and static arrays
 
-template <typename T, bool kSplit>
+template <typename T, bool kSplit, int NB>
 cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxArgs& a, T* Y,
                      unsigned grid, unsigned cluster, size_t smem, cudaStream_t s) {
     static PerDevice memo;
     const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
-        return static_cast<int>(cudaFuncSetAttribute(k_mx_mm<T, kSplit>,
+        return static_cast<int>(cudaFuncSetAttribute(k_mx_mm<T, kSplit, NB>,
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      static_cast<int>(kSmemMax - 1024)));
     }));
@@ -642,7 +649,7 @@ cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxA
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kSplit ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_mx_mm<T, kSplit>, wmap, xmap, a, Y);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_mx_mm<T, kSplit, NB>, wmap, xmap, a, Y);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -701,15 +708,15 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
         a.box = a.tn;
         a.n_tt = (n_rows + a.tn - 1) / a.tn;
     }
-    a.sf_blocks = (a.tn + 127) / 128;
-    a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * 128u + 2u * kSfChunk * (1 + a.sf_blocks);
+    const int sf_blocks = (a.tn + 127) / 128;
+    a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * 128u + 2u * kSfChunk * (1 + sf_blocks);
     a.n_acc = split > 1 ? 1 : 2;
     const size_t extra = split > 1 ? static_cast<size_t>(a.tn) * kM * 4
                                    : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0;
     const size_t budget = kSmemMax / (split > 1 ? per_sm : 1) - kSmemSlack - 1024 - extra;
     a.n_stages = std::min(kMaxStages, static_cast<int>(budget / a.stage_bytes));
     if (split > 1) a.n_stages = std::min(a.n_stages, (a.n_steps + 1) / 2 / split * 2 + 2);
-    const int sf_cols = 8 + 8 * a.sf_blocks;
+    const int sf_cols = 8 + 8 * sf_blocks;
     a.n_stages = std::min(a.n_stages, (512 / (split > 1 ? per_sm : 1) - a.n_acc * a.tn) / sf_cols);
     a.tmem_cols = tmem_columns(a.n_acc * a.tn + a.n_stages * sf_cols);
     if (a.n_stages < 1) return cudaErrorNotSupported;
@@ -729,8 +736,9 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
                                                               : static_cast<unsigned>(tiles);
     auto go = [&](auto* y) {
         using T = std::remove_pointer_t<decltype(y)>;
-        return split > 1 ? launch_k<T, true>(wmap, xmap, a, y, grid, split, smem, s)
-                         : launch_k<T, false>(wmap, xmap, a, y, grid, 1, smem, s);
+        if (split > 1) return launch_k<T, true, 1>(wmap, xmap, a, y, grid, split, smem, s);
+        return sf_blocks == 1 ? launch_k<T, false, 1>(wmap, xmap, a, y, grid, 1, smem, s)
+                              : launch_k<T, false, 2>(wmap, xmap, a, y, grid, 1, smem, s);
     };
     return y_type == kTypeF32 ? go(static_cast<float*>(Y)) : go(static_cast<__nv_bfloat16*>(Y));
 }
