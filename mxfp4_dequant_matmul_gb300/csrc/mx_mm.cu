@@ -50,7 +50,7 @@ constexpr uint32_t kABytes = kM * kK / 2;
 constexpr uint32_t kSfChunk = 512;          // scale bytes of 128 rows x 4 groups
 constexpr int kMaxStages = 10;
 constexpr int kMaxTokens = 208;             // two accumulators and the scales in 512 columns
-constexpr uint32_t kWaitMx = 1u << 24, kDrainMx = 1u << 14;
+constexpr long long kWaitMx = 1ll << 32, kDrainMx = 1ll << 24;   // SM cycles: about 2 s and 8 ms
 
 __device__ int g_fault_mx;
 
@@ -65,6 +65,8 @@ struct MxArgs {
     int n_steps;                  // ring stages per tile
     int tn, box, n_stages, n_acc;
     uint32_t stage_bytes, tmem_cols;
+    int n_sc;                     // 2 tile buffers of scale rows, or 0: loaded from global memory
+    uint32_t sc_w, sc_bytes;      // bytes of W's rows in a buffer, of a buffer
     int n_rt, n_tt;               // row tiles; token tiles (one matrix)
 };
 
@@ -147,6 +149,17 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// Wait for the phase with the given parity, for at most `cycles` SM cycles (a poll may
+// itself be suspended for a while, so polls are not counted).
+__device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, long long cycles) {
+    if (mbar_wait(bar, parity, 1)) return true;
+    const long long t0 = clock64();
+    do {
+        if (mbar_wait(bar, parity, 1)) return true;
+    } while (clock64() - t0 < cycles);
+    return false;
+}
+
 // 16 accumulator columns of this warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -174,34 +187,41 @@ template <int kAhead>
 struct Scales {
     uint32_t w[4][2 * kAhead];
 };
-template <int kAhead>
-__device__ __forceinline__ void load_scales(Scales<kAhead>& s, const uint8_t* plane, int gpr, int g0,
-                                            int row0, int row_end, int lane) {
+// kShared: the rows lie in shared memory (bulk-copied, row 0 at `plane`).
+template <bool kShared, typename V>
+__device__ __forceinline__ V load_word(const V* p) {
+    if constexpr (kShared) return *p;
+    else return __ldg(p);
+}
+template <bool kShared, int kAhead>
+__device__ __forceinline__ void load_scales(Scales<kAhead>& s, const uint8_t* plane, int gpr,
+                                            int g0, int row0, int row_end, int lane) {
     constexpr int kWords = 2 * kAhead;
-    const bool wide = ((gpr | g0) & 15) == 0;
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(plane));
+    const bool wide = ((gpr | g0 | base) & 15) == 0;
     const int nv = min(4 * kWords, gpr - g0);   // bytes of the row that count
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int row = row0 + lane + 32 * j;
-        const size_t at = static_cast<size_t>(row) * gpr + g0;
+        const uint8_t* at = plane + static_cast<size_t>(row) * gpr + g0;
         if (wide) {
 #pragma unroll
             for (int q = 0; q < kWords / 4; ++q) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
                 if (row < row_end && 16 * q < nv)
-                    v = __ldg(reinterpret_cast<const uint4*>(plane + at) + q);
+                    v = load_word<kShared>(reinterpret_cast<const uint4*>(at) + q);
                 s.w[j][4 * q] = v.x;
                 s.w[j][4 * q + 1] = v.y;
                 s.w[j][4 * q + 2] = v.z;
                 s.w[j][4 * q + 3] = v.w;
             }
         } else {
-            const int skew = static_cast<int>(at & 3);
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(plane + (at - skew));
+            const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 3);
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(at - skew);
             uint32_t raw[kWords + 1];
 #pragma unroll
             for (int i = 0; i <= kWords; ++i)
-                raw[i] = row < row_end && 4 * i < nv + skew ? __ldg(p + i) : 0u;
+                raw[i] = row < row_end && 4 * i < nv + skew ? load_word<kShared>(p + i) : 0u;
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
                 const int left = nv - 4 * i;   // bytes of this word that count
@@ -232,12 +252,14 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t sc_full[2], sc_empty[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word, n_tiles_sh;
     volatile int* abort_flag = &abort_word;
-    // after the ring: the experts' row offsets and first tiles (experts), or the
-    // partial sums of a split tile
-    uint8_t* after = smem + static_cast<size_t>(a.n_stages) * a.stage_bytes;
+    // after the ring: the buffers of scale rows, then the experts' row offsets and first
+    // tiles (experts) or the partial sums of a split tile
+    uint8_t* sc_buf = smem + static_cast<size_t>(a.n_stages) * a.stage_bytes;
+    uint8_t* after = sc_buf + static_cast<size_t>(a.n_sc) * a.sc_bytes;
     int32_t* off = reinterpret_cast<int32_t*>(after);
     int32_t* first = off + a.n_experts + 1;
 
@@ -260,6 +282,8 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 4);
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_empty[i], 2);
         }
         mbar_init(&drain, 1);
         abort_word = 0;
@@ -342,7 +366,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         *abort_flag = 1;
         atomicOr(&g_fault_mx, 1);
     };
-    int issued = 0;   // (warp 0) stages started
+    int issued = 0, sc_issued = 0;   // (warp 0) stages and scale buffers started
 
     if (warp == 0) {
         if (lane == 0) {
@@ -353,13 +377,37 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
             int st = 0;
             uint32_t phase = 1;   // of the empty barriers: the first round passes at once
             bool ok = true;
+            // a tile's scale rows, contiguous in both planes, one tile ahead of its codes
+            auto copy_scales = [&](const Tile& t) {
+                const int b = sc_issued % 2;
+                if (!mbar_wait_for(&sc_empty[b], (static_cast<uint32_t>(sc_issued / 2) & 1u) ^ 1u,
+                               kWaitMx))
+                    return false;
+                ++sc_issued;
+                uint8_t* dst = sc_buf + static_cast<size_t>(b) * a.sc_bytes;
+                const size_t w_at = static_cast<size_t>(t.r0) * a.gpr;   // a multiple of 16
+                const size_t x_at = static_cast<size_t>(t.t0) * a.gpr;
+                const uint32_t skew = static_cast<uint32_t>(x_at) & 15u;
+                const uint32_t wb =
+                    (static_cast<uint32_t>(min(kM, a.rows - t.r0) * a.gpr) + 15u) & ~15u;
+                const uint32_t xb = (skew + static_cast<uint32_t>((t.t1 - t.t0) * a.gpr) + 15u) & ~15u;
+                mbar_arrive_expect_tx(&sc_full[b], wb + xb);
+                bulk_g2s(dst, a.w_scales + static_cast<size_t>(t.e) * a.bank_stride + w_at, wb,
+                         &sc_full[b], w_policy);
+                bulk_g2s(dst + a.sc_w, a.x_scales + (x_at - skew), xb, &sc_full[b], keep);
+                return true;
+            };
+            if (a.n_sc > 0 && tile0 < n_tiles) ok = copy_scales(tile_at(tile0));
             for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
                 const Tile t = tile_at(tile);
+                if (a.n_sc > 0 && tile + tile_step < n_tiles)
+                    ok = copy_scales(tile_at(tile + tile_step));
+                if (!ok) break;
                 const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
                 const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
                 const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box) * box_bytes;
                 for (int s = s_lo; s < s_hi; ++s, ++issued) {
-                    ok = mbar_wait(&empty[st], phase, kWaitMx);
+                    ok = mbar_wait_for(&empty[st], phase, kWaitMx);
                     if (!ok) break;
                     const uint32_t dst = ring + static_cast<uint32_t>(st) * a.stage_bytes;
                     mbar_arrive_expect_tx(&full[st], bytes);
@@ -393,12 +441,12 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
             const uint32_t id0 = idesc_mxf4(n, 0u), id2 = idesc_mxf4(n, 2u);
             const int ab = j % a.n_acc;
             if (j >= a.n_acc)
-                ok = mbar_wait(&acc_empty[ab], static_cast<uint32_t>(j / a.n_acc - 1) & 1u,
+                ok = mbar_wait_for(&acc_empty[ab], static_cast<uint32_t>(j / a.n_acc - 1) & 1u,
                                kWaitMx);
             fence_after_mx();
             const uint32_t d = tmem + ab * a.tn;
             for (int s = s_lo; s < s_hi && ok; ++s) {
-                ok = mbar_wait(&full[st], phase, kWaitMx);
+                ok = mbar_wait_for(&full[st], phase, kWaitMx);
                 if (!ok) break;
                 fence_after_mx();
                 const uint32_t sfa = sf_cols + st * sf_stage, sfb = sfa + 8u;
@@ -435,7 +483,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         if (!ok) {
             fail();
             if (leader) umma_commit_mx(&drain);
-            mbar_wait(&drain, 0u, kWaitMx);
+            mbar_wait_for(&drain, 0u, kWaitMx);
         }
         __syncwarp();
     } else if (warp < kEpiWarpMx) {
@@ -449,26 +497,48 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         int f_tile = tile0, f_step = s_lo;   // what to load next
         Tile ft{};
         if (f_tile < n_tiles) ft = tile_at(f_tile);
+        int st = 0, f_count = 0;
+        uint32_t phase = 1;
+        bool ok = true;
         auto fetch = [&](Scales<kAhead>(&r)[NB]) {
-            if (f_tile >= n_tiles) return;
-            const uint8_t* plane =
-                is_w ? a.w_scales + static_cast<size_t>(ft.e) * a.bank_stride : a.x_scales;
+            if (f_tile >= n_tiles || !ok) return;
             const int row0 = is_w ? ft.r0 : ft.t0, row_end = is_w ? a.rows : ft.t1;
+            if (!kSplit && a.n_sc > 0) {
+                const int buf = f_count % 2;
+                if (f_step == 0)
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    mbar_wait_for(&sc_full[buf],
+                                              static_cast<uint32_t>(f_count / 2) & 1u, kWaitMx));
+                if (!ok) return;
+                const uint8_t* rows = sc_buf + static_cast<size_t>(buf) * a.sc_bytes;
+                if (!is_w)
+                    rows += a.sc_w + (static_cast<uint32_t>(static_cast<size_t>(ft.t0) * a.gpr) & 15u);
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-                if (b < blocks)
-                    load_scales(r[b], plane, a.gpr, f_step * kGroupsStage, row0 + 128 * b,
-                                row_end, lane);
+                for (int b = 0; b < NB; ++b)
+                    if (b < blocks)
+                        load_scales<true>(r[b], rows, a.gpr, f_step * kGroupsStage, 128 * b,
+                                          row_end - row0, lane);
+            } else {
+                const uint8_t* plane =
+                    is_w ? a.w_scales + static_cast<size_t>(ft.e) * a.bank_stride : a.x_scales;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                    if (b < blocks)
+                        load_scales<false>(r[b], plane, a.gpr, f_step * kGroupsStage,
+                                           row0 + 128 * b, row_end, lane);
+            }
             f_step += kAhead;
             if (f_step >= s_hi) {
+                if (!kSplit && a.n_sc > 0) {   // the tile's rows are in registers
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_m(&sc_empty[f_count % 2]);
+                    ++f_count;
+                }
                 f_step = s_lo;
                 f_tile += tile_step;
                 if (f_tile < n_tiles) ft = tile_at(f_tile);
             }
         };
-        int st = 0;
-        uint32_t phase = 1;
-        bool ok = true;
         Scales<kAhead> cur[NB], nxt[NB];
         fetch(cur);
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
@@ -477,7 +547,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
 #pragma unroll
                 for (int q = 0; q < kAhead; ++q) {
                     if (s0 + q >= s_hi) break;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(&empty[st], phase, kWaitMx));
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&empty[st], phase, kWaitMx));
                     if (!ok) break;
                     const uint32_t dst = ring + static_cast<uint32_t>(st) * a.stage_bytes;
 #pragma unroll
@@ -505,7 +575,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
             const Tile t = tile_at(tile);
             const int ab = j % a.n_acc;
             if (!__all_sync(0xFFFFFFFFu,
-                            mbar_wait(&acc_full[ab], static_cast<uint32_t>(j / a.n_acc) & 1u,
+                            mbar_wait_for(&acc_full[ab], static_cast<uint32_t>(j / a.n_acc) & 1u,
                                       kWaitMx))) {
                 fail();
                 break;
@@ -567,8 +637,11 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         // a CTA that gave up: let the copies it started land before it exits
         for (int i = issued - a.n_stages; i < issued; ++i)
             if (i >= 0)
-                mbar_wait(&full[i % a.n_stages], static_cast<uint32_t>(i / a.n_stages) & 1u,
+                mbar_wait_for(&full[i % a.n_stages], static_cast<uint32_t>(i / a.n_stages) & 1u,
                           kDrainMx);   // (its scales may never arrive)
+        for (int i = sc_issued - 2; i < sc_issued; ++i)
+            if (i >= 0)
+                mbar_wait_for(&sc_full[i % 2], static_cast<uint32_t>(i / 2) & 1u, kDrainMx);
     }
     fence_before_mx();
     __syncthreads();
@@ -713,7 +786,13 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     a.n_acc = split > 1 ? 1 : 2;
     const size_t extra = split > 1 ? static_cast<size_t>(a.tn) * kM * 4
                                    : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0;
-    const size_t budget = kSmemMax / (split > 1 ? per_sm : 1) - kSmemSlack - 1024 - extra;
+    // Whole scale rows of a tile by bulk copies, two tiles deep, where rows of a tile are short
+    // enough; else (long rows, slices of a split tile) loads a few stages ahead.
+    a.sc_w = static_cast<uint32_t>(kM * a.gpr + 15) & ~15u;
+    a.sc_bytes = a.sc_w + (static_cast<uint32_t>(a.tn * a.gpr + 31 + 15) & ~15u);
+    a.n_sc = split == 1 && a.sc_bytes <= 32 * 1024 ? 2 : 0;
+    const size_t budget = kSmemMax / (split > 1 ? per_sm : 1) - kSmemSlack - 1024 - extra -
+                          static_cast<size_t>(a.n_sc) * a.sc_bytes;
     a.n_stages = std::min(kMaxStages, static_cast<int>(budget / a.stage_bytes));
     if (split > 1) a.n_stages = std::min(a.n_stages, (a.n_steps + 1) / 2 / split * 2 + 2);
     const int sf_cols = 8 + 8 * sf_blocks;
@@ -724,7 +803,8 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     // its SM's whole shared memory (and all 512 columns), and a split CTA at least 40 KB,
     // so that the columns of those that fit an SM together never exceed 512 (2.2 columns
     // per KB at most) and none shares an SM with a kernel that takes them all.
-    const size_t ring = static_cast<size_t>(a.n_stages) * a.stage_bytes + extra + 1024;
+    const size_t ring = static_cast<size_t>(a.n_stages) * a.stage_bytes +
+                        static_cast<size_t>(a.n_sc) * a.sc_bytes + extra + 1024;
     const size_t smem = split > 1 ? max(ring, static_cast<size_t>(40 * 1024)) : kSmemMax - 1024;
     CUtensorMap wmap, xmap;
     if (!code_map(&wmap, bank, cols, rows, n_experts, stride, kM) ||
