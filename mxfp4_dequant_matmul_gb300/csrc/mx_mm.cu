@@ -12,8 +12,10 @@
 // elements: one ring stage, four MMAs of K = 64).  Scale bytes lie row-major with a
 // row stride of cols/32 bytes, which no copy engine can turn into the layout the
 // tensor core wants (32 lanes x 16 bytes: byte 4j + b of lane l is group b of row l +
-// 32j), so two warps load them 32 bytes a row and store them in that layout, and
-// tcgen05.cp moves them to tensor memory ahead of the stage's MMAs.
+// 32j), so two warps take them 32 bytes a row (four stages) and store them in that layout,
+// and tcgen05.cp moves them to tensor memory ahead of each stage's MMAs.  A slot of four
+// stages is handed over at a time: the proxy fence and the barriers cost several hundred
+// cycles, more than a stage has when few tokens stream through.
 //
 // Warp 0 issues the copies, warp 1 the MMAs, warps 2 and 3 the scales of W and X, warps
 // 4..7 read finished accumulators (two, in turn) and store them.  Persistent: CTA c
@@ -49,6 +51,7 @@ constexpr int kEpiWarpMx = 4;               // first epilogue warp
 constexpr uint32_t kABytes = kM * kK / 2;
 constexpr uint32_t kSfChunk = 512;          // scale bytes of 128 rows x 4 groups
 constexpr int kMaxStages = 10;
+constexpr int kTileTable = 64;              // this CTA's first tiles, worked out at the start
 constexpr int kMaxTokens = 208;             // two accumulators and the scales in 512 columns
 constexpr long long kWaitMx = 1ll << 32, kDrainMx = 1ll << 24;   // SM cycles: about 2 s and 8 ms
 
@@ -70,7 +73,7 @@ struct MxArgs {
     int n_rt, n_tt;               // row tiles; token tiles (one matrix)
 };
 
-struct Tile {
+struct alignas(16) Tile {
     int e, r0, t0, t1;
 };
 
@@ -180,9 +183,10 @@ __device__ __forceinline__ void sts128_mx(uint32_t addr, uint32_t a, uint32_t b,
 }
 
 // The scale bytes of kAhead stages (8 groups each, from g0) of rows row0 + lane + 32 j, j < 4, of
-// a plane with gpr bytes a row; bytes past a row's end and rows at or past row_end are 0
-// (2^-127: their codes are 0 or their results are not stored).  Rows that are not 16-byte
-// aligned: aligned words shifted together, none of them past the row's last byte's word.
+// a plane with gpr bytes a row; bytes past a row's end are 0 (2^-127: their codes are 0),
+// rows at or past row_end arbitrary (their results are not stored).  Rows that are not
+// 16-byte aligned: aligned words shifted together, none of them past the row's last byte's
+// word.
 template <int kAhead>
 struct Scales {
     uint32_t w[4][2 * kAhead];
@@ -199,29 +203,54 @@ __device__ __forceinline__ void load_scales(Scales<kAhead>& s, const uint8_t* pl
     constexpr int kWords = 2 * kAhead;
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(plane));
     const bool wide = ((gpr | g0 | base) & 15) == 0;
-    const int nv = min(4 * kWords, gpr - g0);   // bytes of the row that count
+    const int nv = gpr - g0;   // bytes of the row from g0 on
+    const uint8_t* at = plane + static_cast<size_t>(row0 + lane) * gpr + g0;
+    const size_t next = static_cast<size_t>(32) * gpr;
+    if (wide) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = row0 + lane + 32 * j;
-        const uint8_t* at = plane + static_cast<size_t>(row) * gpr + g0;
-        if (wide) {
+        for (int j = 0; j < 4; ++j, at += next) {
 #pragma unroll
             for (int q = 0; q < kWords / 4; ++q) {
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (row < row_end && 16 * q < nv)
+                if (row0 + lane + 32 * j < row_end && 16 * q < nv)
                     v = load_word<kShared>(reinterpret_cast<const uint4*>(at) + q);
                 s.w[j][4 * q] = v.x;
                 s.w[j][4 * q + 1] = v.y;
                 s.w[j][4 * q + 2] = v.z;
                 s.w[j][4 * q + 3] = v.w;
             }
-        } else {
+        }
+    } else if (nv >= 4 * kWords + 4) {   // all words count, and the one a shift draws in
+#pragma unroll
+        for (int j = 0; j < 4; ++j, at += next) {
+            if (row0 + 32 * j >= row_end) {   // the same for the whole warp
+#pragma unroll
+                for (int i = 0; i < kWords; ++i) s.w[j][i] = 0u;
+                continue;
+            }
+            // rows past the end repeat row row0: their results are not stored
+            const uint8_t* p8 = row0 + lane + 32 * j < row_end
+                                    ? at
+                                    : plane + static_cast<size_t>(row0) * gpr + g0;
+            const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p8)) & 3u;
+            const uint32_t* p = reinterpret_cast<const uint32_t*>(p8 - skew);
+            uint32_t raw[kWords + 1];
+#pragma unroll
+            for (int i = 0; i <= kWords; ++i) raw[i] = load_word<kShared>(p + i);
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                s.w[j][i] = __funnelshift_r(raw[i], raw[i + 1], 8u * skew);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j, at += next) {
             const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 3);
             const uint32_t* p = reinterpret_cast<const uint32_t*>(at - skew);
+            const bool in = row0 + lane + 32 * j < row_end;
             uint32_t raw[kWords + 1];
 #pragma unroll
             for (int i = 0; i <= kWords; ++i)
-                raw[i] = row < row_end && 4 * i < nv + skew ? load_word<kShared>(p + i) : 0u;
+                raw[i] = in && 4 * i < nv + skew ? load_word<kShared>(p + i) : 0u;
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
                 const int left = nv - 4 * i;   // bytes of this word that count
@@ -252,13 +281,18 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
-    __shared__ uint64_t sc_full[2], sc_empty[2];
+    __shared__ uint64_t sc_full[2], sc_empty[2], sf_full[2], sf_empty[2];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word, n_tiles_sh;
+    __shared__ Tile table[kTileTable];
     volatile int* abort_flag = &abort_word;
-    // after the ring: the buffers of scale rows, then the experts' row offsets and first
+    // after the ring: two slots of scales in the tensor core's layout, each for kAhead
+    // stages, the buffers of scale rows, then the experts' row offsets and first
     // tiles (experts) or the partial sums of a split tile
-    uint8_t* sc_buf = smem + static_cast<size_t>(a.n_stages) * a.stage_bytes;
+    constexpr int kAhead = kSplit ? 2 : 4;
+    constexpr uint32_t kSfStage = 2u * kSfChunk * (1 + NB), kSfSlot = kAhead * kSfStage;
+    uint8_t* sf_buf = smem + static_cast<size_t>(a.n_stages) * a.stage_bytes;
+    uint8_t* sc_buf = sf_buf + 2u * kSfSlot;
     uint8_t* after = sc_buf + static_cast<size_t>(a.n_sc) * a.sc_bytes;
     int32_t* off = reinterpret_cast<int32_t*>(after);
     int32_t* first = off + a.n_experts + 1;
@@ -276,14 +310,16 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
     }
     if (tid == 0) {
         for (int i = 0; i < a.n_stages; ++i) {
-            mbar_init(&full[i], 3);   // the copies, W's scales, X's scales
+            mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], 4);
             mbar_init(&sc_full[i], 1);
-            mbar_init(&sc_empty[i], 2);
+            mbar_init(&sc_empty[i], 2);   // W's and X's scale warps
+            mbar_init(&sf_full[i], 2);
+            mbar_init(&sf_empty[i], 1);
         }
         mbar_init(&drain, 1);
         abort_word = 0;
@@ -332,11 +368,10 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
     const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x);   // (split: one tile)
     const uint32_t sf_cols = tmem + a.n_acc * a.tn;
     constexpr uint32_t sf_stage = 8u + 8u * NB;   // TMEM columns of a stage's scales
-    const uint32_t sf_off = kABytes + static_cast<uint32_t>(a.tn) * 128u;   // within a stage
 
     // A tile's token tiles come first, so that the weights of a row tile are read again
     // from L2; an expert's rows are cut into equal tiles of a multiple of 16.
-    auto tile_at = [&](int tile) {
+    auto locate = [&](int tile) {
         Tile t;
         if (a.offsets == nullptr) {
             t.e = 0;
@@ -362,6 +397,12 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         }
         return t;
     };
+    // Finding a tile takes over a thousand cycles (a search, divisions), and every role needs
+    // it: the CTA's first tiles are found once, by all threads together.
+    if (tid < kTileTable && tile0 + tid * tile_step < n_tiles)
+        table[tid] = locate(tile0 + tid * tile_step);
+    __syncthreads();
+    auto tile_at = [&](int tile, int j) { return j < kTileTable ? table[j] : locate(tile); };
     auto fail = [&]() {
         *abort_flag = 1;
         atomicOr(&g_fault_mx, 1);
@@ -369,74 +410,81 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
     int issued = 0, sc_issued = 0;   // (warp 0) stages and scale buffers started
 
     if (warp == 0) {
-        if (lane == 0) {
-            // --- copies
-            const uint64_t keep = l2_evict_last();
-            const uint64_t w_policy = kSplit || a.tn <= 16 ? l2_evict_first() : keep;
-            const uint32_t ring = smem_u32(smem);
-            int st = 0;
-            uint32_t phase = 1;   // of the empty barriers: the first round passes at once
-            bool ok = true;
-            // a tile's scale rows, contiguous in both planes, one tile ahead of its codes
-            auto copy_scales = [&](const Tile& t) {
-                const int b = sc_issued % 2;
-                if (!mbar_wait_for(&sc_empty[b], (static_cast<uint32_t>(sc_issued / 2) & 1u) ^ 1u,
+        // --- copies (the whole warp walks, one elected lane issues: as for the MMAs)
+        const bool leader = elect_one();
+        const uint64_t keep = l2_evict_last();
+        const uint64_t w_policy = kSplit || a.tn <= 16 ? l2_evict_first() : keep;
+        const uint32_t ring = smem_u32(smem);
+        uint32_t st = 0, phase = 1;   // phase of the empty barriers: the first round passes at once
+        int j = 0;
+        bool ok = true;
+        // a tile's scale rows, contiguous in both planes, one tile ahead of its codes
+        auto copy_scales = [&](const Tile& t) {
+            const int b = sc_issued % 2;
+            if (!mbar_wait_for(&sc_empty[b], (static_cast<uint32_t>(sc_issued / 2) & 1u) ^ 1u,
                                kWaitMx))
-                    return false;
-                ++sc_issued;
-                uint8_t* dst = sc_buf + static_cast<size_t>(b) * a.sc_bytes;
-                const size_t w_at = static_cast<size_t>(t.r0) * a.gpr;   // a multiple of 16
-                const size_t x_at = static_cast<size_t>(t.t0) * a.gpr;
-                const uint32_t skew = static_cast<uint32_t>(x_at) & 15u;
-                const uint32_t wb =
-                    (static_cast<uint32_t>(min(kM, a.rows - t.r0) * a.gpr) + 15u) & ~15u;
-                const uint32_t xb = (skew + static_cast<uint32_t>((t.t1 - t.t0) * a.gpr) + 15u) & ~15u;
+                return false;
+            ++sc_issued;
+            uint8_t* dst = sc_buf + static_cast<size_t>(b) * a.sc_bytes;
+            const size_t w_at = static_cast<size_t>(t.r0) * a.gpr;   // a multiple of 16
+            const size_t x_at = static_cast<size_t>(t.t0) * a.gpr;
+            const uint32_t skew = static_cast<uint32_t>(x_at) & 15u;
+            const uint32_t wb =
+                (static_cast<uint32_t>(min(kM, a.rows - t.r0) * a.gpr) + 15u) & ~15u;
+            const uint32_t xb = (skew + static_cast<uint32_t>((t.t1 - t.t0) * a.gpr) + 15u) & ~15u;
+            if (leader) {
                 mbar_arrive_expect_tx(&sc_full[b], wb + xb);
                 bulk_g2s(dst, a.w_scales + static_cast<size_t>(t.e) * a.bank_stride + w_at, wb,
                          &sc_full[b], w_policy);
                 bulk_g2s(dst + a.sc_w, a.x_scales + (x_at - skew), xb, &sc_full[b], keep);
-                return true;
-            };
-            if (a.n_sc > 0 && tile0 < n_tiles) ok = copy_scales(tile_at(tile0));
-            for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
-                const Tile t = tile_at(tile);
-                if (a.n_sc > 0 && tile + tile_step < n_tiles)
-                    ok = copy_scales(tile_at(tile + tile_step));
+            }
+            __syncwarp();
+            return true;
+        };
+        if (a.n_sc > 0 && tile0 < n_tiles) ok = copy_scales(tile_at(tile0, 0));
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
+            const Tile t = tile_at(tile, j);
+            const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
+            const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
+            const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box) * box_bytes;
+            for (int s = s_lo; s < s_hi; ++s, ++issued) {
+                ok = mbar_wait_for(&empty[st], phase, kWaitMx);
                 if (!ok) break;
-                const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
-                const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
-                const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box) * box_bytes;
-                for (int s = s_lo; s < s_hi; ++s, ++issued) {
-                    ok = mbar_wait_for(&empty[st], phase, kWaitMx);
-                    if (!ok) break;
-                    const uint32_t dst = ring + static_cast<uint32_t>(st) * a.stage_bytes;
+                const uint32_t dst = ring + st * a.stage_bytes;
+                if (leader) {
                     mbar_arrive_expect_tx(&full[st], bytes);
                     tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[st], w_policy);
                     for (int b = 0; b < n_box; ++b)
                         tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
                               s * (kK / 2), t.t0 + b * a.box, &full[st], keep);
-                    if (++st == a.n_stages) {
-                        st = 0;
-                        phase ^= 1u;
-                    }
                 }
-                ok = ok && !*abort_flag;
+                __syncwarp();
+                if (++st == static_cast<uint32_t>(a.n_stages)) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+                if (s == s_lo && a.n_sc > 0 && tile + tile_step < n_tiles) {
+                    ok = copy_scales(tile_at(tile + tile_step, j + 1));
+                    if (!ok) break;
+                }
             }
-            if (!ok) fail();
+            ok = ok && !*abort_flag;
         }
+        if (!ok) fail();
+        __syncwarp();
     } else if (warp == 1) {
         // --- MMAs: the whole warp walks the stages, so that descriptors and addresses stay
         // in uniform registers (computed by one lane alone they cost several hundred cycles
         // a stage); one elected lane issues
         const bool leader = elect_one();
         const uint32_t ring = smem_u32(smem);
-        const uint64_t op0 = operand_desc(ring), sf0 = scale_desc(ring + sf_off);
+        const uint64_t op0 = operand_desc(ring), sf0 = scale_desc(smem_u32(sf_buf));
         const uint32_t stage16 = a.stage_bytes >> 4;   // descriptors count 16 bytes
-        uint32_t st = 0, phase = 0;
+        uint32_t st = 0, phase = 0, group = 0;   // group: kAhead stages sharing a scale slot
         int j = 0;
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
-            const Tile t = tile_at(tile);
+            const Tile t = tile_at(tile, j);
             const int n = __shfl_sync(0xFFFFFFFFu, (t.t1 - t.t0 + 15) & ~15, 0);
             const uint32_t id0 = idesc_mxf4(n, 0u), id2 = idesc_mxf4(n, 2u);
             const int ab = j % a.n_acc;
@@ -446,12 +494,15 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
             fence_after_mx();
             const uint32_t d = tmem + ab * a.tn;
             for (int s = s_lo; s < s_hi && ok; ++s) {
-                ok = mbar_wait_for(&full[st], phase, kWaitMx);
+                const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
+                if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
+                ok = ok && mbar_wait_for(&full[st], phase, kWaitMx);
                 if (!ok) break;
                 fence_after_mx();
                 const uint32_t sfa = sf_cols + st * sf_stage, sfb = sfa + 8u;
                 const uint64_t ad = op0 + st * stage16, bd = ad + (kABytes >> 4);
-                const uint64_t sd = sf0 + st * stage16;
+                const uint64_t sd = sf0 + ((slot * kSfSlot + q * kSfStage) >> 4);
+                const bool last = q == kAhead - 1 || s + 1 == s_hi;
                 const uint32_t more = s > s_lo ? 1u : 0u;
                 // K = 64 at a time; the last stage of a row may hold fewer
                 const int kk_end = (a.gpr - s * kGroupsStage + 1) / 2;
@@ -470,8 +521,10 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
                     if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
                     if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
                     umma_commit_mx(&empty[st]);
+                    if (last) umma_commit_mx(&sf_empty[slot]);
                 }
                 __syncwarp();
+                group += last ? 1u : 0u;
                 if (++st == static_cast<uint32_t>(a.n_stages)) {
                     st = 0;
                     phase ^= 1u;
@@ -492,13 +545,12 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         const bool is_w = warp == 2;
         const int blocks = is_w ? 1 : NB;
         const uint32_t second = kSfChunk * static_cast<uint32_t>(blocks);
-        const uint32_t ring = smem_u32(smem) + sf_off + (is_w ? 0u : 2u * kSfChunk);
-        constexpr int kAhead = kSplit ? 2 : 4;
+        const uint32_t slots = smem_u32(sf_buf) + (is_w ? 0u : 2u * kSfChunk);
         int f_tile = tile0, f_step = s_lo;   // what to load next
         Tile ft{};
-        if (f_tile < n_tiles) ft = tile_at(f_tile);
-        int st = 0, f_count = 0;
-        uint32_t phase = 1;
+        if (f_tile < n_tiles) ft = tile_at(f_tile, 0);
+        int f_count = 0;
+        uint32_t group = 0;
         bool ok = true;
         auto fetch = [&](Scales<kAhead>(&r)[NB]) {
             if (f_tile >= n_tiles || !ok) return;
@@ -532,11 +584,11 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
                 if (!kSplit && a.n_sc > 0) {   // the tile's rows are in registers
                     __syncwarp();
                     if (lane == 0) mbar_arrive_m(&sc_empty[f_count % 2]);
-                    ++f_count;
                 }
+                ++f_count;
                 f_step = s_lo;
                 f_tile += tile_step;
-                if (f_tile < n_tiles) ft = tile_at(f_tile);
+                if (f_tile < n_tiles) ft = tile_at(f_tile, f_count);
             }
         };
         Scales<kAhead> cur[NB], nxt[NB];
@@ -544,23 +596,22 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead) {
                 fetch(nxt);
+                const uint32_t slot = group & 1u;
+                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_for(&sf_empty[slot],
+                                                                 ((group >> 1) & 1u) ^ 1u, kWaitMx));
+                if (!ok) break;
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    if (s0 + q >= s_hi) break;
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&empty[st], phase, kWaitMx));
-                    if (!ok) break;
-                    const uint32_t dst = ring + static_cast<uint32_t>(st) * a.stage_bytes;
+                for (int q = 0; q < kAhead; ++q)   // (stages past the tile's end: not read)
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        if (b < blocks) store_scales(cur[b], q, dst + b * kSfChunk, second, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_m(&full[st]);
-                    if (++st == a.n_stages) {
-                        st = 0;
-                        phase ^= 1u;
-                    }
-                }
+                        if (b < blocks)
+                            store_scales(cur[b], q,
+                                         slots + slot * kSfSlot + q * kSfStage + b * kSfChunk, second,
+                                         lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_m(&sf_full[slot]);
+                ++group;
 #pragma unroll
                 for (int b = 0; b < NB; ++b) cur[b] = nxt[b];
             }
@@ -572,7 +623,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         const int quarter = warp & 3;   // TMEM lanes 32 * quarter .. + 31
         int j = 0;
         for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step, ++j) {
-            const Tile t = tile_at(tile);
+            const Tile t = tile_at(tile, j);
             const int ab = j % a.n_acc;
             if (!__all_sync(0xFFFFFFFFu,
                             mbar_wait_for(&acc_full[ab], static_cast<uint32_t>(j / a.n_acc) & 1u,
@@ -620,7 +671,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
     if constexpr (kSplit) {
         cg::cluster_group cluster = cg::this_cluster();
         cluster.sync();   // every rank's partial sums are written
-        const Tile t = tile_at(tile0);
+        const Tile t = tile_at(tile0, 0);
         float* part = reinterpret_cast<float*>(after);
         const int n_out = (t.t1 - t.t0) * kM;
         for (int i = rank * kThreadsMx + tid; i < n_out && !*abort_flag;
@@ -698,7 +749,7 @@ int sm_count() {
     });
 }
 
-constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 2048;   // alignment and static arrays
+constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 2048;   // (the static arrays)
 
 template <typename T, bool kSplit, int NB>
 cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxArgs& a, T* Y,
@@ -707,7 +758,7 @@ cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxA
     const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
         return static_cast<int>(cudaFuncSetAttribute(k_mx_mm<T, kSplit, NB>,
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     static_cast<int>(kSmemMax - 1024)));
+                                                     static_cast<int>(kSmemMax - kSmemSlack)));
     }));
     if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
@@ -757,7 +808,7 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
         const int mean = (n_rows + n_experts - 1) / n_experts;
         a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 80 ? 96
                : mean <= 112 ? 128 : 192;
-        a.box = a.tn < 32 ? a.tn : 32;
+        a.box = a.tn < 64 ? a.tn : a.tn % 64 == 0 ? 64 : 32;
         a.n_tt = 0;
     } else {
         a.tn = std::min((n_rows + 15) / 16 * 16, kMaxTokens);
@@ -782,10 +833,11 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
         a.n_tt = (n_rows + a.tn - 1) / a.tn;
     }
     const int sf_blocks = (a.tn + 127) / 128;
-    a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * 128u + 2u * kSfChunk * (1 + sf_blocks);
+    a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * 128u;
     a.n_acc = split > 1 ? 1 : 2;
-    const size_t extra = split > 1 ? static_cast<size_t>(a.tn) * kM * 4
-                                   : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0;
+    const size_t sf_bytes = 2u * (split > 1 ? 2 : 4) * 2u * kSfChunk * (1 + sf_blocks);
+    const size_t extra = sf_bytes + (split > 1 ? static_cast<size_t>(a.tn) * kM * 4
+                                   : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0);
     // Whole scale rows of a tile by bulk copies, two tiles deep, where rows of a tile are short
     // enough; else (long rows, slices of a split tile) loads a few stages ahead.
     a.sc_w = static_cast<uint32_t>(kM * a.gpr + 15) & ~15u;
@@ -805,7 +857,7 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     // per KB at most) and none shares an SM with a kernel that takes them all.
     const size_t ring = static_cast<size_t>(a.n_stages) * a.stage_bytes +
                         static_cast<size_t>(a.n_sc) * a.sc_bytes + extra + 1024;
-    const size_t smem = split > 1 ? max(ring, static_cast<size_t>(40 * 1024)) : kSmemMax - 1024;
+    const size_t smem = split > 1 ? max(ring, static_cast<size_t>(40 * 1024)) : kSmemMax - kSmemSlack;
     CUtensorMap wmap, xmap;
     if (!code_map(&wmap, bank, cols, rows, n_experts, stride, kM) ||
         !code_map(&xmap, xq, cols, n_rows, 0, 16, a.box))
