@@ -127,10 +127,28 @@ def _addr(t) -> int | None:
     return t.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """torch's current stream of the current device as a handle.  Building a Stream object for
+    it costs about 3 us a call, as much as a launch; the raw getters do not (where torch has
+    them)."""
+    import torch
+    torch.cuda.current_stream()   # initialises CUDA
+    try:
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    except AttributeError:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
 def _stream(stream) -> int | None:
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -352,8 +370,16 @@ def _type(given, *tensors):
         import torch
         _TYPE_OF.update({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
                          torch.float16: TYPE_F16})
-    codes = {_TYPE_OF.get(t.dtype, -1) for t in tensors if hasattr(t, "dtype")}
-    return codes.pop() if len(codes) == 1 else -1
+    code = None
+    for t in tensors:
+        dtype = getattr(t, "dtype", None)
+        if dtype is None:
+            continue
+        c = _TYPE_OF.get(dtype, -1)
+        if code is not None and c != code:
+            return -1
+        code = c
+    return -1 if code is None else code
 
 
 def mxfp4_quant(x, x_rows, cols, ld, row_of, rows, out, values=None, type=None, stream=None):

@@ -2,6 +2,7 @@
 // widened to FP32 and stores rounded once to nearest even.
 #pragma once
 
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -30,5 +31,34 @@ template <typename T, int N>
 struct alignas(sizeof(T) * N) Pack {
     T v[N];
 };
+
+// i / d for 0 <= i < 2^32 as one multiplication (Granlund & Montgomery 1994): m =
+// ceil(2^(32 + s) / d) with s = ceil(log2 d), one bit more than 32 bits hold.
+struct FastDiv {
+    uint32_t d, m, s;
+    explicit FastDiv(uint32_t div) : d(div), m(0), s(0) {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t i) const {
+        if (d == 1) return i;
+        const uint32_t t = __umulhi(i, m);
+        return (t + ((i - t) >> 1)) >> (s - 1);
+    }
+};
+
+// Calls go(row0, units) over n_rows rows of
+// per_row units, in runs of rows whose units 32 bits can count.
+template <class F>
+cudaError_t over_rows(int n_rows, int per_row, F&& go) {
+    const uint32_t most = static_cast<uint32_t>((1u << 31) / static_cast<uint32_t>(per_row));
+    for (uint32_t row0 = 0; row0 < static_cast<uint32_t>(n_rows);) {
+        const uint32_t rows = std::min(most, static_cast<uint32_t>(n_rows) - row0);
+        const cudaError_t e = go(row0, rows * static_cast<uint32_t>(per_row));
+        if (e != cudaSuccess) return e;
+        row0 += rows;
+    }
+    return cudaSuccess;
+}
 
 }  // namespace mxk

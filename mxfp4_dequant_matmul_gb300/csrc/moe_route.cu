@@ -9,10 +9,12 @@
 // with its histogram turned into running positions.  Latency-bound: two passes
 // over 4 P bytes that stay in L1.
 //
-// The other kernels move rows and are bound by HBM.
+// The other kernels move rows.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -122,92 +124,166 @@ __global__ void __launch_bounds__(kSortThreads)
         token_at[i] = -1;
 }
 
+// --- moving rows ------------------------------------------------------------------------
+//
+// Bound by HBM, and for few rows by latency.  A row is cut into the widest units that keep
+// every row aligned (16 bytes down to one element); a thread takes kU units a block apart
+// in the flat [rows][units] space, with all their loads in flight before the first store.
+
 constexpr int kRThreads = 256;
 
-// xs[i] = x[token_at[i]], one row a block, P its access unit.
-template <typename P>
+// xs[i] = x[token_at[i]].
+template <typename P, int kU>
 __global__ void __launch_bounds__(kRThreads)
-    k_moe_dispatch(const P* __restrict__ x, int n_tokens, int per_row,
-                   const int32_t* __restrict__ token_at, P* __restrict__ xs) {
-    const size_t row = blockIdx.x;
-    const int t = __ldg(token_at + row);
-    const bool in = t >= 0 && t < n_tokens;
-    for (int c = threadIdx.x; c < per_row; c += kRThreads)
-        xs[row * per_row + c] = in ? x[static_cast<size_t>(t) * per_row + c] : P{};
-}
-
-// y[t] = sum_j w[t][j] o[pos_of[t][j]] (w == nullptr: 1), one token a block.
-template <typename T, int N>
-__global__ void __launch_bounds__(kRThreads)
-    k_moe_gather_sum(const Pack<T, N>* __restrict__ o, int n_rows, int top_k, int per_row,
-                     const int32_t* __restrict__ pos_of, const float* __restrict__ w,
-                     Pack<T, N>* __restrict__ y) {
-    const size_t t = blockIdx.x;
-    for (int c = threadIdx.x; c < per_row; c += kRThreads) {
-        float acc[N] = {};
-        for (int j = 0; j < top_k; ++j) {
-            const int pos = __ldg(pos_of + t * top_k + j);
-            if (pos < 0 || pos >= n_rows) continue;
-            const float wt = w != nullptr ? __ldg(w + t * top_k + j) : 1.0f;
-            const Pack<T, N> a = o[static_cast<size_t>(pos) * per_row + c];
+    k_moe_dispatch(const P* __restrict__ x, int n_tokens, uint32_t row0, uint32_t units,
+                   FastDiv per_row, const int32_t* __restrict__ token_at, P* __restrict__ xs) {
+    P v[kU];
+    const uint32_t i0 = blockIdx.x * (kRThreads * kU) + threadIdx.x;
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(wt, to_f32(a.v[i]), acc[i]);
-        }
-        Pack<T, N> r;
+    for (int u = 0; u < kU; ++u) {
+        const uint32_t i = i0 + u * kRThreads;
+        v[u] = P{};
+        if (i >= units) continue;
+        const uint32_t row = per_row.of(i);
+        const int t = __ldg(token_at + row0 + row);
+        if (t >= 0 && t < n_tokens)
+            v[u] = x[static_cast<size_t>(t) * per_row.d + (i - row * per_row.d)];
+    }
 #pragma unroll
-        for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(acc[i]);
-        y[t * per_row + c] = r;
+    for (int u = 0; u < kU; ++u) {
+        const uint32_t i = i0 + u * kRThreads;
+        if (i < units) xs[static_cast<size_t>(row0) * per_row.d + i] = v[u];
     }
 }
 
-// d_o[pos] = w dy[t], d_w = <dy[t], o[pos]>: one pair a block.
-template <typename T, int N>
+// y[t] = sum_j w[t][j] o[pos_of[t][j]] (w == nullptr: 1), four pairs' loads in flight.
+template <typename T, int N, int kU>
 __global__ void __launch_bounds__(kRThreads)
+    k_moe_gather_sum(const Pack<T, N>* __restrict__ o, int n_rows, int top_k, uint32_t row0,
+                     uint32_t units, FastDiv per_row, const int32_t* __restrict__ pos_of,
+                     const float* __restrict__ w, Pack<T, N>* __restrict__ y) {
+    const uint32_t i0 = blockIdx.x * (kRThreads * kU) + threadIdx.x;
+    float acc[kU][N] = {};
+    for (int j0 = 0; j0 < top_k; j0 += 4) {
+        Pack<T, N> v[kU][4];
+        float wt[kU][4];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const uint32_t i = i0 + u * kRThreads;
+            const uint32_t row = per_row.of(i), c = i - row * per_row.d;
+            const size_t p = (static_cast<size_t>(row0) + row) * top_k + j0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                wt[u][j] = 0.0f;
+                v[u][j] = Pack<T, N>{};
+                if (i >= units || j0 + j >= top_k) continue;
+                const int pos = __ldg(pos_of + p + j);
+                if (pos < 0 || pos >= n_rows) continue;
+                wt[u][j] = w != nullptr ? __ldg(w + p + j) : 1.0f;
+                v[u][j] = o[static_cast<size_t>(pos) * per_row.d + c];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int q = 0; q < N; ++q)
+                    acc[u][q] = fmaf(wt[u][j], to_f32(v[u][j].v[q]), acc[u][q]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const uint32_t i = i0 + u * kRThreads;
+        Pack<T, N> r;
+#pragma unroll
+        for (int q = 0; q < N; ++q) r.v[q] = from_f32<T>(acc[u][q]);
+        if (i < units) y[static_cast<size_t>(row0) * per_row.d + i] = r;
+    }
+}
+
+// d_o[pos] = w dy[t], d_w = <dy[t], o[pos]>: one token a block, four pairs at a time, each
+// unit of dy read once for the four.
+template <typename T, int N>
+__global__ void
     k_moe_combine_grad(const Pack<T, N>* __restrict__ dy, const Pack<T, N>* __restrict__ o,
                        int n_rows, int top_k, int per_row, const int32_t* __restrict__ pos_of,
                        const float* __restrict__ w, Pack<T, N>* __restrict__ d_o,
                        float* __restrict__ d_w) {
-    __shared__ float part[kRThreads / 32];
-    const size_t p = blockIdx.x, t = p / top_k;
-    const int pos = __ldg(pos_of + p);
-    if (pos < 0 || pos >= n_rows) {
-        if (threadIdx.x == 0) d_w[p] = 0.0f;
-        return;
-    }
-    const float wt = __ldg(w + p);
-    float acc = 0.0f;
-    for (int c = threadIdx.x; c < per_row; c += kRThreads) {
-        const Pack<T, N> a = dy[t * per_row + c];
-        const Pack<T, N> b = o[static_cast<size_t>(pos) * per_row + c];
-        Pack<T, N> r;
+    __shared__ float part[4][32];
+    const size_t t = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_warps = static_cast<int>(blockDim.x) >> 5;
+    for (int j0 = 0; j0 < top_k; j0 += 4) {
+        const size_t p = t * top_k + j0;
+        int pos[4];
+        float wt[4], acc[4] = {};
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float g = to_f32(a.v[i]);
-            acc = fmaf(g, to_f32(b.v[i]), acc);
-            r.v[i] = from_f32<T>(wt * g);
+        for (int j = 0; j < 4; ++j) {
+            pos[j] = j0 + j < top_k ? __ldg(pos_of + p + j) : -1;
+            if (pos[j] >= n_rows) pos[j] = -1;
+            wt[j] = pos[j] >= 0 ? __ldg(w + p + j) : 0.0f;
         }
-        d_o[static_cast<size_t>(pos) * per_row + c] = r;
-    }
+        for (int c = threadIdx.x; c < per_row; c += blockDim.x) {
+            const Pack<T, N> a = dy[t * per_row + c];
+            Pack<T, N> b[4];
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, m);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = acc;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int i = 1; i < kRThreads / 32; ++i) acc += part[i];
-        d_w[p] = acc;
+            for (int j = 0; j < 4; ++j)
+                if (pos[j] >= 0) b[j] = o[static_cast<size_t>(pos[j]) * per_row + c];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (pos[j] < 0) continue;
+                Pack<T, N> r;
+#pragma unroll
+                for (int q = 0; q < N; ++q) {
+                    const float g = to_f32(a.v[q]);
+                    acc[j] = fmaf(g, to_f32(b[j].v[q]), acc[j]);
+                    r.v[q] = from_f32<T>(wt[j] * g);
+                }
+                d_o[static_cast<size_t>(pos[j]) * per_row + c] = r;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) acc[j] += __shfl_xor_sync(0xFFFFFFFFu, acc[j], m);
+            if (lane == 0) part[j][warp] = acc[j];
+        }
+        __syncthreads();
+        if (warp < 4) {   // warp j adds pair j's sums (at least four warps a block)
+            float s = lane < n_warps ? part[warp][lane] : 0.0f;
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+            if (lane == 0 && j0 + warp < top_k) d_w[p + warp] = s;
+        }
+        __syncthreads();
     }
 }
 
-// Calls f(T{}, vector width): 16-byte accesses when the rows keep the base
-// pointers' alignment, else one element at a time.
+// Calls f(Pack<T, N>{}) with the widest unit that keeps every row of `width` elements
+// aligned: 16, 8 or 4 bytes, or one element.
 template <class F>
 cudaError_t by_type(int type, int width, F&& f) {
-    const bool vec = static_cast<long long>(width) * type_bytes(type) % 16 == 0;
-    if (type == kTypeF32)
-        return vec ? f(Pack<float, 4>{}) : f(Pack<float, 1>{});
-    if (type == kTypeBF16)
-        return vec ? f(Pack<__nv_bfloat16, 8>{}) : f(Pack<__nv_bfloat16, 1>{});
-    return vec ? f(Pack<__half, 8>{}) : f(Pack<__half, 1>{});
+    if (type == kTypeF32) {
+        if (width % 4 == 0) return f(Pack<float, 4>{});
+        if (width % 2 == 0) return f(Pack<float, 2>{});
+        return f(Pack<float, 1>{});
+    }
+    auto half_width = [&](auto zero) {
+        using T = decltype(zero);
+        if (width % 8 == 0) return f(Pack<T, 8>{});
+        if (width % 4 == 0) return f(Pack<T, 4>{});
+        if (width % 2 == 0) return f(Pack<T, 2>{});
+        return f(Pack<T, 1>{});
+    };
+    return type == kTypeBF16 ? half_width(__nv_bfloat16{}) : half_width(__half{});
+}
+
+// Units per thread: four where that still leaves several blocks an SM, else one.
+bool many_units(uint32_t units) { return units >= 4u * kRThreads * 152u * 4u; }
+
+unsigned blocks_of(uint32_t units, int per_thread) {
+    const uint32_t per_block = static_cast<uint32_t>(kRThreads * per_thread);
+    return static_cast<unsigned>((static_cast<uint64_t>(units) + per_block - 1) / per_block);
 }
 
 }  // namespace
@@ -244,17 +320,22 @@ cudaError_t launch_moe_sort(const int32_t* ids, int n_pairs, int top_k, int n_ex
 
 cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_rows, int width,
                                 const int32_t* token_at, void* xs, cudaStream_t s) {
-    const long long bytes = static_cast<long long>(width) * type_bytes(type);
-    auto go = [&](auto unit) {
+    return by_type(type, width, [&](auto unit) {
         using P = decltype(unit);
-        k_moe_dispatch<P><<<static_cast<unsigned>(n_rows), kRThreads, 0, s>>>(
-            static_cast<const P*>(x), n_tokens, static_cast<int>(bytes / sizeof(P)), token_at,
-            static_cast<P*>(xs));
-        return cudaGetLastError();
-    };
-    if (bytes % 16 == 0) return go(uint4{});
-    if (bytes % 4 == 0) return go(uint32_t{});
-    return go(uint16_t{});
+        const int per_row = width / static_cast<int>(sizeof(unit.v) / sizeof(unit.v[0]));
+        const FastDiv div(static_cast<uint32_t>(per_row));
+        return over_rows(n_rows, per_row, [&](uint32_t row0, uint32_t units) {
+            const P* xp = static_cast<const P*>(x);
+            P* out = static_cast<P*>(xs);
+            if (many_units(units))
+                k_moe_dispatch<P, 4><<<blocks_of(units, 4), kRThreads, 0, s>>>(
+                    xp, n_tokens, row0, units, div, token_at, out);
+            else
+                k_moe_dispatch<P, 1><<<blocks_of(units, 1), kRThreads, 0, s>>>(
+                    xp, n_tokens, row0, units, div, token_at, out);
+            return cudaGetLastError();
+        });
+    });
 }
 
 cudaError_t launch_moe_gather_sum(const void* o, int type, int n_tokens, int top_k, int width,
@@ -264,10 +345,18 @@ cudaError_t launch_moe_gather_sum(const void* o, int type, int n_tokens, int top
         using P = decltype(unit);
         constexpr int kN = sizeof(unit.v) / sizeof(unit.v[0]);
         using T = std::remove_reference_t<decltype(unit.v[0])>;
-        k_moe_gather_sum<T, kN><<<static_cast<unsigned>(n_tokens), kRThreads, 0, s>>>(
-            static_cast<const P*>(o), n_tokens * top_k, top_k, width / kN, pos_of, route_w,
-            static_cast<P*>(y));
-        return cudaGetLastError();
+        const FastDiv div(static_cast<uint32_t>(width / kN));
+        return over_rows(n_tokens, width / kN, [&](uint32_t row0, uint32_t units) {
+            const P* in = static_cast<const P*>(o);
+            P* out = static_cast<P*>(y);
+            if (many_units(units))
+                k_moe_gather_sum<T, kN, 2><<<blocks_of(units, 2), kRThreads, 0, s>>>(
+                    in, n_tokens * top_k, top_k, row0, units, div, pos_of, route_w, out);
+            else
+                k_moe_gather_sum<T, kN, 1><<<blocks_of(units, 1), kRThreads, 0, s>>>(
+                    in, n_tokens * top_k, top_k, row0, units, div, pos_of, route_w, out);
+            return cudaGetLastError();
+        });
     });
 }
 
@@ -279,9 +368,11 @@ cudaError_t launch_moe_combine_grad(const void* dy, const void* o, int type, int
         using P = decltype(unit);
         constexpr int kN = sizeof(unit.v) / sizeof(unit.v[0]);
         using T = std::remove_reference_t<decltype(unit.v[0])>;
-        k_moe_combine_grad<T, kN><<<static_cast<unsigned>(n_tokens * top_k), kRThreads, 0, s>>>(
-            static_cast<const P*>(dy), static_cast<const P*>(o), n_tokens * top_k, top_k,
-            width / kN, pos_of, route_w, static_cast<P*>(d_o), d_route_w);
+        const int per_row = width / kN;
+        const int threads = std::min(512, std::max(128, (per_row + 31) / 32 * 32));
+        k_moe_combine_grad<T, kN><<<static_cast<unsigned>(n_tokens), threads, 0, s>>>(
+            static_cast<const P*>(dy), static_cast<const P*>(o), n_tokens * top_k, top_k, per_row,
+            pos_of, route_w, static_cast<P*>(d_o), d_route_w);
         return cudaGetLastError();
     });
 }

@@ -95,6 +95,12 @@ __device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* map, int 
         : "memory");
 }
 
+__device__ __forceinline__ uint64_t l2_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 // Shared-memory matrix descriptors: operands K-major with 128-byte swizzle (8-row groups
 // 1024 bytes apart); scale chunks unswizzled 8 x 16-byte core matrices 128 bytes apart.
 __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
@@ -271,6 +277,53 @@ __device__ __forceinline__ void store_scales(const Scales<kAhead>& s, int q, uin
               s.w[2][2 * q + 1], s.w[3][2 * q + 1]);
 }
 
+// 32 outputs (TMEM lanes; `valid` of them exist) of each of n tokens (columns of `src`) to
+// y, tokens `pitch` elements apart.  FP32: a store is one token's 128 bytes.  BF16, even
+// pitch: lanes trade so that each holds four consecutive outputs of four tokens, and a
+// store is four tokens' 64 bytes (a store of two bytes a lane costs as much for a quarter).
+template <typename T>
+__device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int n, uint32_t src,
+                                           int lane) {
+    if (valid <= 0) return;
+    const bool quads = sizeof(T) == 2 && (pitch & 3) == 0 && valid == 32;
+    for (int c = 0; c < n; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(src + c, v);
+        if (quads) {
+            // columns as BF16 pairs of this lane's row: u[i] = (column i, column i + 8)
+            uint32_t u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // lane pair (l, l ^ 1): the even lane ends with both rows of columns 0..7,
+                // the odd one with both rows of columns 8..15
+                const uint32_t give = (lane & 1) ? v[i] : v[i + 8];
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+                const float lo = __uint_as_float((lane & 1) ? got : v[i]);
+                const float hi = __uint_as_float((lane & 1) ? v[i + 8] : got);
+                const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+                u[i] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            // lane pair (l, l ^ 2): rows 0..3 of the quad for half of the eight columns
+            const int col0 = (lane & 1) * 8 + ((lane & 2) ? 4 : 0);
+            T* dst = y + static_cast<size_t>(c + col0) * pitch + (lane & ~3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t give = (lane & 2) ? u[i] : u[i + 4];
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 2);
+                if (c + col0 + i < n)
+                    *reinterpret_cast<uint2*>(dst + static_cast<size_t>(i) * pitch) =
+                        (lane & 2) ? make_uint2(got, u[i + 4]) : make_uint2(u[i], got);
+            }
+        } else if (lane < valid) {
+            T* dst = y + static_cast<size_t>(c) * pitch + lane;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < n)
+                    dst[static_cast<size_t>(i) * pitch] = from_f32<T>(__uint_as_float(v[i]));
+        }
+    }
+}
+
 // NB: 128-token blocks of a stage's scales.  Split tiles (few tokens) leave registers for
 // two CTAs on an SM.
 template <typename T, bool kSplit, int NB>
@@ -413,7 +466,10 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         // --- copies (the whole warp walks, one elected lane issues: as for the MMAs)
         const bool leader = elect_one();
         const uint64_t keep = l2_evict_last();
-        const uint64_t w_policy = kSplit || a.tn <= 16 ? l2_evict_first() : keep;
+        // experts' weights pass through once; one matrix may still be there at its next use
+        const uint64_t w_policy = a.offsets != nullptr ? l2_evict_first()
+                                  : kSplit             ? l2_evict_normal()
+                                                       : keep;
         const uint32_t ring = smem_u32(smem);
         uint32_t st = 0, phase = 1;   // phase of the empty barriers: the first round passes at once
         int j = 0;
@@ -633,7 +689,6 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
             }
             fence_after_mx();
             const int n = t.t1 - t.t0;
-            const int r = t.r0 + quarter * 32 + lane;
             const uint32_t src =
                 tmem + ab * a.tn + (static_cast<uint32_t>(quarter * 32) << 16);
             if constexpr (kSplit) {
@@ -648,18 +703,8 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
                             s_hi > s_lo ? __uint_as_float(v[i]) : 0.0f;
                 }
             } else {
-                for (int c = 0; c < n; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld16(src + c, v);
-                    T* dst = Y + static_cast<size_t>(t.t0 + c) * a.rows + r;
-                    if (r < a.rows) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < n)
-                                dst[static_cast<size_t>(i) * a.rows] =
-                                    from_f32<T>(__uint_as_float(v[i]));
-                    }
-                }
+                store_tile(Y + static_cast<size_t>(t.t0) * a.rows + t.r0 + quarter * 32, a.rows,
+                           min(32, a.rows - t.r0 - quarter * 32), n, src, lane);
             }
             fence_before_mx();
             __syncwarp();
@@ -806,8 +851,7 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     int split = 1, per_sm = 1;
     if (offsets != nullptr) {
         const int mean = (n_rows + n_experts - 1) / n_experts;
-        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 80 ? 96
-               : mean <= 112 ? 128 : 192;
+        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 80 ? 96 : 128;
         a.box = a.tn < 64 ? a.tn : a.tn % 64 == 0 ? 64 : 32;
         a.n_tt = 0;
     } else {

@@ -72,41 +72,52 @@ __device__ __forceinline__ float swiglu(float g, float u, float limit) {
     return moe_act(g, u, MoeAct{nullptr, limit, 0}, 0);
 }
 
+// The 8 elements of one item (zeros past the end or for a row index out of range).
 template <typename T, bool kAct, bool kVec>
-__global__ void __launch_bounds__(kQThreads)
-    k_mx_quant(const T* __restrict__ x, const T* __restrict__ up, int x_rows, int cols,
-               long long ld, const int32_t* __restrict__ row_of, float limit, int rows,
-               uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
-               T* __restrict__ values) {
-    const int per_row = cols / 8;
-    const size_t n = static_cast<size_t>(rows) * per_row;   // a multiple of 4
-    for (size_t base = static_cast<size_t>(blockIdx.x) * kQThreads; base < n;
-         base += static_cast<size_t>(gridDim.x) * kQThreads) {
-        const size_t i = base + threadIdx.x;
-        const bool in = i < n;   // the same for the four lanes of a group
-        float v[8] = {};
-        if (in) {
-            const size_t r = i / per_row;
-            const int c = static_cast<int>(i - r * per_row) * 8;
-            long long src = static_cast<long long>(r);
-            if (row_of != nullptr) {
-                src = __ldg(row_of + r);
-                if (src >= x_rows) src = -1;
-            }
-            if (src >= 0) {
-                load8<T, kVec>(x + src * ld + c, v);
-                if constexpr (kAct) {
-                    float u[8];
-                    load8<T, kVec>(up + src * ld + c, u);
+__device__ __forceinline__ void load_item(float (&v)[8], const T* x, const T* up, int x_rows,
+                                          long long ld, const int32_t* row_of, float limit,
+                                          uint32_t row0, uint32_t i, uint32_t items,
+                                          const FastDiv& per_row) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = swiglu(v[q], u[q], limit);
-                }
-            }
-        }
+    for (int q = 0; q < 8; ++q) v[q] = 0.0f;
+    if (i >= items) return;
+    const uint32_t r = per_row.of(i);
+    const uint32_t c = (i - r * per_row.d) * 8;
+    long long src = static_cast<long long>(row0) + r;
+    if (row_of != nullptr) {
+        src = __ldg(row_of + src);
+        if (src < 0 || src >= x_rows) return;
+    }
+    load8<T, kVec>(x + src * ld + c, v);
+    if constexpr (kAct) {
+        float u[8];
+        load8<T, kVec>(up + src * ld + c, u);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = swiglu(v[q], u[q], limit);
+    }
+}
+
+// Items of 8 elements in the flat [rows][cols / 8] space; a thread takes kU of them a block
+// apart, all loaded before the first is quantised.
+template <typename T, bool kAct, bool kVec, int kU>
+__global__ void __launch_bounds__(kQThreads)
+    k_mx_quant(const T* __restrict__ x, const T* __restrict__ up, int x_rows, long long ld,
+               const int32_t* __restrict__ row_of, float limit, uint32_t row0, uint32_t items,
+               FastDiv per_row, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
+               T* __restrict__ values) {
+    const uint32_t i0 = blockIdx.x * (kQThreads * kU) + threadIdx.x;
+    const size_t first = static_cast<size_t>(row0) * per_row.d;   // items of earlier launches
+    float v[kU][8];
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+        load_item<T, kAct, kVec>(v[u], x, up, x_rows, ld, row_of, limit, row0,
+                                 i0 + u * kQThreads, items, per_row);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
         // largest magnitude as bits: a NaN or infinity has exponent 255
         uint32_t top = 0;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(v[q]) & 0x7FFFFFFFu);
+        for (int q = 0; q < 8; ++q) top = max(top, __float_as_uint(v[u][q]) & 0x7FFFFFFFu);
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         const uint32_t e = top >> 23;
@@ -114,17 +125,19 @@ __global__ void __launch_bounds__(kQThreads)
         const uint32_t k = bad ? 255u : (e > 2u ? e - 2u : 0u);
         const float inv = __uint_as_float((254u - (bad ? 127u : k)) << 23);   // 2^(127-k)
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = bad ? 0.0f : __fmul_rn(v[q], inv);
-        const uint32_t word = f32x8_to_e2m1x8(v);
-        if (!in) continue;
-        codes[i] = word;
-        if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(k);
+        for (int q = 0; q < 8; ++q) v[u][q] = bad ? 0.0f : __fmul_rn(v[u][q], inv);
+        const uint32_t word = f32x8_to_e2m1x8(v[u]);
+        const uint32_t i = i0 + u * kQThreads;
+        if (i >= items) continue;   // (a group's four lanes together)
+        const size_t at = first + i;
+        codes[at] = word;
+        if ((i & 3) == 0) scales[at >> 2] = static_cast<uint8_t>(k);
         if (values != nullptr) {
             const float sc = e8m0_to_f32(k);
-            e2m1x8_to_f32(word, v);
+            e2m1x8_to_f32(word, v[u]);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __fmul_rn(v[q], sc);
-            store8<T>(values + i * 8, v);
+            for (int q = 0; q < 8; ++q) v[u][q] = __fmul_rn(v[u][q], sc);
+            store8<T>(values + at * 8, v[u]);
         }
     }
 }
@@ -133,21 +146,26 @@ template <typename T>
 cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, long long ld,
                          const int32_t* row_of, float limit, int rows, uint8_t* out, void* values,
                          cudaStream_t s) {
-    const size_t n = static_cast<size_t>(rows) * (cols / 8);
-    const size_t blocks = (n + kQThreads - 1) / kQThreads;
-    const unsigned grid = static_cast<unsigned>(blocks < (1u << 30) ? blocks : (1u << 30));
     auto* codes = reinterpret_cast<uint32_t*>(out);
     uint8_t* scales = out + static_cast<size_t>(rows) * cols / 2;
     const bool vec = (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(up) |
                       (static_cast<uintptr_t>(ld) * sizeof(T))) % 16 == 0;
-    auto go = [&](auto kernel) {
-        kernel<<<grid, kQThreads, 0, s>>>(static_cast<const T*>(x), static_cast<const T*>(up),
-                                          x_rows, cols, ld, row_of, limit, rows, codes, scales,
-                                          static_cast<T*>(values));
-        return cudaGetLastError();
-    };
-    if (up != nullptr) return vec ? go(k_mx_quant<T, true, true>) : go(k_mx_quant<T, true, false>);
-    return vec ? go(k_mx_quant<T, false, true>) : go(k_mx_quant<T, false, false>);
+    const FastDiv per_row(static_cast<uint32_t>(cols / 8));
+    return over_rows(rows, cols / 8, [&](uint32_t row0, uint32_t items) {
+        auto go = [&](auto kernel, uint32_t per_thread) {
+            const uint32_t per_block = kQThreads * per_thread;
+            kernel<<<(items + per_block - 1) / per_block, kQThreads, 0, s>>>(
+                static_cast<const T*>(x), static_cast<const T*>(up), x_rows, ld, row_of, limit,
+                row0, items, per_row, codes, scales, static_cast<T*>(values));
+            return cudaGetLastError();
+        };
+        // two items a thread where that still leaves several blocks an SM
+        const bool two = items >= 2u * kQThreads * 152u * 8u;
+        if (up != nullptr)
+            return vec ? go(k_mx_quant<T, true, true, 1>, 1) : go(k_mx_quant<T, true, false, 1>, 1);
+        if (!vec) return go(k_mx_quant<T, false, false, 1>, 1);
+        return two ? go(k_mx_quant<T, false, true, 2>, 2) : go(k_mx_quant<T, false, true, 1>, 1);
+    });
 }
 
 }  // namespace
