@@ -26,10 +26,34 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive elements moved as one access (N * sizeof(T) = 4, 8 or 16 bytes).
+// N consecutive elements moved as one access (N * sizeof(T) = 2, 4, 8 or 16 bytes).  The
+// bits are held as integers: copies of element structs come out element by element.
+template <int kBytes>
+struct RawOf;
+template <>
+struct RawOf<2> { using type = uint16_t; };
+template <>
+struct RawOf<4> { using type = uint32_t; };
+template <>
+struct RawOf<8> { using type = uint2; };
+template <>
+struct RawOf<16> { using type = uint4; };
+
 template <typename T, int N>
-struct alignas(sizeof(T) * N) Pack {
-    T v[N];
+struct Pack {
+    using Elem = T;
+    static constexpr int kN = N;
+    typename RawOf<sizeof(T) * N>::type raw;
+    __device__ __forceinline__ void get(float (&f)[N]) const {
+        const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = to_f32(e[i]);
+    }
+    __device__ __forceinline__ void set(const float (&f)[N]) {
+        T* e = reinterpret_cast<T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = from_f32<T>(f[i]);
+    }
 };
 
 // i / d for 0 <= i < 2^32 as one multiplication (Granlund & Montgomery 1994): m =

@@ -14,7 +14,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -26,7 +25,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;   // at most
 constexpr int kSortCluster = 8;
 
 __global__ void __launch_bounds__(kSortThreads)
@@ -34,94 +33,106 @@ __global__ void __launch_bounds__(kSortThreads)
                int32_t* __restrict__ token_at, int32_t* __restrict__ pos_of,
                int32_t* __restrict__ offsets) {
     extern __shared__ int32_t sort_smem[];
-    int32_t* hist = sort_smem;                              // [kSortWarps][n_experts]
-    int32_t* total = sort_smem + kSortWarps * n_experts;    // [n_experts], read by the cluster
+    const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
+    int32_t* total = sort_smem;              // [n_experts], read by the cluster
+    int32_t* base = total + n_experts;       // [n_experts]
+    int32_t* hist = base + n_experts;        // [warps][n_experts]
     __shared__ int32_t warp_sum[kSortWarps];
-    __shared__ int32_t n_kept;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
     const int n_cta = static_cast<int>(cluster.num_blocks());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int32_t* mine = hist + warp * n_experts;
 
-    for (int i = tid; i < kSortWarps * n_experts; i += kSortThreads) hist[i] = 0;
-    __syncthreads();
-    const long long p0 = (static_cast<long long>(rank) * kSortWarps + warp) * run;
+    const long long p0 = (static_cast<long long>(rank) * warps + warp) * run;
     const int lo = static_cast<int>(min(p0, static_cast<long long>(n_pairs)));
     const int hi = static_cast<int>(min(p0 + run, static_cast<long long>(n_pairs)));
+    // the ids of the run's first 32 pairs (all of it, often) stay in a register
+    const int id0 = lo + lane < hi ? __ldg(ids + lo + lane) : -1;
+    auto id_of = [&](int p) {
+        const int id = p == lo ? id0 : p + lane < hi ? __ldg(ids + p + lane) : -1;
+        return id >= 0 && id < n_experts ? id : -1;
+    };
+    for (int e = lane; e < n_experts; e += 32) mine[e] = 0;
+    __syncwarp();
     for (int p = lo; p < hi; p += 32) {
-        const int id = p + lane < hi ? __ldg(ids + p + lane) : -1;
-        const bool ok = id >= 0 && id < n_experts;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, ok ? id : -1);
-        if (ok && lane == __ffs(same) - 1) mine[id] += __popc(same);
+        const int id = id_of(p);
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
         __syncwarp();
     }
     __syncthreads();
     // per expert: exclusive sums over the warps, and the CTA's total
-    for (int e = tid; e < n_experts; e += kSortThreads) {
+    for (int e = tid; e < n_experts; e += threads) {
         int32_t sum = 0;
-        for (int w = 0; w < kSortWarps; ++w) {
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) {
             const int32_t c = hist[w * n_experts + e];
             hist[w * n_experts + e] = sum;
             sum += c;
         }
         total[e] = sum;
     }
-    cluster.sync();
-    // all CTAs' totals (n_experts <= kSortThreads: one expert per thread) and the
-    // exclusive sum over the experts
-    int32_t all = 0, before = 0;
-    if (tid < n_experts) {
-        for (int c = 0; c < n_cta; ++c) {
-            const int32_t t = cluster.map_shared_rank(total, c)[tid];
-            if (c < rank) before += t;
-            all += t;
-        }
-    }
-    int32_t scan = all;
+    if (n_cta > 1) cluster.sync();
+    else __syncthreads();
+    // all CTAs' totals and the exclusive sum over the experts, a block of experts at a time
+    int32_t kept = 0;
+    for (int e0 = 0; e0 < n_experts; e0 += threads) {
+        const int e = e0 + tid;
+        int32_t all = 0, before = 0;
+        if (e < n_experts) {
+            if (n_cta == 1) {
+                all = total[e];
+            } else {
+                int32_t t[kSortCluster];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int32_t o = __shfl_up_sync(0xFFFFFFFFu, scan, d);
-        if (lane >= d) scan += o;
-    }
-    if (lane == 31) warp_sum[warp] = scan;
-    __syncthreads();
-    if (warp == 0) {
-        int32_t s = warp_sum[lane];
+                for (int c = 0; c < kSortCluster; ++c) t[c] = cluster.map_shared_rank(total, c)[e];
+#pragma unroll
+                for (int c = 0; c < kSortCluster; ++c) {
+                    if (c < rank) before += t[c];
+                    all += t[c];
+                }
+            }
+        }
+        int32_t scan = all;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xFFFFFFFFu, scan, d);
+            if (lane >= d) scan += o;
+        }
+        if (lane == 31) warp_sum[warp] = scan;
+        __syncthreads();
+        int32_t s = lane < warps ? warp_sum[lane] : 0;   // (every warp for itself)
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int32_t o = __shfl_up_sync(0xFFFFFFFFu, s, d);
             if (lane >= d) s += o;
         }
-        warp_sum[lane] = s;
+        const int32_t ahead = __shfl_sync(0xFFFFFFFFu, s, max(warp - 1, 0));
+        const int32_t start = kept + scan - all + (warp > 0 ? ahead : 0);
+        if (e < n_experts) {
+            base[e] = start + before;
+            if (rank == 0) offsets[e] = start;
+        }
+        kept += __shfl_sync(0xFFFFFFFFu, s, 31);
+        __syncthreads();
     }
-    __syncthreads();
-    const int32_t start = scan - all + (warp > 0 ? warp_sum[warp - 1] : 0);
-    if (tid < n_experts) {
-        for (int w = 0; w < kSortWarps; ++w) hist[w * n_experts + tid] += start + before;
-        if (rank == 0) offsets[tid] = start;
-    }
-    if (tid == n_experts - 1) {
-        n_kept = start + all;
-        if (rank == 0) offsets[n_experts] = start + all;
-    }
-    cluster.sync();   // the totals are read; positions and n_kept are written
+    if (rank == 0 && tid == 0) offsets[n_experts] = kept;
     for (int p = lo; p < hi; p += 32) {
-        const int id = p + lane < hi ? __ldg(ids + p + lane) : -1;
-        const bool ok = id >= 0 && id < n_experts;
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, ok ? id : -1);
+        const int id = id_of(p);
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
         int32_t pos = -1;
-        if (ok) pos = mine[id] + __popc(same & ((1u << lane) - 1u));
+        if (id >= 0) pos = base[id] + mine[id] + __popc(same & ((1u << lane) - 1u));
         __syncwarp();
-        if (ok && lane == __ffs(same) - 1) mine[id] += __popc(same);
+        if (id >= 0 && lane == __ffs(same) - 1) mine[id] += __popc(same);
         __syncwarp();
         if (p + lane < hi) {
             pos_of[p + lane] = pos;
-            if (ok) token_at[pos] = (p + lane) / top_k;
+            if (id >= 0) token_at[pos] = (p + lane) / top_k;
         }
     }
-    for (int i = n_kept + rank * kSortThreads + tid; i < n_pairs; i += n_cta * kSortThreads)
-        token_at[i] = -1;
+    for (int i = kept + rank * threads + tid; i < n_pairs; i += n_cta * threads) token_at[i] = -1;
+    if (n_cta > 1) cluster.sync();   // no CTA leaves while its totals may be read
 }
 
 // --- moving rows ------------------------------------------------------------------------
@@ -142,7 +153,7 @@ __global__ void __launch_bounds__(kRThreads)
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         const uint32_t i = i0 + u * kRThreads;
-        v[u] = P{};
+        v[u].raw = {};
         if (i >= units) continue;
         const uint32_t row = per_row.of(i);
         const int t = __ldg(token_at + row0 + row);
@@ -175,7 +186,7 @@ __global__ void __launch_bounds__(kRThreads)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 wt[u][j] = 0.0f;
-                v[u][j] = Pack<T, N>{};
+                v[u][j].raw = {};
                 if (i >= units || j0 + j >= top_k) continue;
                 const int pos = __ldg(pos_of + p + j);
                 if (pos < 0 || pos >= n_rows) continue;
@@ -186,17 +197,18 @@ __global__ void __launch_bounds__(kRThreads)
 #pragma unroll
         for (int u = 0; u < kU; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                float f[N];
+                v[u][j].get(f);
 #pragma unroll
-                for (int q = 0; q < N; ++q)
-                    acc[u][q] = fmaf(wt[u][j], to_f32(v[u][j].v[q]), acc[u][q]);
+                for (int q = 0; q < N; ++q) acc[u][q] = fmaf(wt[u][j], f[q], acc[u][q]);
+            }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         const uint32_t i = i0 + u * kRThreads;
         Pack<T, N> r;
-#pragma unroll
-        for (int q = 0; q < N; ++q) r.v[q] = from_f32<T>(acc[u][q]);
+        r.set(acc[u]);
         if (i < units) y[static_cast<size_t>(row0) * per_row.d + i] = r;
     }
 }
@@ -227,19 +239,24 @@ __global__ void
             const Pack<T, N> a = dy[t * per_row + c];
             Pack<T, N> b[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                b[j].raw = {};
                 if (pos[j] >= 0) b[j] = o[static_cast<size_t>(pos[j]) * per_row + c];
+            }
+            float g[N];
+            a.get(g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (pos[j] < 0) continue;
-                Pack<T, N> r;
+                float f[N];
+                b[j].get(f);
 #pragma unroll
                 for (int q = 0; q < N; ++q) {
-                    const float g = to_f32(a.v[q]);
-                    acc[j] = fmaf(g, to_f32(b[j].v[q]), acc[j]);
-                    r.v[q] = from_f32<T>(wt[j] * g);
+                    acc[j] = pos[j] >= 0 ? fmaf(g[q], f[q], acc[j]) : 0.0f;
+                    f[q] = wt[j] * g[q];
                 }
-                d_o[static_cast<size_t>(pos[j]) * per_row + c] = r;
+                Pack<T, N> r;
+                r.set(f);
+                if (pos[j] >= 0) d_o[static_cast<size_t>(pos[j]) * per_row + c] = r;
             }
         }
 #pragma unroll
@@ -291,19 +308,21 @@ unsigned blocks_of(uint32_t units, int per_thread) {
 cudaError_t launch_moe_sort(const int32_t* ids, int n_pairs, int top_k, int n_experts,
                             int32_t* token_at, int32_t* pos_of, int32_t* offsets,
                             cudaStream_t s) {
-    const size_t smem = static_cast<size_t>(kSortWarps + 1) * n_experts * sizeof(int32_t);
     static PerDevice memo;
     const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
         return static_cast<int>(cudaFuncSetAttribute(
             k_moe_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            static_cast<int>((kSortWarps + 1) * kSortThreads * sizeof(int32_t))));
+            static_cast<int>((kSortWarps + 2) * kSortThreads * sizeof(int32_t))));
     }));
     if (attr_err != cudaSuccess) return attr_err;
-    const int n_cta = n_pairs <= kSortThreads ? 1 : kSortCluster;
-    const int run = (n_pairs + n_cta * kSortThreads - 1) / (n_cta * kSortThreads) * 32;
+    // one CTA for as many pairs as its warps take in two steps of 32, else a cluster of 8
+    const int n_cta = n_pairs <= 2 * kSortThreads ? 1 : kSortCluster;
+    const int warps = std::min(kSortWarps, std::max(4, (n_pairs + 32 * n_cta - 1) / (32 * n_cta)));
+    const int run = (n_pairs + n_cta * warps * 32 - 1) / (n_cta * warps * 32) * 32;
+    const size_t smem = static_cast<size_t>(warps + 2) * n_experts * sizeof(int32_t);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n_cta));
-    cfg.blockDim = dim3(kSortThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -322,7 +341,7 @@ cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_row
                                 const int32_t* token_at, void* xs, cudaStream_t s) {
     return by_type(type, width, [&](auto unit) {
         using P = decltype(unit);
-        const int per_row = width / static_cast<int>(sizeof(unit.v) / sizeof(unit.v[0]));
+        const int per_row = width / P::kN;
         const FastDiv div(static_cast<uint32_t>(per_row));
         return over_rows(n_rows, per_row, [&](uint32_t row0, uint32_t units) {
             const P* xp = static_cast<const P*>(x);
@@ -343,8 +362,8 @@ cudaError_t launch_moe_gather_sum(const void* o, int type, int n_tokens, int top
                                   cudaStream_t s) {
     return by_type(type, width, [&](auto unit) {
         using P = decltype(unit);
-        constexpr int kN = sizeof(unit.v) / sizeof(unit.v[0]);
-        using T = std::remove_reference_t<decltype(unit.v[0])>;
+        constexpr int kN = P::kN;
+        using T = typename P::Elem;
         const FastDiv div(static_cast<uint32_t>(width / kN));
         return over_rows(n_tokens, width / kN, [&](uint32_t row0, uint32_t units) {
             const P* in = static_cast<const P*>(o);
@@ -366,8 +385,8 @@ cudaError_t launch_moe_combine_grad(const void* dy, const void* o, int type, int
                                     cudaStream_t s) {
     return by_type(type, width, [&](auto unit) {
         using P = decltype(unit);
-        constexpr int kN = sizeof(unit.v) / sizeof(unit.v[0]);
-        using T = std::remove_reference_t<decltype(unit.v[0])>;
+        constexpr int kN = P::kN;
+        using T = typename P::Elem;
         const int per_row = width / kN;
         const int threads = std::min(512, std::max(128, (per_row + 31) / 32 * 32));
         k_moe_combine_grad<T, kN><<<static_cast<unsigned>(n_tokens), threads, 0, s>>>(

@@ -37,17 +37,19 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8]) {
     return w;
 }
 
-// 8 elements at p; kVec: p is aligned to 8 * sizeof(T) or 16 bytes.
+// 8 elements at p; kVec: p is 16-byte aligned.
 template <typename T, bool kVec>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
     if constexpr (kVec) {
         constexpr int kN = 16 / sizeof(T);
 #pragma unroll
         for (int q = 0; q < 8 / kN; ++q) {
-            const uint4 raw = ldg_stream(reinterpret_cast<const uint4*>(p) + q);
-            const Pack<T, kN> a = *reinterpret_cast<const Pack<T, kN>*>(&raw);
+            Pack<T, kN> a;
+            a.raw = ldg_stream(reinterpret_cast<const uint4*>(p) + q);
+            float f[kN];
+            a.get(f);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) v[q * kN + i] = to_f32(a.v[i]);
+            for (int i = 0; i < kN; ++i) v[q * kN + i] = f[i];
         }
     } else {
 #pragma unroll
@@ -60,10 +62,12 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
     constexpr int kN = 16 / sizeof(T);
 #pragma unroll
     for (int q = 0; q < 8 / kN; ++q) {
-        Pack<T, kN> a;
+        float f[kN];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) a.v[i] = from_f32<T>(v[q * kN + i]);
-        *reinterpret_cast<Pack<T, kN>*>(p + q * kN) = a;
+        for (int i = 0; i < kN; ++i) f[i] = v[q * kN + i];
+        Pack<T, kN> a;
+        a.set(f);
+        *reinterpret_cast<uint4*>(p + q * kN) = a.raw;
     }
 }
 
