@@ -8,7 +8,7 @@
 // exact unless it underflows far below half of E2M1's smallest step, so the
 // code is the only rounding.
 //
-// Bound by HBM: each element is read once and 17/32 byte (and the rounded value)
+// Bound by HBM in FP32: each element is read once and 17/32 byte (and the rounded value)
 // written.  A thread takes 8 elements (one 16-byte load in 16-bit types), four
 // lanes a group: amax by two shuffles, one 32-bit word of codes per lane (128
 // bytes per warp) and the group's scale byte from the first of the four.
@@ -212,62 +212,81 @@ __device__ __forceinline__ float2 halves_to_f32<__nv_bfloat16>(uint32_t h) {
 template <>
 __device__ __forceinline__ float2 halves_to_f32<__half>(uint32_t h) { return f16x2_to_f32x2(h); }
 
+// Packed maximum of unsigned halves.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ void ldg_stream32(const void* p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+
+__device__ __forceinline__ void stg32(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
+                 "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
+// An item is 16 elements (32 bytes, one access), two lanes a group.
 template <typename T, int kU, bool kValues>
 __global__ void __launch_bounds__(kQThreads)
     k_mx_quant16(const T* __restrict__ x, int x_rows, long long ld,
                  const int32_t* __restrict__ row_of, uint32_t row0, uint32_t items,
-                 FastDiv per_row, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
-                 uint4* __restrict__ values) {
+                 FastDiv per_row, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
+                 T* __restrict__ values) {
     const uint32_t i0 = blockIdx.x * (kQThreads * kU) + threadIdx.x;
-    const size_t first = static_cast<size_t>(row0) * per_row.d;
-    uint32_t raw[kU][4];
+    const size_t first = static_cast<size_t>(row0) * per_row.d + i0;
+    uint32_t raw[kU][8];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         const uint32_t i = i0 + u * kQThreads;
-        raw[u][0] = raw[u][1] = raw[u][2] = raw[u][3] = 0u;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) raw[u][q] = 0u;
         if (i < items) {
             const uint32_t r = per_row.of(i);
-            long long src = static_cast<long long>(row0) + r;
-            if (row_of != nullptr) {
-                src = __ldg(row_of + src);
-                if (src >= x_rows) src = -1;
-            }
-            if (src >= 0) {
-                const uint4 q = ldg_stream(
-                    reinterpret_cast<const uint4*>(x + src * ld + (i - r * per_row.d) * 8));
-                raw[u][0] = q.x;
-                raw[u][1] = q.y;
-                raw[u][2] = q.z;
-                raw[u][3] = q.w;
-            }
+            int src = static_cast<int>(row0 + r);
+            if (row_of != nullptr) src = __ldg(row_of + src);
+            if (src >= 0 && src < x_rows)
+                ldg_stream32(x + src * ld + (i - r * per_row.d) * 16, raw[u]);
         }
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-        uint32_t top = __vmaxu2(__vmaxu2(raw[u][0] & 0x7FFF7FFFu, raw[u][1] & 0x7FFF7FFFu),
-                                __vmaxu2(raw[u][2] & 0x7FFF7FFFu, raw[u][3] & 0x7FFF7FFFu));
-        top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        uint32_t top = raw[u][0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int q = 1; q < 8; ++q) top = max_u16x2(top, raw[u][q] & 0x7FFF7FFFu);
+        top = max_u16x2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top & 0xFFFFu, top >> 16);
         const uint32_t e = __float_as_uint(halves_to_f32<T>(top).x) >> 23;
         const bool bad = e == 255u;
         const uint32_t k = bad ? 255u : (e > 2u ? e - 2u : 0u);
         const float inv = __uint_as_float((254u - (bad ? 127u : k)) << 23);   // 2^(127-k)
-        float v[8];
+        uint32_t word[2];
+        uint4 val[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float2 f =
-                __fmul2_rn(halves_to_f32<T>(raw[u][q]), make_float2(inv, inv));
-            v[2 * q] = f.x;
-            v[2 * q + 1] = f.y;
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            const uint32_t r4[4] = {raw[u][4 * h], raw[u][4 * h + 1], raw[u][4 * h + 2],
+                                    raw[u][4 * h + 3]};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 f = __fmul2_rn(halves_to_f32<T>(r4[q]), make_float2(inv, inv));
+                v[2 * q] = f.x;
+                v[2 * q + 1] = f.y;
+            }
+            word[h] = bad ? 0u : f32x8_to_e2m1x8(v);
+            if (kValues) val[h] = rounded_values<T>(word[h], r4, k);
         }
-        const uint32_t word = bad ? 0u : f32x8_to_e2m1x8(v);
-        const uint32_t i = i0 + u * kQThreads;
-        if (i >= items) continue;   // (a group's four lanes together)
-        const size_t at = first + i;
-        codes[at] = word;
-        if ((i & 3) == 0) scales[at >> 2] = static_cast<uint8_t>(k);
-        if (kValues) values[at] = rounded_values<T>(word, raw[u], k);
+        if (i0 + u * kQThreads >= items) continue;   // (a group's two lanes together)
+        const size_t at = first + u * kQThreads;
+        codes[at] = make_uint2(word[0], word[1]);
+        if ((threadIdx.x & 1) == 0) scales[at >> 1] = static_cast<uint8_t>(k);
+        if (kValues) stg32(values + at * 16, val[0], val[1]);
     }
 }
 
@@ -279,6 +298,26 @@ cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, lo
     uint8_t* scales = out + static_cast<size_t>(rows) * cols / 2;
     const bool vec = (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(up) |
                       (static_cast<uintptr_t>(ld) * sizeof(T))) % 16 == 0;
+    if constexpr (sizeof(T) == 2) {
+        if (up == nullptr && (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(values) |
+                              (static_cast<uintptr_t>(ld) * sizeof(T))) % 32 == 0) {
+            const FastDiv per16(static_cast<uint32_t>(cols / 16));
+            return over_rows(rows, cols / 16, [&](uint32_t row0, uint32_t items) {
+                auto go = [&](auto kernel, uint32_t per_thread) {
+                    const uint32_t per_block = kQThreads * per_thread;
+                    kernel<<<(items + per_block - 1) / per_block, kQThreads, 0, s>>>(
+                        static_cast<const T*>(x), x_rows, ld, row_of, row0, items, per16,
+                        reinterpret_cast<uint2*>(codes), scales, static_cast<T*>(values));
+                    return cudaGetLastError();
+                };
+                // two items a thread where that still leaves several blocks an SM
+                const bool two = items >= 2u * kQThreads * 152u * 8u;
+                if (values != nullptr)
+                    return two ? go(k_mx_quant16<T, 2, true>, 2) : go(k_mx_quant16<T, 1, true>, 1);
+                return two ? go(k_mx_quant16<T, 2, false>, 2) : go(k_mx_quant16<T, 1, false>, 1);
+            });
+        }
+    }
     const FastDiv per_row(static_cast<uint32_t>(cols / 8));
     return over_rows(rows, cols / 8, [&](uint32_t row0, uint32_t items) {
         auto go = [&](auto kernel, uint32_t per_thread) {
@@ -288,24 +327,12 @@ cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, lo
                 row0, items, per_row, codes, scales, static_cast<T*>(values));
             return cudaGetLastError();
         };
-        // two items a thread where that still leaves several blocks an SM
-        const bool two = items >= 2u * kQThreads * 152u * 8u;
         if (up != nullptr)
             return vec ? go(k_mx_quant<T, true, true, 1>, 1) : go(k_mx_quant<T, true, false, 1>, 1);
         if (!vec) return go(k_mx_quant<T, false, false, 1>, 1);
-        if constexpr (sizeof(T) == 2) {
-            auto go16 = [&](auto kernel, uint32_t per_thread) {
-                const uint32_t per_block = kQThreads * per_thread;
-                kernel<<<(items + per_block - 1) / per_block, kQThreads, 0, s>>>(
-                    static_cast<const T*>(x), x_rows, ld, row_of, row0, items, per_row, codes,
-                    scales, static_cast<uint4*>(values));
-                return cudaGetLastError();
-            };
-            if (values != nullptr)
-                return two ? go16(k_mx_quant16<T, 2, true>, 2) : go16(k_mx_quant16<T, 1, true>, 1);
-            return two ? go16(k_mx_quant16<T, 2, false>, 2) : go16(k_mx_quant16<T, 1, false>, 1);
-        } else
-            return two ? go(k_mx_quant<T, false, true, 2>, 2) : go(k_mx_quant<T, false, true, 1>, 1);
+        // two items a thread where that still leaves several blocks an SM
+        return items >= 2u * kQThreads * 152u * 8u ? go(k_mx_quant<T, false, true, 2>, 2)
+                                                   : go(k_mx_quant<T, false, true, 1>, 1);
     });
 }
 
