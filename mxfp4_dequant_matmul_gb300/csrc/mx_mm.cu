@@ -12,13 +12,13 @@
 // elements: one ring stage, four MMAs of K = 64).  Scale bytes lie row-major with a
 // row stride of cols/32 bytes, which no copy engine can turn into the layout the
 // tensor core wants (32 lanes x 16 bytes: byte 4j + b of lane l is group b of row l +
-// 32j), so two warps take them 32 bytes a row (four stages) and store them in that layout,
+// 32j), so warps of their own take them 32 bytes a row (four stages) and store them in that layout,
 // and tcgen05.cp moves them to tensor memory ahead of each stage's MMAs.  A slot of four
 // stages is handed over at a time: the proxy fence and the barriers cost several hundred
 // cycles, more than a stage has when few tokens stream through.
 //
-// Warp 0 issues the copies, warp 1 the MMAs, warps 2 and 3 the scales of W and X, warps
-// 4..7 read finished accumulators (two, in turn) and store them.  Persistent: CTA c
+// One warp issues the copies, one the MMAs, two or three handle the scales, four or eight
+// read finished accumulators (two, in turn) and store them.  Persistent: CTA c
 // takes tiles c, c + grid, ...  With few tokens the tiles are too few to fill the SMs;
 // then a cluster of CTAs shares a tile, each a slice of K, and adds the partial sums
 // through distributed shared memory in rank order.
@@ -46,8 +46,14 @@ namespace cg = cooperative_groups;
 constexpr int kM = 128;                     // weight rows per tile
 constexpr int kK = 256;                     // elements per ring stage: 128 code bytes a row
 constexpr int kGroupsStage = kK / kGroup;   // 8 scale bytes a row
-constexpr int kThreadsMx = 256;
-constexpr int kEpiWarpMx = 4;               // first epilogue warp
+// Warps: copies, MMAs, W's scales, one or two of X's scales, epilogue (each TMEM lane quarter
+// once, or twice: a warp's stores wait for each other, 33 MB of FP32 results took 18.5 us by
+// four warps an SM and 12.4 us by eight).
+template <bool kSplit>
+struct Roles {
+    static constexpr int kEpi = kSplit ? 4 : 5, kEpiWarps = kSplit ? 4 : 8;
+    static constexpr int kThreads = 32 * (kEpi + kEpiWarps);
+};
 constexpr uint32_t kABytes = kM * kK / 2;
 constexpr uint32_t kSfChunk = 512;          // scale bytes of 128 rows x 4 groups
 constexpr int kMaxStages = 10;
@@ -277,16 +283,16 @@ __device__ __forceinline__ void store_scales(const Scales<kAhead>& s, int q, uin
               s.w[2][2 * q + 1], s.w[3][2 * q + 1]);
 }
 
-// 32 outputs (TMEM lanes; `valid` of them exist) of each of n tokens (columns of `src`) to
-// y, tokens `pitch` elements apart.  FP32: a store is one token's 128 bytes.  BF16, even
+// 32 outputs (TMEM lanes; `valid` of them exist) of every other 16 of n tokens (columns of
+// `src`, from c0) to y, tokens `pitch` elements apart.  FP32: a store is one token's 128 bytes.  BF16, even
 // pitch: lanes trade so that each holds four consecutive outputs of four tokens, and a
 // store is four tokens' 64 bytes (a store of two bytes a lane costs as much for a quarter).
 template <typename T>
-__device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int n, uint32_t src,
-                                           int lane) {
+__device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int c0, int n,
+                                           uint32_t src, int lane) {
     if (valid <= 0) return;
     const bool quads = sizeof(T) == 2 && (pitch & 3) == 0 && valid == 32;
-    for (int c = 0; c < n; c += 16) {
+    for (int c = c0; c < n; c += 32) {
         uint32_t v[16];
         tmem_ld16(src + c, v);
         if (quads) {
@@ -327,7 +333,7 @@ __device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int n, ui
 // NB: 128-token blocks of a stage's scales.  Split tiles (few tokens) leave registers for
 // two CTAs on an SM.
 template <typename T, bool kSplit, int NB>
-__global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
+__global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
     k_mx_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
             const MxArgs a, T* __restrict__ Y) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -368,10 +374,10 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], 4);
+            mbar_init(&acc_empty[i], Roles<kSplit>::kEpiWarps);
             mbar_init(&sc_full[i], 1);
-            mbar_init(&sc_empty[i], 2);   // W's and X's scale warps
-            mbar_init(&sf_full[i], 2);
+            mbar_init(&sc_empty[i], 1 + NB);   // W's and X's scale warps
+            mbar_init(&sf_full[i], 1 + NB);
             mbar_init(&sf_empty[i], 1);
         }
         mbar_init(&drain, 1);
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         fence_mbar_init();
     }
     if (a.offsets != nullptr) {
-        for (int e = tid; e <= a.n_experts; e += kThreadsMx)
+        for (int e = tid; e <= a.n_experts; e += Roles<kSplit>::kThreads)
             off[e] = min(max(__ldg(a.offsets + e), 0), a.n_rows);
         __syncthreads();
         if (warp == 0) {   // first[e]: tiles of the experts before e
@@ -595,22 +601,23 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
             mbar_wait_for(&drain, 0u, kWaitMx);
         }
         __syncwarp();
-    } else if (warp < kEpiWarpMx) {
-        // --- scales of W (warp 2) or X (warp 3), loaded four to eight stages ahead of
+    } else if (warp < 3 + NB) {
+        // --- scales of W (warp 2) or of 128 tokens of X (warps 3, 4), loaded four to eight stages ahead of
         // their use and across tiles
         const bool is_w = warp == 2;
-        const int blocks = is_w ? 1 : NB;
-        const uint32_t second = kSfChunk * static_cast<uint32_t>(blocks);
-        const uint32_t slots = smem_u32(sf_buf) + (is_w ? 0u : 2u * kSfChunk);
+        const int block = is_w ? 0 : warp - 3;
+        const uint32_t second = kSfChunk * static_cast<uint32_t>(is_w ? 1 : NB);
+        const uint32_t slots = smem_u32(sf_buf) + (is_w ? 0u : (2u + block) * kSfChunk);
         int f_tile = tile0, f_step = s_lo;   // what to load next
         Tile ft{};
         if (f_tile < n_tiles) ft = tile_at(f_tile, 0);
         int f_count = 0;
         uint32_t group = 0;
         bool ok = true;
-        auto fetch = [&](Scales<kAhead>(&r)[NB]) {
+        auto fetch = [&](Scales<kAhead>& r) {
             if (f_tile >= n_tiles || !ok) return;
             const int row0 = is_w ? ft.r0 : ft.t0, row_end = is_w ? a.rows : ft.t1;
+            const int g0 = f_step * kGroupsStage;
             if (!kSplit && a.n_sc > 0) {
                 const int buf = f_count % 2;
                 if (f_step == 0)
@@ -621,19 +628,11 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
                 const uint8_t* rows = sc_buf + static_cast<size_t>(buf) * a.sc_bytes;
                 if (!is_w)
                     rows += a.sc_w + (static_cast<uint32_t>(static_cast<size_t>(ft.t0) * a.gpr) & 15u);
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if (b < blocks)
-                        load_scales<true>(r[b], rows, a.gpr, f_step * kGroupsStage, 128 * b,
-                                          row_end - row0, lane);
+                load_scales<true>(r, rows, a.gpr, g0, 128 * block, row_end - row0, lane);
             } else {
                 const uint8_t* plane =
                     is_w ? a.w_scales + static_cast<size_t>(ft.e) * a.bank_stride : a.x_scales;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-                    if (b < blocks)
-                        load_scales<false>(r[b], plane, a.gpr, f_step * kGroupsStage,
-                                           row0 + 128 * b, row_end, lane);
+                load_scales<false>(r, plane, a.gpr, g0, row0 + 128 * block, row_end, lane);
             }
             f_step += kAhead;
             if (f_step >= s_hi) {
@@ -647,7 +646,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
                 if (f_tile < n_tiles) ft = tile_at(f_tile, f_count);
             }
         };
-        Scales<kAhead> cur[NB], nxt[NB];
+        Scales<kAhead> cur, nxt;
         fetch(cur);
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead) {
@@ -658,25 +657,20 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
                 if (!ok) break;
 #pragma unroll
                 for (int q = 0; q < kAhead; ++q)   // (stages past the tile's end: not read)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        if (b < blocks)
-                            store_scales(cur[b], q,
-                                         slots + slot * kSfSlot + q * kSfStage + b * kSfChunk, second,
-                                         lane);
+                    store_scales(cur, q, slots + slot * kSfSlot + q * kSfStage, second, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_m(&sf_full[slot]);
                 ++group;
-#pragma unroll
-                for (int b = 0; b < NB; ++b) cur[b] = nxt[b];
+                cur = nxt;
             }
             ok = ok && !*abort_flag;
         }
         if (!ok) fail();
-    } else {
+    } else if (warp >= Roles<kSplit>::kEpi) {
         // --- epilogue
         const int quarter = warp & 3;   // TMEM lanes 32 * quarter .. + 31
+        const int half = (warp - Roles<kSplit>::kEpi) >> 2;
         int j = 0;
         for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
@@ -704,7 +698,7 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
                 }
             } else {
                 store_tile(Y + static_cast<size_t>(t.t0) * a.rows + t.r0 + quarter * 32, a.rows,
-                           min(32, a.rows - t.r0 - quarter * 32), n, src, lane);
+                           min(32, a.rows - t.r0 - quarter * 32), 16 * half, n, src, lane);
             }
             fence_before_mx();
             __syncwarp();
@@ -719,8 +713,8 @@ __global__ void __launch_bounds__(kThreadsMx, kSplit ? 2 : 1)
         const Tile t = tile_at(tile0, 0);
         float* part = reinterpret_cast<float*>(after);
         const int n_out = (t.t1 - t.t0) * kM;
-        for (int i = rank * kThreadsMx + tid; i < n_out && !*abort_flag;
-             i += n_rank * kThreadsMx) {
+        for (int i = rank * Roles<kSplit>::kThreads + tid; i < n_out && !*abort_flag;
+             i += n_rank * Roles<kSplit>::kThreads) {
             const int r = t.r0 + (i & (kM - 1)), tok = t.t0 + i / kM;
             float sum = 0.0f;
             for (int q = 0; q < n_rank; ++q) sum += cluster.map_shared_rank(part, q)[i];
@@ -808,7 +802,7 @@ cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxA
     if (attr_err != cudaSuccess) return attr_err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreadsMx);
+    cfg.blockDim = dim3(Roles<kSplit>::kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
