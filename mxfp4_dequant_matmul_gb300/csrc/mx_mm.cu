@@ -46,12 +46,17 @@ namespace cg = cooperative_groups;
 constexpr int kM = 128;                     // weight rows per tile
 constexpr int kK = 256;                     // elements per ring stage: 128 code bytes a row
 constexpr int kGroupsStage = kK / kGroup;   // 8 scale bytes a row
-// Warps: copies, MMAs, W's scales, one or two of X's scales, epilogue (each TMEM lane quarter
-// once, or twice: a warp's stores wait for each other, 33 MB of FP32 results took 18.5 us by
-// four warps an SM and 12.4 us by eight).
+// Warps.  0: copies (of W alone when unsplit), 1: MMAs, 2: W's scales, 3 and 4: X's scales
+// (128 tokens each; 4 unused when split or with one block), 5 and 6 (unsplit): copies of X,
+// scales to tensor memory.  A role is one warp's chain of waits and issues, several hundred
+// cycles a stage, so an unsplit CTA spreads them: one copy warp and one warp for scales and
+// MMAs were both busy all the time and held a prompt's experts at 72 us.  Then the epilogue,
+// each TMEM lane quarter once, or twice: a warp's stores wait for each other, 33 MB of FP32
+// results took 18.5 us by four warps an SM and 12.4 us by eight.
 template <bool kSplit>
 struct Roles {
-    static constexpr int kEpi = kSplit ? 4 : 5, kEpiWarps = kSplit ? 4 : 8;
+    static constexpr int kCopyX = 5, kToTmem = 6;
+    static constexpr int kEpi = kSplit ? 4 : 7, kEpiWarps = kSplit ? 4 : 8;
     static constexpr int kThreads = 32 * (kEpi + kEpiWarps);
 };
 constexpr uint32_t kABytes = kM * kK / 2;
@@ -64,7 +69,7 @@ constexpr long long kWaitMx = 1ll << 32, kDrainMx = 1ll << 24;   // SM cycles: a
 __device__ int g_fault_mx;
 
 // One launch's shape.  tn: most tokens of a tile (a multiple of 16); box: token rows of
-// one TMA copy (divides the stage's token rows); n_acc accumulators of tn columns.
+// one TMA copy (divides the stage's token rows).
 struct MxArgs {
     const uint8_t* w_scales;      // scale plane of expert 0
     size_t bank_stride;
@@ -72,7 +77,7 @@ struct MxArgs {
     const int32_t* offsets;       // nullptr: one matrix
     int n_experts, rows, gpr, n_rows;
     int n_steps;                  // ring stages per tile
-    int tn, box, n_stages, n_acc;
+    int tn, box, n_stages;
     uint32_t stage_bytes, tmem_cols;
     int n_sc;                     // 2 tile buffers of scale rows, or 0: loaded from global memory
     uint32_t sc_w, sc_bytes;      // bytes of W's rows in a buffer, of a buffer
@@ -142,6 +147,14 @@ __device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
                  : "memory");
 }
 
+// A stage's scales: two chunks of W, then two times NB of X.
+template <int NB>
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
+#pragma unroll
+    for (uint32_t i = 0; i < 2u * (1 + NB); ++i)
+        cp_scales(taddr + 4u * i, desc + i * (kSfChunk >> 4));
+}
+
 __device__ __forceinline__ void umma_commit_mx(uint64_t* bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -162,6 +175,19 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(p));
     return p != 0;
+}
+
+// One poll that does not suspend.  Its answer takes about a hundred cycles: a role asks
+// about its next stage before it issues the current one.
+__device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 // Wait for the phase with the given parity, for at most `cycles` SM cycles (a poll may
@@ -333,7 +359,7 @@ __device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int c0, i
 // NB: 128-token blocks of a stage's scales.  Split tiles (few tokens) leave registers for
 // two CTAs on an SM.
 template <typename T, bool kSplit, int NB>
-__global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
+__global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     k_mx_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
             const MxArgs a, T* __restrict__ Y) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -341,6 +367,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint64_t sc_full[2], sc_empty[2], sf_full[2], sf_empty[2];
+    __shared__ uint64_t in_tmem[kMaxStages];   // (unsplit) a stage's scales are in tensor memory
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word, n_tiles_sh;
     __shared__ Tile table[kTileTable];
@@ -360,6 +387,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
     const int rank = kSplit ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
     const int n_rank = kSplit ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
 
+    constexpr int kCopiers = kSplit ? 1 : 2;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_base)),
@@ -369,13 +397,14 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
     }
     if (tid == 0) {
         for (int i = 0; i < a.n_stages; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], kCopiers);
+            mbar_init(&in_tmem[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], Roles<kSplit>::kEpiWarps);
-            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_full[i], kCopiers);
             mbar_init(&sc_empty[i], 1 + NB);   // W's and X's scale warps
             mbar_init(&sf_full[i], 1 + NB);
             mbar_init(&sf_empty[i], 1);
@@ -425,7 +454,8 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
                : a.n_steps;
     const int tile0 = kSplit ? static_cast<int>(blockIdx.x) / n_rank : static_cast<int>(blockIdx.x);
     const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x);   // (split: one tile)
-    const uint32_t sf_cols = tmem + a.n_acc * a.tn;
+    constexpr int kAcc = kSplit ? 1 : 2;   // accumulators, of tn columns each
+    const uint32_t sf_cols = tmem + kAcc * a.tn;
     constexpr uint32_t sf_stage = 8u + 8u * NB;   // TMEM columns of a stage's scales
 
     // A tile's token tiles come first, so that the weights of a row tile are read again
@@ -468,7 +498,8 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
     };
     int issued = 0, sc_issued = 0;   // (warp 0) stages and scale buffers started
 
-    if (warp == 0) {
+    if (warp == 0 || (!kSplit && warp == Roles<kSplit>::kCopyX)) {
+        const bool do_w = warp == 0, do_x = kSplit || warp != 0;
         // --- copies (the whole warp walks, one elected lane issues: as for the MMAs)
         const bool leader = elect_one();
         const uint64_t keep = l2_evict_last();
@@ -479,7 +510,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
         const uint32_t ring = smem_u32(smem);
         uint32_t st = 0, phase = 1;   // phase of the empty barriers: the first round passes at once
         int j = 0;
-        bool ok = true;
+        bool ok = true, ready = false;
         // a tile's scale rows, contiguous in both planes, one tile ahead of its codes
         auto copy_scales = [&](const Tile& t) {
             const int b = sc_issued % 2;
@@ -494,10 +525,12 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
             const uint32_t wb =
                 (static_cast<uint32_t>(min(kM, a.rows - t.r0) * a.gpr) + 15u) & ~15u;
             const uint32_t xb = (skew + static_cast<uint32_t>((t.t1 - t.t0) * a.gpr) + 15u) & ~15u;
-            if (leader) {
-                mbar_arrive_expect_tx(&sc_full[b], wb + xb);
+            if (leader && do_w) {
+                mbar_arrive_expect_tx(&sc_full[b], wb);
                 bulk_g2s(dst, a.w_scales + static_cast<size_t>(t.e) * a.bank_stride + w_at, wb,
                          &sc_full[b], w_policy);
+            } else if (leader) {
+                mbar_arrive_expect_tx(&sc_full[b], xb);
                 bulk_g2s(dst + a.sc_w, a.x_scales + (x_at - skew), xb, &sc_full[b], keep);
             }
             __syncwarp();
@@ -508,23 +541,26 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
             const Tile t = tile_at(tile, j);
             const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
             const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
-            const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box) * box_bytes;
+            const uint32_t bytes =
+                (do_w ? kABytes : 0u) + (do_x ? static_cast<uint32_t>(n_box) * box_bytes : 0u);
             for (int s = s_lo; s < s_hi; ++s, ++issued) {
-                ok = mbar_wait_for(&empty[st], phase, kWaitMx);
+                ok = ready || mbar_wait_for(&empty[st], phase, kWaitMx);
                 if (!ok) break;
-                const uint32_t dst = ring + st * a.stage_bytes;
-                if (leader) {
-                    mbar_arrive_expect_tx(&full[st], bytes);
-                    tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[st], w_policy);
-                    for (int b = 0; b < n_box; ++b)
-                        tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
-                              s * (kK / 2), t.t0 + b * a.box, &full[st], keep);
-                }
-                __syncwarp();
+                const uint32_t dst = ring + st * a.stage_bytes, now = st;
                 if (++st == static_cast<uint32_t>(a.n_stages)) {
                     st = 0;
                     phase ^= 1u;
                 }
+                ready = mbar_ready(&empty[st], phase);
+                if (leader) {
+                    mbar_arrive_expect_tx(&full[now], bytes);
+                    if (do_w) tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[now], w_policy);
+                    if (do_x)
+                        for (int b = 0; b < n_box; ++b)
+                            tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
+                                  s * (kK / 2), t.t0 + b * a.box, &full[now], keep);
+                }
+                __syncwarp();
                 if (s == s_lo && a.n_sc > 0 && tile + tile_step < n_tiles) {
                     ok = copy_scales(tile_at(tile + tile_step, j + 1));
                     if (!ok) break;
@@ -544,53 +580,52 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
         const uint32_t stage16 = a.stage_bytes >> 4;   // descriptors count 16 bytes
         uint32_t st = 0, phase = 0, group = 0;   // group: kAhead stages sharing a scale slot
         int j = 0;
-        bool ok = true;
+        bool ok = true, ready = false, sf_ready = false;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
             const int n = __shfl_sync(0xFFFFFFFFu, (t.t1 - t.t0 + 15) & ~15, 0);
             const uint32_t id0 = idesc_mxf4(n, 0u), id2 = idesc_mxf4(n, 2u);
-            const int ab = j % a.n_acc;
-            if (j >= a.n_acc)
-                ok = mbar_wait_for(&acc_empty[ab], static_cast<uint32_t>(j / a.n_acc - 1) & 1u,
+            const int ab = j % kAcc;
+            if (j >= kAcc)
+                ok = mbar_wait_for(&acc_empty[ab], static_cast<uint32_t>(j / kAcc - 1) & 1u,
                                kWaitMx);
             fence_after_mx();
             const uint32_t d = tmem + ab * a.tn;
             for (int s = s_lo; s < s_hi && ok; ++s) {
                 const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
-                if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
-                ok = ok && mbar_wait_for(&full[st], phase, kWaitMx);
+                if (!kSplit)
+                    ok = sf_ready || mbar_wait_for(&in_tmem[st], phase, kWaitMx);
+                else if (q == 0)
+                    ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
+                ok = ok && (ready || mbar_wait_for(&full[st], phase, kWaitMx));
                 if (!ok) break;
                 fence_after_mx();
-                const uint32_t sfa = sf_cols + st * sf_stage, sfb = sfa + 8u;
-                const uint64_t ad = op0 + st * stage16, bd = ad + (kABytes >> 4);
+                const uint32_t now = st;
+                if (++st == static_cast<uint32_t>(a.n_stages)) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+                ready = mbar_ready(&full[st], phase);
+                if (!kSplit) sf_ready = mbar_ready(&in_tmem[st], phase);
+                const uint32_t sfa = sf_cols + now * sf_stage, sfb = sfa + 8u;
+                const uint64_t ad = op0 + now * stage16, bd = ad + (kABytes >> 4);
                 const uint64_t sd = sf0 + ((slot * kSfSlot + q * kSfStage) >> 4);
                 const bool last = q == kAhead - 1 || s + 1 == s_hi;
                 const uint32_t more = s > s_lo ? 1u : 0u;
                 // K = 64 at a time; the last stage of a row may hold fewer
                 const int kk_end = (a.gpr - s * kGroupsStage + 1) / 2;
                 if (leader) {
-                    cp_scales(sfa, sd);
-                    cp_scales(sfa + 4u, sd + (kSfChunk >> 4));
-                    cp_scales(sfb, sd + 2 * (kSfChunk >> 4));
-                    cp_scales(sfb + 4u, sd + 3 * (kSfChunk >> 4));
-                    if (NB == 2) {
-                        cp_scales(sfb + 8u, sd + 4 * (kSfChunk >> 4));
-                        cp_scales(sfb + 12u, sd + 5 * (kSfChunk >> 4));
-                    }
+                    if (kSplit) scales_to_tmem<NB>(sfa, sd);
                     const uint32_t sfb2 = sfb + 4u * NB;
                     umma_mxf4(d, ad, bd, id0, sfa, sfb, more);
                     if (kk_end > 1) umma_mxf4(d, ad + 2, bd + 2, id2, sfa, sfb, 1u);
                     if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
                     if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
-                    umma_commit_mx(&empty[st]);
-                    if (last) umma_commit_mx(&sf_empty[slot]);
+                    umma_commit_mx(&empty[now]);
+                    if (kSplit && last) umma_commit_mx(&sf_empty[slot]);
                 }
                 __syncwarp();
                 group += last ? 1u : 0u;
-                if (++st == static_cast<uint32_t>(a.n_stages)) {
-                    st = 0;
-                    phase ^= 1u;
-                }
             }
             if (ok && leader) umma_commit_mx(&acc_full[ab]);
             ok = ok && !*abort_flag;
@@ -601,7 +636,38 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
             mbar_wait_for(&drain, 0u, kWaitMx);
         }
         __syncwarp();
-    } else if (warp < 3 + NB) {
+    } else if (!kSplit && warp == Roles<kSplit>::kToTmem) {
+        // --- scales from shared to tensor memory, as far ahead as the ring goes
+        const bool leader = elect_one();
+        const uint64_t sf0 = scale_desc(smem_u32(sf_buf));
+        uint32_t st = 0, phase = 1, group = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
+            for (int s = s_lo; s < s_hi; ++s) {
+                const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
+                if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
+                ok = ok && mbar_wait_for(&empty[st], phase, kWaitMx);
+                if (!ok) break;
+                fence_after_mx();
+                const bool last = q == kAhead - 1 || s + 1 == s_hi;
+                if (leader) {
+                    scales_to_tmem<NB>(sf_cols + st * sf_stage,
+                                       sf0 + ((slot * kSfSlot + q * kSfStage) >> 4));
+                    umma_commit_mx(&in_tmem[st]);
+                    if (last) umma_commit_mx(&sf_empty[slot]);
+                }
+                __syncwarp();
+                group += last ? 1u : 0u;
+                if (++st == static_cast<uint32_t>(a.n_stages)) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+            ok = ok && !*abort_flag;
+        }
+        if (!ok) fail();
+        __syncwarp();
+    } else if (warp >= 2 && warp < 3 + NB) {
         // --- scales of W (warp 2) or of 128 tokens of X (warps 3, 4), loaded four to eight stages ahead of
         // their use and across tiles
         const bool is_w = warp == 2;
@@ -674,9 +740,9 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 2 : 1)
         int j = 0;
         for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
-            const int ab = j % a.n_acc;
+            const int ab = j % kAcc;
             if (!__all_sync(0xFFFFFFFFu,
-                            mbar_wait_for(&acc_full[ab], static_cast<uint32_t>(j / a.n_acc) & 1u,
+                            mbar_wait_for(&acc_full[ab], static_cast<uint32_t>(j / kAcc) & 1u,
                                       kWaitMx))) {
                 fail();
                 break;
@@ -872,7 +938,7 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     }
     const int sf_blocks = (a.tn + 127) / 128;
     a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * 128u;
-    a.n_acc = split > 1 ? 1 : 2;
+    const int n_acc = split > 1 ? 1 : 2;
     const size_t sf_bytes = 2u * (split > 1 ? 2 : 4) * 2u * kSfChunk * (1 + sf_blocks);
     const size_t extra = sf_bytes + (split > 1 ? static_cast<size_t>(a.tn) * kM * 4
                                    : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0);
@@ -886,8 +952,8 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     a.n_stages = std::min(kMaxStages, static_cast<int>(budget / a.stage_bytes));
     if (split > 1) a.n_stages = std::min(a.n_stages, (a.n_steps + 1) / 2 / split * 2 + 2);
     const int sf_cols = 8 + 8 * sf_blocks;
-    a.n_stages = std::min(a.n_stages, (512 / (split > 1 ? per_sm : 1) - a.n_acc * a.tn) / sf_cols);
-    a.tmem_cols = tmem_columns(a.n_acc * a.tn + a.n_stages * sf_cols);
+    a.n_stages = std::min(a.n_stages, (512 / (split > 1 ? per_sm : 1) - n_acc * a.tn) / sf_cols);
+    a.tmem_cols = tmem_columns(n_acc * a.tn + a.n_stages * sf_cols);
     if (a.n_stages < 1) return cudaErrorNotSupported;
     // A CTA that waits for tensor memory must not hold up a cluster: an unsplit CTA takes
     // its SM's whole shared memory (and all 512 columns), and a split CTA at least 40 KB,
