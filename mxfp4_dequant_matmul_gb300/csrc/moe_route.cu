@@ -19,6 +19,7 @@
 #include "elem.cuh"
 #include "kernels.h"
 #include "mx4_kernels.h"
+#include "pdl.cuh"
 
 namespace mxk {
 namespace {
@@ -32,6 +33,8 @@ __global__ void __launch_bounds__(kSortThreads)
     k_moe_sort(const int32_t* __restrict__ ids, int n_pairs, int top_k, int n_experts, int run,
                int32_t* __restrict__ token_at, int32_t* __restrict__ pos_of,
                int32_t* __restrict__ offsets) {
+    pdl_trigger();
+    pdl_wait();
     extern __shared__ int32_t sort_smem[];
     const int threads = static_cast<int>(blockDim.x), warps = threads >> 5;
     int32_t* total = sort_smem;              // [n_experts], read by the cluster
@@ -148,6 +151,8 @@ template <typename P, int kU>
 __global__ void __launch_bounds__(kRThreads)
     k_moe_dispatch(const P* __restrict__ x, int n_tokens, uint32_t row0, uint32_t units,
                    FastDiv per_row, const int32_t* __restrict__ token_at, P* __restrict__ xs) {
+    pdl_trigger();
+    pdl_wait();
     P v[kU];
     const uint32_t i0 = blockIdx.x * (kRThreads * kU) + threadIdx.x;
 #pragma unroll
@@ -173,6 +178,8 @@ __global__ void __launch_bounds__(kRThreads)
     k_moe_gather_sum(const Pack<T, N>* __restrict__ o, int n_rows, int top_k, uint32_t row0,
                      uint32_t units, FastDiv per_row, const int32_t* __restrict__ pos_of,
                      const float* __restrict__ w, Pack<T, N>* __restrict__ y) {
+    pdl_trigger();
+    pdl_wait();
     const uint32_t i0 = blockIdx.x * (kRThreads * kU) + threadIdx.x;
     float acc[kU][N] = {};
     for (int j0 = 0; j0 < top_k; j0 += 4) {
@@ -221,6 +228,8 @@ __global__ void
                        int n_rows, int top_k, int per_row, const int32_t* __restrict__ pos_of,
                        const float* __restrict__ w, Pack<T, N>* __restrict__ d_o,
                        float* __restrict__ d_w) {
+    pdl_trigger();
+    pdl_wait();
     __shared__ float part[4][32];
     const size_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -320,21 +329,10 @@ cudaError_t launch_moe_sort(const int32_t* ids, int n_pairs, int top_k, int n_ex
     const int warps = std::min(kSortWarps, std::max(4, (n_pairs + 32 * n_cta - 1) / (32 * n_cta)));
     const int run = (n_pairs + n_cta * warps * 32 - 1) / (n_cta * warps * 32) * 32;
     const size_t smem = static_cast<size_t>(warps + 2) * n_experts * sizeof(int32_t);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(n_cta));
-    cfg.blockDim = dim3(static_cast<unsigned>(warps * 32));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(n_cta);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_moe_sort, ids, n_pairs, top_k, n_experts, run,
-                                             token_at, pos_of, offsets);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_after(k_moe_sort, dim3(static_cast<unsigned>(n_cta)),
+                        static_cast<unsigned>(warps * 32), smem, s,
+                        static_cast<unsigned>(n_cta), ids, n_pairs, top_k, n_experts, run,
+                        token_at, pos_of, offsets);
 }
 
 cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_rows, int width,
@@ -347,12 +345,10 @@ cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_row
             const P* xp = static_cast<const P*>(x);
             P* out = static_cast<P*>(xs);
             if (many_units(units))
-                k_moe_dispatch<P, 4><<<blocks_of(units, 4), kRThreads, 0, s>>>(
-                    xp, n_tokens, row0, units, div, token_at, out);
-            else
-                k_moe_dispatch<P, 1><<<blocks_of(units, 1), kRThreads, 0, s>>>(
-                    xp, n_tokens, row0, units, div, token_at, out);
-            return cudaGetLastError();
+                return launch_after(k_moe_dispatch<P, 4>, dim3(blocks_of(units, 4)), kRThreads, 0, s, 1,
+                                    xp, n_tokens, row0, units, div, token_at, out);
+            return launch_after(k_moe_dispatch<P, 1>, dim3(blocks_of(units, 1)), kRThreads, 0, s, 1,
+                                    xp, n_tokens, row0, units, div, token_at, out);
         });
     });
 }
@@ -369,12 +365,12 @@ cudaError_t launch_moe_gather_sum(const void* o, int type, int n_tokens, int top
             const P* in = static_cast<const P*>(o);
             P* out = static_cast<P*>(y);
             if (many_units(units))
-                k_moe_gather_sum<T, kN, 2><<<blocks_of(units, 2), kRThreads, 0, s>>>(
-                    in, n_tokens * top_k, top_k, row0, units, div, pos_of, route_w, out);
-            else
-                k_moe_gather_sum<T, kN, 1><<<blocks_of(units, 1), kRThreads, 0, s>>>(
-                    in, n_tokens * top_k, top_k, row0, units, div, pos_of, route_w, out);
-            return cudaGetLastError();
+                return launch_after(k_moe_gather_sum<T, kN, 2>, dim3(blocks_of(units, 2)), kRThreads, 0,
+                                    s, 1, in, n_tokens * top_k, top_k, row0, units, div, pos_of,
+                                    route_w, out);
+            return launch_after(k_moe_gather_sum<T, kN, 1>, dim3(blocks_of(units, 1)), kRThreads, 0,
+                                    s, 1, in, n_tokens * top_k, top_k, row0, units, div, pos_of,
+                                    route_w, out);
         });
     });
 }
@@ -389,10 +385,10 @@ cudaError_t launch_moe_combine_grad(const void* dy, const void* o, int type, int
         using T = typename P::Elem;
         const int per_row = width / kN;
         const int threads = std::min(512, std::max(128, (per_row + 31) / 32 * 32));
-        k_moe_combine_grad<T, kN><<<static_cast<unsigned>(n_tokens), threads, 0, s>>>(
-            static_cast<const P*>(dy), static_cast<const P*>(o), n_tokens * top_k, top_k, per_row,
-            pos_of, route_w, static_cast<P*>(d_o), d_route_w);
-        return cudaGetLastError();
+        return launch_after(k_moe_combine_grad<T, kN>, dim3(static_cast<unsigned>(n_tokens)),
+                            static_cast<unsigned>(threads), 0, s, 1, static_cast<const P*>(dy),
+                            static_cast<const P*>(o), n_tokens * top_k, top_k, per_row, pos_of,
+                            route_w, static_cast<P*>(d_o), d_route_w);
     });
 }
 

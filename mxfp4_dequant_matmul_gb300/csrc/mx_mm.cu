@@ -37,6 +37,7 @@
 #include "elem.cuh"
 #include "kernels.h"
 #include "mx4_kernels.h"
+#include "pdl.cuh"
 
 namespace mxk {
 namespace {
@@ -414,6 +415,17 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         n_tiles_sh = a.n_rt * a.n_tt;
         fence_mbar_init();
     }
+    if (tid == 32 * 2) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&wmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+    }
+    fence_before_mx();
+    __syncthreads();
+    fence_after_mx();
+    // the next launch may be placed now that this CTA has its tensor memory (a CTA of the
+    // next one that waits for columns then waits for CTAs that need nothing more)
+    pdl_trigger();
+    pdl_wait();
     if (a.offsets != nullptr) {
         for (int e = tid; e <= a.n_experts; e += Roles<kSplit>::kThreads)
             off[e] = min(max(__ldg(a.offsets + e), 0), a.n_rows);
@@ -440,9 +452,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
             }
         }
     }
-    fence_before_mx();
     __syncthreads();
-    fence_after_mx();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
     const int n_tiles = __shfl_sync(0xFFFFFFFFu, n_tiles_sh, 0);
     // (split) slices of whole pairs of stages, so that 16-byte scale loads stay aligned
@@ -866,20 +876,9 @@ cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxA
                                                      static_cast<int>(kSmemMax - kSmemSlack)));
     }));
     if (attr_err != cudaSuccess) return attr_err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(Roles<kSplit>::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = kSplit ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, k_mx_mm<T, kSplit, NB>, wmap, xmap, a, Y);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_after(k_mx_mm<T, kSplit, NB>, dim3(grid),
+                        static_cast<unsigned>(Roles<kSplit>::kThreads), smem, s, cluster, wmap,
+                        xmap, a, Y);
 }
 
 uint32_t tmem_columns(int need) {

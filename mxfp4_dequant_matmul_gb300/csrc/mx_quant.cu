@@ -18,6 +18,7 @@
 #include "elem.cuh"
 #include "kernels.h"
 #include "mx4_kernels.h"
+#include "pdl.cuh"
 
 namespace mxk {
 namespace {
@@ -109,6 +110,8 @@ __global__ void __launch_bounds__(kQThreads)
                const int32_t* __restrict__ row_of, float limit, uint32_t row0, uint32_t items,
                FastDiv per_row, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
                T* __restrict__ values) {
+    pdl_trigger();
+    pdl_wait();
     const uint32_t i0 = blockIdx.x * (kQThreads * kU) + threadIdx.x;
     const size_t first = static_cast<size_t>(row0) * per_row.d;   // items of earlier launches
     float v[kU][8];
@@ -239,6 +242,8 @@ __global__ void __launch_bounds__(kQThreads)
                  const int32_t* __restrict__ row_of, uint32_t row0, uint32_t items,
                  FastDiv per_row, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                  T* __restrict__ values) {
+    pdl_trigger();
+    pdl_wait();
     const uint32_t i0 = blockIdx.x * (kQThreads * kU) + threadIdx.x;
     const size_t first = static_cast<size_t>(row0) * per_row.d + i0;
     uint32_t raw[kU][8];
@@ -305,10 +310,11 @@ cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, lo
             return over_rows(rows, cols / 16, [&](uint32_t row0, uint32_t items) {
                 auto go = [&](auto kernel, uint32_t per_thread) {
                     const uint32_t per_block = kQThreads * per_thread;
-                    kernel<<<(items + per_block - 1) / per_block, kQThreads, 0, s>>>(
-                        static_cast<const T*>(x), x_rows, ld, row_of, row0, items, per16,
-                        reinterpret_cast<uint2*>(codes), scales, static_cast<T*>(values));
-                    return cudaGetLastError();
+                    return launch_after(kernel, dim3((items + per_block - 1) / per_block),
+                                        kQThreads, 0, s, 1, static_cast<const T*>(x), x_rows, ld,
+                                        row_of, row0, items, per16,
+                                        reinterpret_cast<uint2*>(codes), scales,
+                                        static_cast<T*>(values));
                 };
                 // two items a thread where that still leaves several blocks an SM
                 const bool two = items >= 2u * kQThreads * 152u * 8u;
@@ -322,10 +328,10 @@ cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, lo
     return over_rows(rows, cols / 8, [&](uint32_t row0, uint32_t items) {
         auto go = [&](auto kernel, uint32_t per_thread) {
             const uint32_t per_block = kQThreads * per_thread;
-            kernel<<<(items + per_block - 1) / per_block, kQThreads, 0, s>>>(
-                static_cast<const T*>(x), static_cast<const T*>(up), x_rows, ld, row_of, limit,
-                row0, items, per_row, codes, scales, static_cast<T*>(values));
-            return cudaGetLastError();
+            return launch_after(kernel, dim3((items + per_block - 1) / per_block), kQThreads, 0, s,
+                                1, static_cast<const T*>(x), static_cast<const T*>(up), x_rows, ld,
+                                row_of, limit, row0, items, per_row, codes, scales,
+                                static_cast<T*>(values));
         };
         if (up != nullptr)
             return vec ? go(k_mx_quant<T, true, true, 1>, 1) : go(k_mx_quant<T, true, false, 1>, 1);
