@@ -927,8 +927,13 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
                 }
             }
         } else {
-            // few tokens: slices of K over a cluster until the SMs are full twice over
-            while (split < 8 && a.n_rt * split * 2 <= 2 * sms && a.n_steps / (split * 2) >= 2)
+            // few tokens, and row tiles for less than two thirds of the SMs: slices of K over a
+            // cluster, as many as two CTAs an SM hold (us, one token unless said: 4096x4096
+            // 8.0 unsplit, 6.2 split by 4, 6.0 by 8; 2880x2880, 4 tokens 7.4, 6.8, 5.9;
+            // 8192x8192, 16 tokens 12.6, 10.7 by 4, 16.2 by 8; with 112 row tiles, 14336x4096,
+            // 8.4 unsplit, 9.4 by 2)
+            while (split < 8 && 3 * a.n_rt < 2 * sms && a.n_rt * split * 2 <= 2 * sms &&
+                   split * 2 <= a.n_steps)
                 split *= 2;
             per_sm = std::min(4, (a.n_rt * split + sms - 1) / sms);
         }
