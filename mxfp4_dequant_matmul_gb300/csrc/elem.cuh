@@ -26,8 +26,11 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// N consecutive elements moved as one access (N * sizeof(T) = 2, 4, 8 or 16 bytes).  The
+// N consecutive elements moved as one access (N * sizeof(T) = 2, 4, 8, 16 or 32 bytes).  The
 // bits are held as integers: copies of element structs come out element by element.
+struct alignas(32) Raw32 {
+    uint32_t w[8];
+};
 template <int kBytes>
 struct RawOf;
 template <>
@@ -38,6 +41,8 @@ template <>
 struct RawOf<8> { using type = uint2; };
 template <>
 struct RawOf<16> { using type = uint4; };
+template <>
+struct RawOf<32> { using type = Raw32; };
 
 template <typename T, int N>
 struct Pack {
@@ -55,6 +60,31 @@ struct Pack {
         for (int i = 0; i < N; ++i) e[i] = from_f32<T>(f[i]);
     }
 };
+
+// One load or store of a pack; data that is read once does not stay in L1.
+template <typename P>
+__device__ __forceinline__ P load_pack(const P* p) {
+    P v;
+    if constexpr (sizeof(P) == 32) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v.raw.w[0]), "=r"(v.raw.w[1]), "=r"(v.raw.w[2]), "=r"(v.raw.w[3]),
+                       "=r"(v.raw.w[4]), "=r"(v.raw.w[5]), "=r"(v.raw.w[6]), "=r"(v.raw.w[7])
+                     : "l"(p));
+    } else {
+        v.raw = __ldg(&p->raw);
+    }
+    return v;
+}
+template <typename P>
+__device__ __forceinline__ void store_pack(P* p, const P& v) {
+    if constexpr (sizeof(P) == 32)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v.raw.w[0]),
+                     "r"(v.raw.w[1]), "r"(v.raw.w[2]), "r"(v.raw.w[3]), "r"(v.raw.w[4]),
+                     "r"(v.raw.w[5]), "r"(v.raw.w[6]), "r"(v.raw.w[7])
+                     : "memory");
+    else
+        p->raw = v.raw;
+}
 
 // i / d for 0 <= i < 2^32 as one multiplication (Granlund & Montgomery 1994): m =
 // ceil(2^(32 + s) / d) with s = ceil(log2 d), one bit more than 32 bits hold.

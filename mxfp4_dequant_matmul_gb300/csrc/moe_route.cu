@@ -27,6 +27,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;   // at most
+constexpr int kMaxExperts = 1024;
 constexpr int kSortCluster = 8;
 
 __global__ void __launch_bounds__(kSortThreads)
@@ -67,12 +68,13 @@ __global__ void __launch_bounds__(kSortThreads)
     __syncthreads();
     // per expert: exclusive sums over the warps, and the CTA's total
     for (int e = tid; e < n_experts; e += threads) {
-        int32_t sum = 0;
-#pragma unroll 8
-        for (int w = 0; w < warps; ++w) {
-            const int32_t c = hist[w * n_experts + e];
-            hist[w * n_experts + e] = sum;
-            sum += c;
+        int32_t c[kSortWarps], sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) c[w] = w < warps ? hist[w * n_experts + e] : 0;
+#pragma unroll
+        for (int w = 0; w < kSortWarps; ++w) {
+            if (w < warps) hist[w * n_experts + e] = sum;
+            sum += c[w];
         }
         total[e] = sum;
     }
@@ -158,66 +160,61 @@ __global__ void __launch_bounds__(kRThreads)
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         const uint32_t i = i0 + u * kRThreads;
-        v[u].raw = {};
-        if (i >= units) continue;
         const uint32_t row = per_row.of(i);
-        const int t = __ldg(token_at + row0 + row);
+        const int t = i < units ? __ldg(token_at + row0 + row) : -1;
+        v[u].raw = {};
         if (t >= 0 && t < n_tokens)
-            v[u] = x[static_cast<size_t>(t) * per_row.d + (i - row * per_row.d)];
+            v[u] = load_pack(x + static_cast<size_t>(t) * per_row.d + (i - row * per_row.d));
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
         const uint32_t i = i0 + u * kRThreads;
-        if (i < units) xs[static_cast<size_t>(row0) * per_row.d + i] = v[u];
+        if (i < units) store_pack(xs + static_cast<size_t>(row0) * per_row.d + i, v[u]);
     }
 }
 
-// y[t] = sum_j w[t][j] o[pos_of[t][j]] (w == nullptr: 1), four pairs' loads in flight.
-template <typename T, int N, int kU>
+// y[t] = sum_j w[t][j] o[pos_of[t][j]] (w == nullptr: 1): one unit a thread, four pairs'
+// rows in flight.
+template <typename T, int N>
 __global__ void __launch_bounds__(kRThreads)
     k_moe_gather_sum(const Pack<T, N>* __restrict__ o, int n_rows, int top_k, uint32_t row0,
                      uint32_t units, FastDiv per_row, const int32_t* __restrict__ pos_of,
                      const float* __restrict__ w, Pack<T, N>* __restrict__ y) {
     pdl_trigger();
     pdl_wait();
-    const uint32_t i0 = blockIdx.x * (kRThreads * kU) + threadIdx.x;
-    float acc[kU][N] = {};
+    const uint32_t i = blockIdx.x * kRThreads + threadIdx.x;
+    if (i >= units) return;
+    const uint32_t row = per_row.of(i), c = i - row * per_row.d;
+    const size_t p0 = (static_cast<size_t>(row0) + row) * top_k;
+    float acc[N] = {};
     for (int j0 = 0; j0 < top_k; j0 += 4) {
-        Pack<T, N> v[kU][4];
-        float wt[kU][4];
+        int pos[4];
+        float wt[4];
+        Pack<T, N> v[4];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const uint32_t i = i0 + u * kRThreads;
-            const uint32_t row = per_row.of(i), c = i - row * per_row.d;
-            const size_t p = (static_cast<size_t>(row0) + row) * top_k + j0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                wt[u][j] = 0.0f;
-                v[u][j].raw = {};
-                if (i >= units || j0 + j >= top_k) continue;
-                const int pos = __ldg(pos_of + p + j);
-                if (pos < 0 || pos >= n_rows) continue;
-                wt[u][j] = w != nullptr ? __ldg(w + p + j) : 1.0f;
-                v[u][j] = o[static_cast<size_t>(pos) * per_row.d + c];
-            }
+        for (int j = 0; j < 4; ++j) {
+            const bool in = j0 + j < top_k;
+            pos[j] = in ? __ldg(pos_of + p0 + j0 + j) : -1;
+            wt[j] = in && w != nullptr ? __ldg(w + p0 + j0 + j) : 1.0f;
         }
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
+        for (int j = 0; j < 4; ++j) {
+            const bool in = pos[j] >= 0 && pos[j] < n_rows;
+            if (!in) wt[j] = 0.0f;
+            v[j].raw = {};
+            if (in) v[j] = load_pack(o + static_cast<size_t>(pos[j]) * per_row.d + c);
+        }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float f[N];
-                v[u][j].get(f);
+        for (int j = 0; j < 4; ++j) {
+            float f[N];
+            v[j].get(f);
 #pragma unroll
-                for (int q = 0; q < N; ++q) acc[u][q] = fmaf(wt[u][j], f[q], acc[u][q]);
-            }
+            for (int q = 0; q < N; ++q) acc[q] = fmaf(wt[j], f[q], acc[q]);
+        }
     }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        const uint32_t i = i0 + u * kRThreads;
-        Pack<T, N> r;
-        r.set(acc[u]);
-        if (i < units) y[static_cast<size_t>(row0) * per_row.d + i] = r;
-    }
+    Pack<T, N> r;
+    r.set(acc);
+    store_pack(y + static_cast<size_t>(row0) * per_row.d + i, r);
 }
 
 // d_o[pos] = w dy[t], d_w = <dy[t], o[pos]>: one token a block, four pairs at a time, each
@@ -245,12 +242,12 @@ __global__ void
             wt[j] = pos[j] >= 0 ? __ldg(w + p + j) : 0.0f;
         }
         for (int c = threadIdx.x; c < per_row; c += blockDim.x) {
-            const Pack<T, N> a = dy[t * per_row + c];
+            const Pack<T, N> a = load_pack(dy + t * per_row + c);
             Pack<T, N> b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 b[j].raw = {};
-                if (pos[j] >= 0) b[j] = o[static_cast<size_t>(pos[j]) * per_row + c];
+                if (pos[j] >= 0) b[j] = load_pack(o + static_cast<size_t>(pos[j]) * per_row + c);
             }
             float g[N];
             a.get(g);
@@ -265,7 +262,7 @@ __global__ void
                 }
                 Pack<T, N> r;
                 r.set(f);
-                if (pos[j] >= 0) d_o[static_cast<size_t>(pos[j]) * per_row + c] = r;
+                if (pos[j] >= 0) store_pack(d_o + static_cast<size_t>(pos[j]) * per_row + c, r);
             }
         }
 #pragma unroll
@@ -286,16 +283,21 @@ __global__ void
 }
 
 // Calls f(Pack<T, N>{}) with the widest unit that keeps every row of `width` elements
-// aligned: 16, 8 or 4 bytes, or one element.
+// aligned: 32 (where `base`, the buffers' addresses together, allows it), 16, 8 or 4 bytes,
+// or one element.
 template <class F>
-cudaError_t by_type(int type, int width, F&& f) {
+cudaError_t by_type(int type, int width, uintptr_t base, F&& f) {
+    const bool wide =
+        (base | static_cast<uintptr_t>(width) * static_cast<uintptr_t>(type_bytes(type))) % 32 == 0;
     if (type == kTypeF32) {
+        if (wide) return f(Pack<float, 8>{});
         if (width % 4 == 0) return f(Pack<float, 4>{});
         if (width % 2 == 0) return f(Pack<float, 2>{});
         return f(Pack<float, 1>{});
     }
     auto half_width = [&](auto zero) {
         using T = decltype(zero);
+        if (wide) return f(Pack<T, 16>{});
         if (width % 8 == 0) return f(Pack<T, 8>{});
         if (width % 4 == 0) return f(Pack<T, 4>{});
         if (width % 2 == 0) return f(Pack<T, 2>{});
@@ -303,6 +305,8 @@ cudaError_t by_type(int type, int width, F&& f) {
     };
     return type == kTypeBF16 ? half_width(__nv_bfloat16{}) : half_width(__half{});
 }
+
+uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 // Units per thread: four where that still leaves several blocks an SM, else one.
 bool many_units(uint32_t units) { return units >= 4u * kRThreads * 152u * 4u; }
@@ -321,7 +325,7 @@ cudaError_t launch_moe_sort(const int32_t* ids, int n_pairs, int top_k, int n_ex
     const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
         return static_cast<int>(cudaFuncSetAttribute(
             k_moe_sort, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            static_cast<int>((kSortWarps + 2) * kSortThreads * sizeof(int32_t))));
+            static_cast<int>((kSortWarps + 2) * kMaxExperts * sizeof(int32_t))));
     }));
     if (attr_err != cudaSuccess) return attr_err;
     // one CTA for as many pairs as its warps take in two steps of 32, else a cluster of 8
@@ -337,7 +341,7 @@ cudaError_t launch_moe_sort(const int32_t* ids, int n_pairs, int top_k, int n_ex
 
 cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_rows, int width,
                                 const int32_t* token_at, void* xs, cudaStream_t s) {
-    return by_type(type, width, [&](auto unit) {
+    return by_type(type, width, bits(x) | bits(xs), [&](auto unit) {
         using P = decltype(unit);
         const int per_row = width / P::kN;
         const FastDiv div(static_cast<uint32_t>(per_row));
@@ -345,10 +349,10 @@ cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_row
             const P* xp = static_cast<const P*>(x);
             P* out = static_cast<P*>(xs);
             if (many_units(units))
-                return launch_after(k_moe_dispatch<P, 4>, dim3(blocks_of(units, 4)), kRThreads, 0, s, 1,
-                                    xp, n_tokens, row0, units, div, token_at, out);
-            return launch_after(k_moe_dispatch<P, 1>, dim3(blocks_of(units, 1)), kRThreads, 0, s, 1,
-                                    xp, n_tokens, row0, units, div, token_at, out);
+                return launch_after(k_moe_dispatch<P, 4>, dim3(blocks_of(units, 4)), kRThreads, 0,
+                                    s, 1, xp, n_tokens, row0, units, div, token_at, out);
+            return launch_after(k_moe_dispatch<P, 1>, dim3(blocks_of(units, 1)), kRThreads, 0, s,
+                                1, xp, n_tokens, row0, units, div, token_at, out);
         });
     });
 }
@@ -356,21 +360,14 @@ cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_row
 cudaError_t launch_moe_gather_sum(const void* o, int type, int n_tokens, int top_k, int width,
                                   const int32_t* pos_of, const float* route_w, void* y,
                                   cudaStream_t s) {
-    return by_type(type, width, [&](auto unit) {
+    return by_type(type, width, bits(o) | bits(y), [&](auto unit) {
         using P = decltype(unit);
-        constexpr int kN = P::kN;
         using T = typename P::Elem;
-        const FastDiv div(static_cast<uint32_t>(width / kN));
-        return over_rows(n_tokens, width / kN, [&](uint32_t row0, uint32_t units) {
-            const P* in = static_cast<const P*>(o);
-            P* out = static_cast<P*>(y);
-            if (many_units(units))
-                return launch_after(k_moe_gather_sum<T, kN, 2>, dim3(blocks_of(units, 2)), kRThreads, 0,
-                                    s, 1, in, n_tokens * top_k, top_k, row0, units, div, pos_of,
-                                    route_w, out);
-            return launch_after(k_moe_gather_sum<T, kN, 1>, dim3(blocks_of(units, 1)), kRThreads, 0,
-                                    s, 1, in, n_tokens * top_k, top_k, row0, units, div, pos_of,
-                                    route_w, out);
+        const FastDiv div(static_cast<uint32_t>(width / P::kN));
+        return over_rows(n_tokens, width / P::kN, [&](uint32_t row0, uint32_t units) {
+            return launch_after(k_moe_gather_sum<T, P::kN>, dim3(blocks_of(units, 1)), kRThreads,
+                                0, s, 1, static_cast<const P*>(o), n_tokens * top_k, top_k, row0,
+                                units, div, pos_of, route_w, static_cast<P*>(y));
         });
     });
 }
@@ -379,7 +376,7 @@ cudaError_t launch_moe_combine_grad(const void* dy, const void* o, int type, int
                                     int top_k, int width, const int32_t* pos_of,
                                     const float* route_w, void* d_o, float* d_route_w,
                                     cudaStream_t s) {
-    return by_type(type, width, [&](auto unit) {
+    return by_type(type, width, bits(dy) | bits(o) | bits(d_o), [&](auto unit) {
         using P = decltype(unit);
         constexpr int kN = P::kN;
         using T = typename P::Elem;
