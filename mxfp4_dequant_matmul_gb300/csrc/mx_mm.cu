@@ -47,17 +47,18 @@ namespace cg = cooperative_groups;
 constexpr int kM = 128;                     // weight rows per tile
 constexpr int kK = 256;                     // elements per ring stage: 128 code bytes a row
 constexpr int kGroupsStage = kK / kGroup;   // 8 scale bytes a row
-// Warps.  0: copies (of W alone when unsplit), 1: MMAs, 2: W's scales, 3 and 4: X's scales
-// (128 tokens each; 4 unused when split or with one block), 5 and 6 (unsplit): copies of X,
-// scales to tensor memory.  A role is one warp's chain of waits and issues, several hundred
-// cycles a stage, so an unsplit CTA spreads them: one copy warp and one warp for scales and
-// MMAs were both busy all the time and held a prompt's experts at 72 us.  Then the epilogue,
-// each TMEM lane quarter once, or twice: a warp's stores wait for each other, 33 MB of FP32
-// results took 18.5 us by four warps an SM and 12.4 us by eight.
+// Warps.  0, and unsplit 5 and 7: copies; 1: MMAs; 2: W's scales; 3 and 4: X's scales (128
+// tokens each; 4 unused when split or with one block); 6 (unsplit): scales to tensor memory;
+// then the epilogue.  A role is one warp's chain of waits and issues, 400 to 700 cycles a
+// stage whatever it does: a copy holds its registers for some 200 cycles after it is issued,
+// a poll answers after 100.  One copy warp for both operands needs 700, so three take the
+// stages in turn.  The epilogue has each TMEM lane quarter once, or twice: a warp's stores
+// wait for each other, 33 MB of FP32 results took 18.5 us by four warps an SM and 12.4 us by
+// eight.
 template <bool kSplit>
 struct Roles {
-    static constexpr int kCopyX = 5, kToTmem = 6;
-    static constexpr int kEpi = kSplit ? 4 : 7, kEpiWarps = kSplit ? 4 : 8;
+    static constexpr int kToTmem = 6, kCopiers = kSplit ? 1 : 3;
+    static constexpr int kEpi = kSplit ? 4 : 8, kEpiWarps = kSplit ? 4 : 8;
     static constexpr int kThreads = 32 * (kEpi + kEpiWarps);
 };
 constexpr uint32_t kABytes = kM * kK / 2;
@@ -388,7 +389,6 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     const int rank = kSplit ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
     const int n_rank = kSplit ? static_cast<int>(cg::this_cluster().num_blocks()) : 1;
 
-    constexpr int kCopiers = kSplit ? 1 : 2;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&tmem_base)),
@@ -398,14 +398,14 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     }
     if (tid == 0) {
         for (int i = 0; i < a.n_stages; ++i) {
-            mbar_init(&full[i], kCopiers);
+            mbar_init(&full[i], 1);
             mbar_init(&in_tmem[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_empty[i], Roles<kSplit>::kEpiWarps);
-            mbar_init(&sc_full[i], kCopiers);
+            mbar_init(&sc_full[i], 1);
             mbar_init(&sc_empty[i], 1 + NB);   // W's and X's scale warps
             mbar_init(&sf_full[i], 1 + NB);
             mbar_init(&sf_empty[i], 1);
@@ -462,8 +462,9 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         kSplit ? min(a.n_steps,
                      2 * static_cast<int>(static_cast<long long>(pairs) * (rank + 1) / n_rank))
                : a.n_steps;
-    const int tile0 = kSplit ? static_cast<int>(blockIdx.x) / n_rank : static_cast<int>(blockIdx.x);
-    const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x);   // (split: one tile)
+    // a cluster's tiles (split: one)
+    const int tile0 = static_cast<int>(blockIdx.x) / n_rank;
+    const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x) / n_rank;
     constexpr int kAcc = kSplit ? 1 : 2;   // accumulators, of tn columns each
     const uint32_t sf_cols = tmem + kAcc * a.tn;
     constexpr uint32_t sf_stage = 8u + 8u * NB;   // TMEM columns of a stage's scales
@@ -506,20 +507,28 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         *abort_flag = 1;
         atomicOr(&g_fault_mx, 1);
     };
-    int issued = 0, sc_issued = 0;   // (warp 0) stages and scale buffers started
-
-    if (warp == 0 || (!kSplit && warp == Roles<kSplit>::kCopyX)) {
-        const bool do_w = warp == 0, do_x = kSplit || warp != 0;
+    if (warp == 0 || (!kSplit && (warp == 5 || warp == 7))) {
         // --- copies (the whole warp walks, one elected lane issues: as for the MMAs)
+        const int turn = warp == 0 ? 0 : warp == 5 ? 1 : 2;
+        constexpr int kTurns = Roles<kSplit>::kCopiers;
         const bool leader = elect_one();
         const uint64_t keep = l2_evict_last();
-        // experts' weights pass through once; one matrix may still be there at its next use
-        const uint64_t w_policy = a.offsets != nullptr ? l2_evict_first()
-                                  : kSplit             ? l2_evict_normal()
-                                                       : keep;
-        const uint32_t ring = smem_u32(smem);
-        uint32_t st = 0, phase = 1;   // phase of the empty barriers: the first round passes at once
-        int j = 0;
+        // Experts' weights pass through once when few tokens are with each; more tokens read a
+        // row tile again (2048 tokens, top-4 of 64 experts 2880x2880: 68.7 us, evicted first
+        // 73.2).  One matrix may still be there at its next use.
+        const uint64_t w_policy = a.offsets != nullptr && a.tn <= 32 ? l2_evict_first()
+                                  : kSplit || a.offsets != nullptr   ? l2_evict_normal()
+                                                                     : keep;
+        const uint32_t ring = smem_u32(smem), n_stages = static_cast<uint32_t>(a.n_stages);
+        const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
+        // the ring position of this warp's next stage; phase of the empty barriers: the first
+        // round passes at once
+        uint32_t st = 0, phase = 1;
+        auto advance = [&](uint32_t by) {
+            for (st += by; st >= n_stages; st -= n_stages) phase ^= 1u;
+        };
+        advance(turn);
+        int j = 0, sc_issued = 0, s = s_lo + turn;
         bool ok = true, ready = false;
         // a tile's scale rows, contiguous in both planes, one tile ahead of its codes
         auto copy_scales = [&](const Tile& t) {
@@ -535,47 +544,42 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
             const uint32_t wb =
                 (static_cast<uint32_t>(min(kM, a.rows - t.r0) * a.gpr) + 15u) & ~15u;
             const uint32_t xb = (skew + static_cast<uint32_t>((t.t1 - t.t0) * a.gpr) + 15u) & ~15u;
-            if (leader && do_w) {
-                mbar_arrive_expect_tx(&sc_full[b], wb);
+            if (leader) {
+                mbar_arrive_expect_tx(&sc_full[b], wb + xb);
                 bulk_g2s(dst, a.w_scales + static_cast<size_t>(t.e) * a.bank_stride + w_at, wb,
                          &sc_full[b], w_policy);
-            } else if (leader) {
-                mbar_arrive_expect_tx(&sc_full[b], xb);
                 bulk_g2s(dst + a.sc_w, a.x_scales + (x_at - skew), xb, &sc_full[b], keep);
             }
             __syncwarp();
             return true;
         };
-        if (a.n_sc > 0 && tile0 < n_tiles) ok = copy_scales(tile_at(tile0, 0));
+        const bool scales = a.n_sc > 0 && turn == 0;
+        if (scales && tile0 < n_tiles) ok = copy_scales(tile_at(tile0, 0));
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
             const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
-            const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
-            const uint32_t bytes =
-                (do_w ? kABytes : 0u) + (do_x ? static_cast<uint32_t>(n_box) * box_bytes : 0u);
-            for (int s = s_lo; s < s_hi; ++s, ++issued) {
+            const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box) * box_bytes;
+            if (scales && tile + tile_step < n_tiles) {
+                ok = copy_scales(tile_at(tile + tile_step, j + 1));
+                if (!ok) break;
+            }
+            for (; s < s_hi; s += kTurns) {
                 ok = ready || mbar_wait_for(&empty[st], phase, kWaitMx);
                 if (!ok) break;
                 const uint32_t dst = ring + st * a.stage_bytes, now = st;
-                if (++st == static_cast<uint32_t>(a.n_stages)) {
-                    st = 0;
-                    phase ^= 1u;
-                }
+                advance(kTurns);
                 ready = mbar_ready(&empty[st], phase);
                 if (leader) {
                     mbar_arrive_expect_tx(&full[now], bytes);
-                    if (do_w) tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[now], w_policy);
-                    if (do_x)
-                        for (int b = 0; b < n_box; ++b)
-                            tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
-                                  s * (kK / 2), t.t0 + b * a.box, &full[now], keep);
+                    tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[now], w_policy);
+                    tma2d(dst + kABytes, &xmap, s * (kK / 2), t.t0, &full[now], keep);
+                    for (int b = 1; b < n_box; ++b)
+                        tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
+                              s * (kK / 2), t.t0 + b * a.box, &full[now], keep);
                 }
                 __syncwarp();
-                if (s == s_lo && a.n_sc > 0 && tile + tile_step < n_tiles) {
-                    ok = copy_scales(tile_at(tile + tile_step, j + 1));
-                    if (!ok) break;
-                }
             }
+            s -= s_hi - s_lo;   // stages of the next tile before this warp's turn
             ok = ok && !*abort_flag;
         }
         if (!ok) fail();
@@ -588,9 +592,22 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         const uint32_t ring = smem_u32(smem);
         const uint64_t op0 = operand_desc(ring), sf0 = scale_desc(smem_u32(sf_buf));
         const uint32_t stage16 = a.stage_bytes >> 4;   // descriptors count 16 bytes
-        uint32_t st = 0, phase = 0, group = 0;   // group: kAhead stages sharing a scale slot
+        const uint32_t n_stages = static_cast<uint32_t>(a.n_stages);
+        uint32_t st = 0, phase = 0;
+        uint32_t group = 0;   // (split) kAhead stages sharing a scale slot
         int j = 0;
-        bool ok = true, ready = false, sf_ready = false;
+        bool ok = true;
+        auto next_of = [&](uint32_t& stage, uint32_t& parity) {
+            if (++stage == n_stages) {
+                stage = 0;
+                parity ^= 1u;
+            }
+        };
+        auto wait = [&](uint32_t stage, uint32_t parity) {
+            bool r = mbar_wait_for(&full[stage], parity, kWaitMx);
+            if (!kSplit) r = r && mbar_wait_for(&in_tmem[stage], parity, kWaitMx);
+            return r;
+        };
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
             const int n = __shfl_sync(0xFFFFFFFFu, (t.t1 - t.t0 + 15) & ~15, 0);
@@ -598,44 +615,63 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
             const int ab = j % kAcc;
             if (j >= kAcc)
                 ok = mbar_wait_for(&acc_empty[ab], static_cast<uint32_t>(j / kAcc - 1) & 1u,
-                               kWaitMx);
+                                   kWaitMx);
             fence_after_mx();
             const uint32_t d = tmem + ab * a.tn;
-            for (int s = s_lo; s < s_hi && ok; ++s) {
-                const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
-                if (!kSplit)
-                    ok = sf_ready || mbar_wait_for(&in_tmem[st], phase, kWaitMx);
-                else if (q == 0)
-                    ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
-                ok = ok && (ready || mbar_wait_for(&full[st], phase, kWaitMx));
-                if (!ok) break;
-                fence_after_mx();
-                const uint32_t now = st;
-                if (++st == static_cast<uint32_t>(a.n_stages)) {
-                    st = 0;
-                    phase ^= 1u;
-                }
-                ready = mbar_ready(&full[st], phase);
-                if (!kSplit) sf_ready = mbar_ready(&in_tmem[st], phase);
-                const uint32_t sfa = sf_cols + now * sf_stage, sfb = sfa + 8u;
-                const uint64_t ad = op0 + now * stage16, bd = ad + (kABytes >> 4);
-                const uint64_t sd = sf0 + ((slot * kSfSlot + q * kSfStage) >> 4);
-                const bool last = q == kAhead - 1 || s + 1 == s_hi;
-                const uint32_t more = s > s_lo ? 1u : 0u;
-                // K = 64 at a time; the last stage of a row may hold fewer
+            // four MMAs of K = 64 and the stage's release; the last stage of a row may hold fewer
+            auto issue = [&](int s, uint32_t stage) {
+                const uint32_t sfa = sf_cols + stage * sf_stage, sfb = sfa + 8u;
+                const uint32_t sfb2 = sfb + 4u * NB;
+                const uint64_t ad = op0 + stage * stage16, bd = ad + (kABytes >> 4);
                 const int kk_end = (a.gpr - s * kGroupsStage + 1) / 2;
-                if (leader) {
-                    if (kSplit) scales_to_tmem<NB>(sfa, sd);
-                    const uint32_t sfb2 = sfb + 4u * NB;
-                    umma_mxf4(d, ad, bd, id0, sfa, sfb, more);
-                    if (kk_end > 1) umma_mxf4(d, ad + 2, bd + 2, id2, sfa, sfb, 1u);
-                    if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
-                    if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
-                    umma_commit_mx(&empty[now]);
-                    if (kSplit && last) umma_commit_mx(&sf_empty[slot]);
+                umma_mxf4(d, ad, bd, id0, sfa, sfb, s > s_lo ? 1u : 0u);
+                if (kk_end > 1) umma_mxf4(d, ad + 2, bd + 2, id2, sfa, sfb, 1u);
+                if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
+                if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
+                umma_commit_mx(&empty[stage]);
+            };
+            for (int s = s_lo; s < s_hi && ok;) {
+                const uint32_t st0 = st, phase0 = phase;
+                next_of(st, phase);
+                if constexpr (kSplit) {
+                    const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
+                    if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
+                    ok = ok && wait(st0, phase0);
+                    if (!ok) break;
+                    fence_after_mx();
+                    const bool last = q == kAhead - 1 || s + 1 == s_hi;
+                    if (leader) {
+                        scales_to_tmem<NB>(sf_cols + st0 * sf_stage,
+                                                  sf0 + ((slot * kSfSlot + q * kSfStage) >> 4));
+                        issue(s, st0);
+                        if (last) umma_commit_mx(&sf_empty[slot]);
+                    }
+                    __syncwarp();
+                    group += last ? 1u : 0u;
+                    ++s;
+                } else {
+                    // two stages at a time where the second is there too: their polls overlap
+                    const uint32_t st1 = st, phase1 = phase;
+                    bool both = s + 1 < s_hi;
+                    const bool f1 = mbar_ready(&full[st1], phase1);
+                    const bool m1 = mbar_ready(&in_tmem[st1], phase1);
+                    ok = wait(st0, phase0);
+                    if (!ok) break;
+                    both = __all_sync(0xFFFFFFFFu, both && f1 && m1);
+                    fence_after_mx();
+                    if (both) {
+                        next_of(st, phase);
+                        if (leader) {
+                            issue(s, st0);
+                            issue(s + 1, st1);
+                        }
+                        s += 2;
+                    } else {
+                        if (leader) issue(s, st0);
+                        ++s;
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-                group += last ? 1u : 0u;
             }
             if (ok && leader) umma_commit_mx(&acc_full[ab]);
             ok = ok && !*abort_flag;
@@ -650,27 +686,41 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         // --- scales from shared to tensor memory, as far ahead as the ring goes
         const bool leader = elect_one();
         const uint64_t sf0 = scale_desc(smem_u32(sf_buf));
+        const uint32_t n_stages = static_cast<uint32_t>(a.n_stages);
         uint32_t st = 0, phase = 1, group = 0;
         bool ok = true;
+        auto copy = [&](uint32_t stage, uint32_t slot, uint32_t q) {
+            scales_to_tmem<NB>(sf_cols + stage * sf_stage,
+                                      sf0 + ((slot * kSfSlot + q * kSfStage) >> 4));
+            umma_commit_mx(&in_tmem[stage]);
+        };
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
-            for (int s = s_lo; s < s_hi; ++s) {
-                const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
-                if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
-                ok = ok && mbar_wait_for(&empty[st], phase, kWaitMx);
-                if (!ok) break;
-                fence_after_mx();
-                const bool last = q == kAhead - 1 || s + 1 == s_hi;
-                if (leader) {
-                    scales_to_tmem<NB>(sf_cols + st * sf_stage,
-                                       sf0 + ((slot * kSfSlot + q * kSfStage) >> 4));
-                    umma_commit_mx(&in_tmem[st]);
-                    if (last) umma_commit_mx(&sf_empty[slot]);
-                }
-                __syncwarp();
-                group += last ? 1u : 0u;
-                if (++st == static_cast<uint32_t>(a.n_stages)) {
-                    st = 0;
-                    phase ^= 1u;
+            for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead, ++group) {
+                const uint32_t slot = group & 1u;
+                const int n_q = min(kAhead, s_hi - s0);
+                ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
+                for (int q = 0; q < n_q && ok;) {   // two stages at a time, as the MMAs
+                    const uint32_t st0 = st, phase0 = phase;
+                    if (++st == n_stages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                    bool both = mbar_ready(&empty[st], phase);
+                    ok = mbar_wait_for(&empty[st0], phase0, kWaitMx);
+                    if (!ok) break;
+                    both = __all_sync(0xFFFFFFFFu, both && q + 1 < n_q);
+                    fence_after_mx();
+                    if (leader) {
+                        copy(st0, slot, q);
+                        if (both) copy(st, slot, q + 1);
+                        if (q + (both ? 2 : 1) == n_q) umma_commit_mx(&sf_empty[slot]);
+                    }
+                    __syncwarp();
+                    if (both && ++st == n_stages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                    q += both ? 2 : 1;
                 }
             }
             ok = ok && !*abort_flag;
@@ -800,14 +850,8 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     }
     __syncthreads();
     if (*abort_flag && tid == 0) {
-        // a CTA that gave up: let the copies it started land before it exits
-        for (int i = issued - a.n_stages; i < issued; ++i)
-            if (i >= 0)
-                mbar_wait_for(&full[i % a.n_stages], static_cast<uint32_t>(i / a.n_stages) & 1u,
-                          kDrainMx);   // (its scales may never arrive)
-        for (int i = sc_issued - 2; i < sc_issued; ++i)
-            if (i >= 0)
-                mbar_wait_for(&sc_full[i % 2], static_cast<uint32_t>(i / 2) & 1u, kDrainMx);
+        // a CTA that gave up: its copies in flight land long before this
+        for (const long long t0 = clock64(); clock64() - t0 < kDrainMx;) __nanosleep(1000);
     }
     fence_before_mx();
     __syncthreads();
@@ -970,15 +1014,21 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     if (!code_map(&wmap, bank, cols, rows, n_experts, stride, kM) ||
         !code_map(&xmap, xq, cols, n_rows, 0, 16, a.box))
         return cudaErrorNotSupported;
+    const unsigned cluster = static_cast<unsigned>(split);
     const long tiles = static_cast<long>(a.n_rt) * (offsets != nullptr ? 1 : a.n_tt);
-    const unsigned grid = split > 1 ? static_cast<unsigned>(a.n_rt * split)
-                          : offsets != nullptr || tiles > sms ? static_cast<unsigned>(sms)
-                                                              : static_cast<unsigned>(tiles);
+    const unsigned most = static_cast<unsigned>(sms) / cluster;
+    const unsigned grid =
+        cluster * (split > 1 ? static_cast<unsigned>(a.n_rt)
+                   : offsets != nullptr || tiles > static_cast<long>(most)
+                       ? most
+                       : static_cast<unsigned>(tiles));
     auto go = [&](auto* y) {
         using T = std::remove_pointer_t<decltype(y)>;
-        if (split > 1) return launch_k<T, true, 1>(wmap, xmap, a, y, grid, split, smem, s);
-        return sf_blocks == 1 ? launch_k<T, false, 1>(wmap, xmap, a, y, grid, 1, smem, s)
-                              : launch_k<T, false, 2>(wmap, xmap, a, y, grid, 1, smem, s);
+        auto launch = [&](auto kernel_launch) {
+            return kernel_launch(wmap, xmap, a, y, grid, cluster, smem, s);
+        };
+        if (split > 1) return launch(launch_k<T, true, 1>);
+        return sf_blocks == 1 ? launch(launch_k<T, false, 1>) : launch(launch_k<T, false, 2>);
     };
     return y_type == kTypeF32 ? go(static_cast<float*>(Y)) : go(static_cast<__nv_bfloat16*>(Y));
 }
