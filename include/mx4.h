@@ -4,7 +4,10 @@
  * expert's matrix), and the routing of tokens to experts and back with its
  * gradient.  Status codes, pointer rules and stream semantics are those of
  * mxfp4.h (MXFP4_STATUS_*; work enqueued on `stream`, nothing enqueued on a
- * refusal, nothing allocated, deterministic results).
+ * refusal, nothing allocated, deterministic results).  The kernels are launched
+ * as programmatic dependents: their set-up may run while the kernel ahead of
+ * them in the stream finishes, but they read and write memory only after it has
+ * completed.
  *
  * An MXFP4 matrix here is a weight buffer of mxfp4.h, whatever it holds: [rows,
  * cols] with cols % 32 == 0, code plane then scale plane, mxfp4_nbytes(rows,
@@ -66,10 +69,15 @@ int mxfp4_swiglu_quant(const void* gate, const void* up, int type, int rows, int
 
 /* Product of two MXFP4 matrices: Y[t*rows + r] = sum_c W[r][c] * X[t][c], W
  * [rows, cols], X [nb, cols], Y [nb, rows] of y_type (F32 or BF16; the FP32 sum
- * rounded once to nearest even).  Every product of two elements is exact; sums
- * are FP32.  Error bound (before the rounding to BF16): 1e-5 * sum_c |W X|.  A
- * group with scale byte 255 in either operand makes its row (W) or its token
- * (X) NaN. */
+ * rounded once to nearest even).  On the block-scaled 4-bit tensor cores, any
+ * nb >= 1.  Every product of two elements is exact; sums are FP32, 64 columns
+ * added at a time, each addition losing less than 2^-23 of the running sum.
+ * Error bound (before the rounding to BF16): (cols / 64 + 8) * 2^-24 * sum_c
+ * |W X|, reached to a third by sums of one sign; with mixed signs the error is
+ * two orders smaller.  A group with scale byte 255 in either operand makes its
+ * row (W) or its token (X) NaN.  Per token the result does not depend on the
+ * other tokens' values, but it may on nb (the order of the sums is chosen by
+ * the shape).  Deterministic. */
 int mxfp4_mm_mx(const void* w, int rows, int cols, const void* xq, int nb, void* Y, int y_type,
                 cudaStream_t stream);
 

@@ -954,13 +954,21 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     int split = 1, per_sm = 1;
     if (offsets != nullptr) {
         const int mean = (n_rows + n_experts - 1) / n_experts;
-        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 80 ? 96 : 128;
+        // widest tile near the mean: narrower ones read the weights again, wider ones leave
+        // less room for copies in flight (64 experts 2880x2880, us: 2 rows each 38.8 at 16
+        // columns, 39.4 at 32; 64 rows 84 at 32, 53.6 at 96, 57.1 at 160; 256 rows 123 at 96, 108 at
+        // 128, 101 at 160, 109 at 192)
+        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 80 ? 96
+               : mean <= 128 ? 128 : 160;
         a.box = a.tn < 64 ? a.tn : a.tn % 64 == 0 ? 64 : 32;
         a.n_tt = 0;
     } else {
         a.tn = std::min((n_rows + 15) / 16 * 16, kMaxTokens);
         if (n_rows > 64) {
-            // token tiles: the fewest rounds of tiles over the SMs x columns per tile
+            // token tiles: the fewest rounds of tiles over the SMs x columns per tile (and 32
+            // for what a tile costs by itself).  Within 3 % of the best width from 32 to 208 on
+            // eleven shapes swept, e.g. 4096x4096, 512 tokens: 128 columns 9.3 us (64: 12.2,
+            // 208: 11.3); 4096 tokens: 192 columns 32.9 us (128: 37.3)
             long best = -1;
             for (int tn = 32; tn <= kMaxTokens; tn += 16) {
                 const long tiles = static_cast<long>(a.n_rt) * ((n_rows + tn - 1) / tn);
@@ -992,9 +1000,11 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
                                    : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0);
     // Whole scale rows of a tile by bulk copies, two tiles deep, where rows of a tile are short
     // enough; else (long rows, slices of a split tile) loads a few stages ahead.
-    a.sc_w = static_cast<uint32_t>(kM * a.gpr + 15) & ~15u;
-    a.sc_bytes = a.sc_w + (static_cast<uint32_t>(a.tn * a.gpr + 31 + 15) & ~15u);
-    a.n_sc = split == 1 && a.sc_bytes <= 32 * 1024 ? 2 : 0;
+    if (split == 1 && static_cast<long>(kM + a.tn) * a.gpr <= 32 * 1024 - 64) {
+        a.n_sc = 2;
+        a.sc_w = static_cast<uint32_t>(kM * a.gpr);
+        a.sc_bytes = a.sc_w + (static_cast<uint32_t>(a.tn * a.gpr + 31 + 15) & ~15u);
+    }
     const size_t budget = kSmemMax / (split > 1 ? per_sm : 1) - kSmemSlack - 1024 - extra -
                           static_cast<size_t>(a.n_sc) * a.sc_bytes;
     a.n_stages = std::min(kMaxStages, static_cast<int>(budget / a.stage_bytes));

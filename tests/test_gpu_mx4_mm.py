@@ -70,6 +70,19 @@ def test_exact_sums_exactly(mx, rows, cols, nb):
     assert np.array_equal(product(mx, w, x), both(w, x)[0])
 
 
+@pytest.mark.parametrize("cols", [4096, 32768, 131072])
+@pytest.mark.parametrize("nb", [2, 70])
+def test_long_sums_of_one_sign(mx, cols, nb):
+    # the running sum grows by 64 columns at a time, each addition losing less than 2^-23 of it:
+    # cols/64 additions of a linearly growing sum lose less than cols/64 * 2^-24 of the whole,
+    # and the sums within 64 columns and over slices of K a few units more
+    rng = np.random.default_rng(cols + nb)
+    w, x = ref.random_matrix(rng, 70, cols), ref.random_matrix(rng, nb, cols)
+    w, x = (w[0] & 7, w[1]), (x[0] & 7, x[1])
+    want, l1 = both(w, x)
+    assert (np.abs(product(mx, w, x) - want) <= (cols / 64 + 8) * 2.0**-24 * l1).all()
+
+
 @pytest.mark.parametrize("nb", [1, 20, 200])
 def test_every_pair_of_codes(mx, nb):
     # row r holds code r % 16 in one place, token t code t % 16 there: the 256 products
