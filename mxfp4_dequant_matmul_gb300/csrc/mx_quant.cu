@@ -72,9 +72,23 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
     }
 }
 
-// silu(g) * u in FP32 with the limit of the routed-expert passes.
-__device__ __forceinline__ float swiglu(float g, float u, float limit) {
-    return moe_act(g, u, MoeAct{nullptr, limit, 0}, 0);
+// silu(g) * u of two elements in FP32, u clamped to [-limit, limit] and g to at most limit where
+// limit > 0.  silu(g) = g e^min(g,0) / (1 + e^-|g|): the denominator is in [1, 2], so nothing
+// overflows on the way and rcp.approx holds it to 2^-23, far below the codes' 3 bits (the exact
+// division costs as much as all the rest).
+__device__ __forceinline__ float2 swiglu(float2 g, float2 u, float limit) {
+    if (limit > 0.0f) {
+        u.x = u.x < -limit ? -limit : (u.x > limit ? limit : u.x);
+        u.y = u.y < -limit ? -limit : (u.y > limit ? limit : u.y);
+        g.x = g.x < limit ? g.x : limit;
+        g.y = g.y < limit ? g.y : limit;
+    }
+    const float2 e = make_float2(expf(-fabsf(g.x)), expf(-fabsf(g.y)));
+    float2 r = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.y));
+    const float2 top = make_float2(g.x < 0.0f ? e.x : 1.0f, g.y < 0.0f ? e.y : 1.0f);
+    return __fmul2_rn(__fmul2_rn(__fmul2_rn(g, top), r), u);
 }
 
 // The 8 elements of one item (zeros past the end or for a row index out of range).
@@ -98,7 +112,12 @@ __device__ __forceinline__ void load_item(float (&v)[8], const T* x, const T* up
         float u[8];
         load8<T, kVec>(up + src * ld + c, u);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = swiglu(v[q], u[q], limit);
+        for (int q = 0; q < 8; q += 2) {
+            const float2 a =
+                swiglu(make_float2(v[q], v[q + 1]), make_float2(u[q], u[q + 1]), limit);
+            v[q] = a.x;
+            v[q + 1] = a.y;
+        }
     }
 }
 
@@ -295,6 +314,70 @@ __global__ void __launch_bounds__(kQThreads)
     }
 }
 
+// The larger magnitude of three, NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// silu(gate) * up of aligned 16-bit rows: items as k_mx_quant16's, the act in FP32.
+template <typename T, bool kValues>
+__global__ void __launch_bounds__(kQThreads)
+    k_mx_swiglu16(const T* __restrict__ gate, const T* __restrict__ up, long long ld, float limit,
+                  uint32_t row0, uint32_t items, FastDiv per_row, uint2* __restrict__ codes,
+                  uint8_t* __restrict__ scales, T* __restrict__ values) {
+    pdl_trigger();
+    pdl_wait();
+    const uint32_t i = blockIdx.x * kQThreads + threadIdx.x;
+    uint32_t rg[8] = {}, ru[8] = {};
+    if (i < items) {
+        const uint32_t r = per_row.of(i);
+        const size_t at = static_cast<size_t>(row0 + r) * ld + (i - r * per_row.d) * 16;
+        ldg_stream32(gate + at, rg);
+        ldg_stream32(up + at, ru);
+    }
+    float2 v[8];
+    float top = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        v[q] = swiglu(halves_to_f32<T>(rg[q]), halves_to_f32<T>(ru[q]), limit);
+        top = max_abs3(top, v[q].x, v[q].y);
+    }
+    const float other = __shfl_xor_sync(0xFFFFFFFFu, top, 1);
+    const uint32_t e = __float_as_uint(max_abs3(top, other, other)) >> 23;
+    const bool bad = e == 255u;
+    const uint32_t k = bad ? 255u : (e > 2u ? e - 2u : 0u);
+    const float inv = __uint_as_float((254u - (bad ? 127u : k)) << 23);   // 2^(127-k)
+    uint32_t word[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float t[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float2 f = __fmul2_rn(v[4 * h + q], make_float2(inv, inv));
+            t[2 * q] = f.x;
+            t[2 * q + 1] = f.y;
+        }
+        word[h] = bad ? 0u : f32x8_to_e2m1x8(t);
+    }
+    if (i >= items) return;   // (a group's two lanes together)
+    const size_t at = static_cast<size_t>(row0) * per_row.d + i;
+    codes[at] = make_uint2(word[0], word[1]);
+    if ((threadIdx.x & 1) == 0) scales[at >> 1] = static_cast<uint8_t>(k);
+    if (kValues) {
+        const float sc = e8m0_to_f32(k);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float t[8];
+            e2m1x8_to_f32(word[h], t);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) t[q] = __fmul_rn(t[q], sc);
+            store8<T>(values + at * 16 + 8 * h, t);
+        }
+    }
+}
+
 template <typename T>
 cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, long long ld,
                          const int32_t* row_of, float limit, int rows, uint8_t* out, void* values,
@@ -304,9 +387,22 @@ cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, lo
     const bool vec = (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(up) |
                       (static_cast<uintptr_t>(ld) * sizeof(T))) % 16 == 0;
     if constexpr (sizeof(T) == 2) {
-        if (up == nullptr && (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(values) |
-                              (static_cast<uintptr_t>(ld) * sizeof(T))) % 32 == 0) {
+        if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(up) |
+             reinterpret_cast<uintptr_t>(values) | (static_cast<uintptr_t>(ld) * sizeof(T))) % 32 ==
+            0) {
             const FastDiv per16(static_cast<uint32_t>(cols / 16));
+            if (up != nullptr)
+                return over_rows(rows, cols / 16, [&](uint32_t row0, uint32_t items) {
+                    auto go = [&](auto kernel) {
+                        return launch_after(kernel, dim3((items + kQThreads - 1) / kQThreads),
+                                            kQThreads, 0, s, 1, static_cast<const T*>(x),
+                                            static_cast<const T*>(up), ld, limit, row0, items,
+                                            per16, reinterpret_cast<uint2*>(codes), scales,
+                                            static_cast<T*>(values));
+                    };
+                    return values != nullptr ? go(k_mx_swiglu16<T, true>)
+                                             : go(k_mx_swiglu16<T, false>);
+                });
             return over_rows(rows, cols / 16, [&](uint32_t row0, uint32_t items) {
                 auto go = [&](auto kernel, uint32_t per_thread) {
                     const uint32_t per_block = kQThreads * per_thread;
