@@ -8,10 +8,11 @@
 // exact unless it underflows far below half of E2M1's smallest step, so the
 // code is the only rounding.
 //
-// Bound by HBM in FP32: each element is read once and 17/32 byte (and the rounded value)
-// written.  A thread takes 8 elements (one 16-byte load in 16-bit types), four
-// lanes a group: amax by two shuffles, one 32-bit word of codes per lane (128
-// bytes per warp) and the group's scale byte from the first of the four.
+// k_mx_quant takes any alignment.  Bound by HBM in FP32: each element is read once and 17/32
+// byte (and the rounded value) written.  A thread takes 8 elements, four lanes a group: amax
+// by two shuffles, one 32-bit word of codes per lane (128 bytes per warp) and the group's
+// scale byte from the first of the four.  [14336, 4096] floats and their rounded values: 73.4 us,
+// 6.8 TB/s.
 #include <cstdint>
 
 #include "common.cuh"
@@ -171,7 +172,8 @@ __global__ void __launch_bounds__(kQThreads)
 // The same for aligned 16-bit rows, on the raw halves: with 16 bits an element the steps above
 // issue about 160 instructions per 8 elements, twice what HBM leaves time for.  Here amax is a
 // packed integer maximum of the magnitudes, and the rounded value is put together from the
-// code: for bfloat16 its two bytes by permutation out of a table of the eight magnitudes, x's
+// code ([7996, 2880] bfloat16 gathered from 1999 rows, with the rounded values: 12.6 us, 5.5
+// TB/s; the steps above took 24.6).  For bfloat16 its two bytes by permutation out of a table of the eight magnitudes, x's
 // sign, and one packed product with the scale (a power of two, exact); for half the
 // hardware's E2M1 decode and two packed products, as 2^(k-127) alone may be below half's
 // range although the value is not.
@@ -321,7 +323,10 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
     return r;
 }
 
-// silu(gate) * up of aligned 16-bit rows: items as k_mx_quant16's, the act in FP32.
+// silu(gate) * up of aligned 16-bit rows: items as k_mx_quant16's, the act in FP32.  Bound by
+// issue (about 20 instructions an element, two of them on the special-function unit; HBM leaves
+// time for 16): [8192, 2880] bfloat16 19.8 us, 5.4 TB/s, against 29.7 us with 8 elements a
+// thread and exact divisions.
 template <typename T, bool kValues>
 __global__ void __launch_bounds__(kQThreads)
     k_mx_swiglu16(const T* __restrict__ gate, const T* __restrict__ up, long long ld, float limit,
@@ -412,7 +417,8 @@ cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, lo
                                         reinterpret_cast<uint2*>(codes), scales,
                                         static_cast<T*>(values));
                 };
-                // two items a thread where that still leaves several blocks an SM
+                // two items a thread where that still leaves several blocks an SM (the sorted
+                // prompt above: 12.6 us against 13.3; 1000 rows: 3.2 against 2.8)
                 const bool two = items >= 2u * kQThreads * 152u * 8u;
                 if (values != nullptr)
                     return two ? go(k_mx_quant16<T, 2, true>, 2) : go(k_mx_quant16<T, 1, true>, 1);
@@ -432,7 +438,7 @@ cudaError_t launch_typed(const void* x, const void* up, int x_rows, int cols, lo
         if (up != nullptr)
             return vec ? go(k_mx_quant<T, true, true, 1>, 1) : go(k_mx_quant<T, true, false, 1>, 1);
         if (!vec) return go(k_mx_quant<T, false, false, 1>, 1);
-        // two items a thread where that still leaves several blocks an SM
+        // two items a thread as above ([14336, 4096] floats, codes alone: 39.4 us against 40.6)
         return items >= 2u * kQThreads * 152u * 8u ? go(k_mx_quant<T, false, true, 2>, 2)
                                                    : go(k_mx_quant<T, false, true, 1>, 1);
     });
