@@ -369,7 +369,6 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint64_t sc_full[2], sc_empty[2], sf_full[2], sf_empty[2];
-    __shared__ uint64_t in_tmem[kMaxStages];   // (unsplit) a stage's scales are in tensor memory
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word, n_tiles_sh;
     __shared__ Tile table[kTileTable];
@@ -398,8 +397,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     }
     if (tid == 0) {
         for (int i = 0; i < a.n_stages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&in_tmem[i], 1);
+            mbar_init(&full[i], kSplit ? 1 : 2);   // the copies, and scales in tensor memory
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -425,8 +423,8 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     // the next launch may be placed now that this CTA has its tensor memory (a CTA of the
     // next one that waits for columns then waits for CTAs that need nothing more)
     pdl_trigger();
-    pdl_wait();
     if (a.offsets != nullptr) {
+        pdl_wait();
         for (int e = tid; e <= a.n_experts; e += Roles<kSplit>::kThreads)
             off[e] = min(max(__ldg(a.offsets + e), 0), a.n_rows);
         __syncthreads();
@@ -502,6 +500,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     if (tid < kTileTable && tile0 + tid * tile_step < n_tiles)
         table[tid] = locate(tile0 + tid * tile_step);
     __syncthreads();
+    if (a.offsets == nullptr) pdl_wait();   // nothing in memory was needed so far
     auto tile_at = [&](int tile, int j) { return j < kTileTable ? table[j] : locate(tile); };
     auto fail = [&]() {
         *abort_flag = 1;
@@ -603,11 +602,6 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 parity ^= 1u;
             }
         };
-        auto wait = [&](uint32_t stage, uint32_t parity) {
-            bool r = mbar_wait_for(&full[stage], parity, kWaitMx);
-            if (!kSplit) r = r && mbar_wait_for(&in_tmem[stage], parity, kWaitMx);
-            return r;
-        };
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
             const int n = __shfl_sync(0xFFFFFFFFu, (t.t1 - t.t0 + 15) & ~15, 0);
@@ -636,7 +630,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 if constexpr (kSplit) {
                     const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
                     if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
-                    ok = ok && wait(st0, phase0);
+                    ok = ok && mbar_wait_for(&full[st0], phase0, kWaitMx);
                     if (!ok) break;
                     fence_after_mx();
                     const bool last = q == kAhead - 1 || s + 1 == s_hi;
@@ -653,11 +647,10 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                     // two stages at a time where the second is there too: their polls overlap
                     const uint32_t st1 = st, phase1 = phase;
                     bool both = s + 1 < s_hi;
-                    const bool f1 = mbar_ready(&full[st1], phase1);
-                    const bool m1 = mbar_ready(&in_tmem[st1], phase1);
-                    ok = wait(st0, phase0);
+                    const bool there = mbar_ready(&full[st1], phase1);
+                    ok = mbar_wait_for(&full[st0], phase0, kWaitMx);
                     if (!ok) break;
-                    both = __all_sync(0xFFFFFFFFu, both && f1 && m1);
+                    both = __all_sync(0xFFFFFFFFu, both && there);
                     fence_after_mx();
                     if (both) {
                         next_of(st, phase);
@@ -692,7 +685,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         auto copy = [&](uint32_t stage, uint32_t slot, uint32_t q) {
             scales_to_tmem<NB>(sf_cols + stage * sf_stage,
                                       sf0 + ((slot * kSfSlot + q * kSfStage) >> 4));
-            umma_commit_mx(&in_tmem[stage]);
+            umma_commit_mx(&full[stage]);
         };
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead, ++group) {
