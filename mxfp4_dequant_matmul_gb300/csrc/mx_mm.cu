@@ -71,7 +71,7 @@ constexpr long long kWaitMx = 1ll << 32, kDrainMx = 1ll << 24;   // SM cycles: a
 __device__ int g_fault_mx;
 
 // One launch's shape.  tn: most tokens of a tile (a multiple of 16); box: token rows of
-// one TMA copy (divides the stage's token rows).
+// one TMA copy (divides tn).
 struct MxArgs {
     const uint8_t* w_scales;      // scale plane of expert 0
     size_t bank_stride;
@@ -359,7 +359,7 @@ __device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int c0, i
 }
 
 // NB: 128-token blocks of a stage's scales.  Split tiles (few tokens) leave registers for
-// two CTAs on an SM.
+// three CTAs on an SM.
 template <typename T, bool kSplit, int NB>
 __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     k_mx_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -571,8 +571,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 if (leader) {
                     mbar_arrive_expect_tx(&full[now], bytes);
                     tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[now], w_policy);
-                    tma2d(dst + kABytes, &xmap, s * (kK / 2), t.t0, &full[now], keep);
-                    for (int b = 1; b < n_box; ++b)
+                    for (int b = 0; b < n_box; ++b)
                         tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
                               s * (kK / 2), t.t0 + b * a.box, &full[now], keep);
                 }
@@ -949,11 +948,12 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
         const int mean = (n_rows + n_experts - 1) / n_experts;
         // widest tile near the mean: narrower ones read the weights again, wider ones leave
         // less room for copies in flight (64 experts 2880x2880, us: 2 rows each 38.8 at 16
-        // columns, 39.4 at 32; 64 rows 84 at 32, 53.6 at 96, 57.1 at 160; 256 rows 123 at 96, 108 at
-        // 128, 101 at 160, 109 at 192)
-        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 80 ? 96
-               : mean <= 128 ? 128 : 160;
-        a.box = a.tn < 64 ? a.tn : a.tn % 64 == 0 ? 64 : 32;
+        // columns, 39.4 at 32; 32 rows 51.8 at 32, 49.5 at 96; 64 rows 82.5 at 32, 53.2 at 96,
+        // 56.5 at 160; 128 rows 70.6 at 96, 66.4 at 128, 68.3 at 160; 256 rows 104 at 128, 98 at
+        // 160, 113 at 176).  Copies of 16 rows: a tile brings no rows that it does not use (128
+        // rows 66.4, with copies of 64 68.0).
+        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 80 ? 96 : mean <= 128 ? 128 : 160;
+        a.box = 16;
         a.n_tt = 0;
     } else {
         a.tn = std::min((n_rows + 15) / 16 * 16, kMaxTokens);
