@@ -360,13 +360,14 @@ __device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int c0, i
 
 // NB: 128-token blocks of a stage's scales.  Split tiles (few tokens) leave registers for
 // three CTAs on an SM.
-template <typename T, bool kSplit, int NB>
+template <typename T, bool kSplit, int NB, int kP>
 __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     k_mx_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
             const MxArgs a, T* __restrict__ Y) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // (one barrier of each for a unit of kP stages)
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
     __shared__ uint64_t sc_full[2], sc_empty[2], sf_full[2], sf_empty[2];
     __shared__ uint32_t tmem_base;
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        for (int i = 0; i < a.n_stages; ++i) {
+        for (int i = 0; i < a.n_stages / kP; ++i) {
             mbar_init(&full[i], kSplit ? 1 : 2);   // the copies, and scales in tensor memory
             mbar_init(&empty[i], 1);
         }
@@ -463,6 +464,8 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     // a cluster's tiles (split: one)
     const int tile0 = static_cast<int>(blockIdx.x) / n_rank;
     const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x) / n_rank;
+    const int tile_units = (s_hi - s_lo + kP - 1) / kP;
+    const uint32_t n_units = static_cast<uint32_t>(a.n_stages / kP);   // of the ring
     constexpr int kAcc = kSplit ? 1 : 2;   // accumulators, of tn columns each
     const uint32_t sf_cols = tmem + kAcc * a.tn;
     constexpr uint32_t sf_stage = 8u + 8u * NB;   // TMEM columns of a stage's scales
@@ -518,16 +521,16 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         const uint64_t w_policy = a.offsets != nullptr && a.tn <= 32 ? l2_evict_first()
                                   : kSplit || a.offsets != nullptr   ? l2_evict_normal()
                                                                      : keep;
-        const uint32_t ring = smem_u32(smem), n_stages = static_cast<uint32_t>(a.n_stages);
+        const uint32_t ring = smem_u32(smem);
         const uint32_t box_bytes = static_cast<uint32_t>(a.box) * 128u;
-        // the ring position of this warp's next stage; phase of the empty barriers: the first
+        // the ring position of this warp's next unit; phase of the empty barriers: the first
         // round passes at once
-        uint32_t st = 0, phase = 1;
+        uint32_t un = 0, phase = 1;
         auto advance = [&](uint32_t by) {
-            for (st += by; st >= n_stages; st -= n_stages) phase ^= 1u;
+            for (un += by; un >= n_units; un -= n_units) phase ^= 1u;
         };
         advance(turn);
-        int j = 0, sc_issued = 0, s = s_lo + turn;
+        int j = 0, sc_issued = 0, u = turn;
         bool ok = true, ready = false;
         // a tile's scale rows, contiguous in both planes, one tile ahead of its codes
         auto copy_scales = [&](const Tile& t) {
@@ -562,22 +565,29 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 ok = copy_scales(tile_at(tile + tile_step, j + 1));
                 if (!ok) break;
             }
-            for (; s < s_hi; s += kTurns) {
-                ok = ready || mbar_wait_for(&empty[st], phase, kWaitMx);
+            for (; u < tile_units; u += kTurns) {
+                ok = ready || mbar_wait_for(&empty[un], phase, kWaitMx);
                 if (!ok) break;
-                const uint32_t dst = ring + st * a.stage_bytes, now = st;
+                const uint32_t now = un;
                 advance(kTurns);
-                ready = mbar_ready(&empty[st], phase);
+                ready = mbar_ready(&empty[un], phase);
                 if (leader) {
-                    mbar_arrive_expect_tx(&full[now], bytes);
-                    tma3d(dst, &wmap, s * (kK / 2), t.r0, t.e, &full[now], w_policy);
-                    for (int b = 0; b < n_box; ++b)
-                        tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
-                              s * (kK / 2), t.t0 + b * a.box, &full[now], keep);
+                    const int s0 = s_lo + u * kP, n_s = min(kP, s_hi - s0);
+                    mbar_arrive_expect_tx(&full[now], n_s * bytes);
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) {
+                        if (i == n_s) break;
+                        const uint32_t dst = ring + (now * kP + i) * a.stage_bytes;
+                        const int x = (s0 + i) * (kK / 2);
+                        tma3d(dst, &wmap, x, t.r0, t.e, &full[now], w_policy);
+                        for (int b = 0; b < n_box; ++b)
+                            tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap, x,
+                                  t.t0 + b * a.box, &full[now], keep);
+                    }
                 }
                 __syncwarp();
             }
-            s -= s_hi - s_lo;   // stages of the next tile before this warp's turn
+            u -= tile_units;   // units of the next tile before this warp's turn
             ok = ok && !*abort_flag;
         }
         if (!ok) fail();
@@ -590,14 +600,13 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         const uint32_t ring = smem_u32(smem);
         const uint64_t op0 = operand_desc(ring), sf0 = scale_desc(smem_u32(sf_buf));
         const uint32_t stage16 = a.stage_bytes >> 4;   // descriptors count 16 bytes
-        const uint32_t n_stages = static_cast<uint32_t>(a.n_stages);
-        uint32_t st = 0, phase = 0;
+        uint32_t un = 0, phase = 0;
         uint32_t group = 0;   // (split) kAhead stages sharing a scale slot
         int j = 0;
         bool ok = true;
-        auto next_of = [&](uint32_t& stage, uint32_t& parity) {
-            if (++stage == n_stages) {
-                stage = 0;
+        auto next_of = [&](uint32_t& unit, uint32_t& parity) {
+            if (++unit == n_units) {
+                unit = 0;
                 parity ^= 1u;
             }
         };
@@ -611,55 +620,72 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                                    kWaitMx);
             fence_after_mx();
             const uint32_t d = tmem + ab * a.tn;
-            // four MMAs of K = 64 and the stage's release; the last stage of a row may hold fewer
-            auto issue = [&](int s, uint32_t stage) {
-                const uint32_t sfa = sf_cols + stage * sf_stage, sfb = sfa + 8u;
-                const uint32_t sfb2 = sfb + 4u * NB;
-                const uint64_t ad = op0 + stage * stage16, bd = ad + (kABytes >> 4);
-                const int kk_end = (a.gpr - s * kGroupsStage + 1) / 2;
-                umma_mxf4(d, ad, bd, id0, sfa, sfb, s > s_lo ? 1u : 0u);
-                if (kk_end > 1) umma_mxf4(d, ad + 2, bd + 2, id2, sfa, sfb, 1u);
-                if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
-                if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
-                umma_commit_mx(&empty[stage]);
+            // four MMAs of K = 64 a stage and the unit's release; the last stage of a row may
+            // hold fewer
+            auto issue = [&](int s0, uint32_t unit) {
+#pragma unroll
+                for (int i = 0; i < kP; ++i) {
+                    const int s = s0 + i;
+                    if (i > 0 && s >= s_hi) break;
+                    const uint32_t stage = unit * kP + i;
+                    const uint32_t sfa = sf_cols + stage * sf_stage, sfb = sfa + 8u;
+                    const uint32_t sfb2 = sfb + 4u * NB;
+                    const uint64_t ad = op0 + stage * stage16, bd = ad + (kABytes >> 4);
+                    const int kk_end = (a.gpr - s * kGroupsStage + 1) / 2;
+                    umma_mxf4(d, ad, bd, id0, sfa, sfb, s > s_lo ? 1u : 0u);
+                    if (kk_end > 1) umma_mxf4(d, ad + 2, bd + 2, id2, sfa, sfb, 1u);
+                    if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
+                    if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
+                }
+                umma_commit_mx(&empty[unit]);
             };
             for (int s = s_lo; s < s_hi && ok;) {
-                const uint32_t st0 = st, phase0 = phase;
-                next_of(st, phase);
+                const uint32_t u0 = un, phase0 = phase;
+                next_of(un, phase);
                 if constexpr (kSplit) {
                     const uint32_t q = static_cast<uint32_t>(s - s_lo) % kAhead, slot = group & 1u;
                     if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
-                    ok = ok && mbar_wait_for(&full[st0], phase0, kWaitMx);
+                    ok = ok && mbar_wait_for(&full[u0], phase0, kWaitMx);
                     if (!ok) break;
                     fence_after_mx();
-                    const bool last = q == kAhead - 1 || s + 1 == s_hi;
+                    const bool last = q + kP == kAhead || s + kP >= s_hi;
                     if (leader) {
-                        scales_to_tmem<NB>(sf_cols + st0 * sf_stage,
-                                                  sf0 + ((slot * kSfSlot + q * kSfStage) >> 4));
-                        issue(s, st0);
+#pragma unroll
+                        for (int i = 0; i < kP; ++i)
+                            if (i == 0 || s + i < s_hi)
+                                scales_to_tmem<NB>(sf_cols + (u0 * kP + i) * sf_stage,
+                                                   sf0 + ((slot * kSfSlot + (q + i) * kSfStage) >> 4));
+                        issue(s, u0);
                         if (last) umma_commit_mx(&sf_empty[slot]);
                     }
                     __syncwarp();
                     group += last ? 1u : 0u;
-                    ++s;
+                    s += kP;
+                } else if constexpr (kP > 1) {
+                    ok = mbar_wait_for(&full[u0], phase0, kWaitMx);
+                    if (!ok) break;
+                    fence_after_mx();
+                    if (leader) issue(s, u0);
+                    __syncwarp();
+                    s += kP;
                 } else {
                     // two stages at a time where the second is there too: their polls overlap
-                    const uint32_t st1 = st, phase1 = phase;
+                    const uint32_t u1 = un, phase1 = phase;
                     bool both = s + 1 < s_hi;
-                    const bool there = mbar_ready(&full[st1], phase1);
-                    ok = mbar_wait_for(&full[st0], phase0, kWaitMx);
+                    const bool there = mbar_ready(&full[u1], phase1);
+                    ok = mbar_wait_for(&full[u0], phase0, kWaitMx);
                     if (!ok) break;
                     both = __all_sync(0xFFFFFFFFu, both && there);
                     fence_after_mx();
                     if (both) {
-                        next_of(st, phase);
+                        next_of(un, phase);
                         if (leader) {
-                            issue(s, st0);
-                            issue(s + 1, st1);
+                            issue(s, u0);
+                            issue(s + 1, u1);
                         }
                         s += 2;
                     } else {
-                        if (leader) issue(s, st0);
+                        if (leader) issue(s, u0);
                         ++s;
                     }
                     __syncwarp();
@@ -678,41 +704,43 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         // --- scales from shared to tensor memory, as far ahead as the ring goes
         const bool leader = elect_one();
         const uint64_t sf0 = scale_desc(smem_u32(sf_buf));
-        const uint32_t n_stages = static_cast<uint32_t>(a.n_stages);
-        uint32_t st = 0, phase = 1, group = 0;
+        uint32_t un = 0, phase = 1, group = 0;
         bool ok = true;
-        auto copy = [&](uint32_t stage, uint32_t slot, uint32_t q) {
-            scales_to_tmem<NB>(sf_cols + stage * sf_stage,
-                                      sf0 + ((slot * kSfSlot + q * kSfStage) >> 4));
-            umma_commit_mx(&full[stage]);
+        auto copy = [&](uint32_t unit, uint32_t slot, int q, int n_q) {
+#pragma unroll
+            for (int i = 0; i < kP; ++i)
+                if (i == 0 || q + i < n_q)
+                    scales_to_tmem<NB>(sf_cols + (unit * kP + i) * sf_stage,
+                                       sf0 + ((slot * kSfSlot + (q + i) * kSfStage) >> 4));
+            umma_commit_mx(&full[unit]);
         };
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead, ++group) {
                 const uint32_t slot = group & 1u;
                 const int n_q = min(kAhead, s_hi - s0);
                 ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
-                for (int q = 0; q < n_q && ok;) {   // two stages at a time, as the MMAs
-                    const uint32_t st0 = st, phase0 = phase;
-                    if (++st == n_stages) {
-                        st = 0;
+                for (int q = 0; q < n_q && ok;) {   // two units at a time, as the MMAs
+                    const uint32_t u0 = un, phase0 = phase;
+                    if (++un == n_units) {
+                        un = 0;
                         phase ^= 1u;
                     }
-                    bool both = mbar_ready(&empty[st], phase);
-                    ok = mbar_wait_for(&empty[st0], phase0, kWaitMx);
+                    bool both = mbar_ready(&empty[un], phase);
+                    ok = mbar_wait_for(&empty[u0], phase0, kWaitMx);
                     if (!ok) break;
-                    both = __all_sync(0xFFFFFFFFu, both && q + 1 < n_q);
+                    both = __all_sync(0xFFFFFFFFu, both && q + kP < n_q);
                     fence_after_mx();
                     if (leader) {
-                        copy(st0, slot, q);
-                        if (both) copy(st, slot, q + 1);
-                        if (q + (both ? 2 : 1) == n_q) umma_commit_mx(&sf_empty[slot]);
+                        copy(u0, slot, q, n_q);
+                        if (both) copy(un, slot, q + kP, n_q);
+                        if (q + (both ? 2 * kP : kP) >= n_q) umma_commit_mx(&sf_empty[slot]);
                     }
                     __syncwarp();
-                    if (both && ++st == n_stages) {
-                        st = 0;
+                    if (both && ++un == n_units) {
+                        un = 0;
                         phase ^= 1u;
                     }
-                    q += both ? 2 : 1;
+                    q += both ? 2 * kP : kP;
                 }
             }
             ok = ok && !*abort_flag;
@@ -902,17 +930,17 @@ int sm_count() {
 
 constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 2048;   // (the static arrays)
 
-template <typename T, bool kSplit, int NB>
+template <typename T, bool kSplit, int NB, int kP>
 cudaError_t launch_k(const CUtensorMap& wmap, const CUtensorMap& xmap, const MxArgs& a, T* Y,
                      unsigned grid, unsigned cluster, size_t smem, cudaStream_t s) {
     static PerDevice memo;
     const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
-        return static_cast<int>(cudaFuncSetAttribute(k_mx_mm<T, kSplit, NB>,
+        return static_cast<int>(cudaFuncSetAttribute(k_mx_mm<T, kSplit, NB, kP>,
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                      static_cast<int>(kSmemMax - kSmemSlack)));
     }));
     if (attr_err != cudaSuccess) return attr_err;
-    return launch_after(k_mx_mm<T, kSplit, NB>, dim3(grid),
+    return launch_after(k_mx_mm<T, kSplit, NB, kP>, dim3(grid),
                         static_cast<unsigned>(Roles<kSplit>::kThreads), smem, s, cluster, wmap,
                         xmap, a, Y);
 }
@@ -1004,6 +1032,12 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     if (split > 1) a.n_stages = std::min(a.n_stages, (a.n_steps + 1) / 2 / split * 2 + 2);
     const int sf_cols = 8 + 8 * sf_blocks;
     a.n_stages = std::min(a.n_stages, (512 / (split > 1 ? per_sm : 1) - n_acc * a.tn) / sf_cols);
+    // Units of two stages (one barrier each way for both) where three of them fit, or a slice
+    // of a split tile has two (us: 4096x14336, 8 tokens 9.4, single stages 10.1; 4096x4096, 128
+    // tokens 7.2, single 7.7; with one unit a slice, 4096x4096, one token, 5.4, single 5.15)
+    const bool pairs = sf_blocks == 1 && (split > 1 ? a.n_stages >= 4 && a.n_steps >= 4 * split
+                                                    : a.n_stages >= 6);
+    if (pairs) a.n_stages &= ~1;
     a.tmem_cols = tmem_columns(n_acc * a.tn + a.n_stages * sf_cols);
     if (a.n_stages < 1) return cudaErrorNotSupported;
     // A CTA that waits for tensor memory must not hold up a cluster: an unsplit CTA takes
@@ -1030,8 +1064,9 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
         auto launch = [&](auto kernel_launch) {
             return kernel_launch(wmap, xmap, a, y, grid, cluster, smem, s);
         };
-        if (split > 1) return launch(launch_k<T, true, 1>);
-        return sf_blocks == 1 ? launch(launch_k<T, false, 1>) : launch(launch_k<T, false, 2>);
+        if (split > 1) return pairs ? launch(launch_k<T, true, 1, 2>) : launch(launch_k<T, true, 1, 1>);
+        if (sf_blocks == 2) return launch(launch_k<T, false, 2, 1>);
+        return pairs ? launch(launch_k<T, false, 1, 2>) : launch(launch_k<T, false, 1, 1>);
     };
     return y_type == kTypeF32 ? go(static_cast<float*>(Y)) : go(static_cast<__nv_bfloat16*>(Y));
 }
