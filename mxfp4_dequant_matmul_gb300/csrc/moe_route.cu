@@ -354,8 +354,8 @@ cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_row
         const FastDiv div(static_cast<uint32_t>(per_row));
         return over_rows(n_rows, per_row, [&](uint32_t row0, uint32_t units) {
             return launch_after(k_moe_dispatch<P>, dim3(blocks_of(units, kUnits<P>)), kRThreads, 0,
-                                s, 1, static_cast<const P*>(x), n_tokens, row0, units, div, token_at,
-                                static_cast<P*>(xs));
+                                s, 1, static_cast<const P*>(x), n_tokens, row0, units, div,
+                                token_at, static_cast<P*>(xs));
         });
     });
 }

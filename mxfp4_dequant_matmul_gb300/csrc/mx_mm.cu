@@ -12,16 +12,23 @@
 // elements: one ring stage, four MMAs of K = 64).  Scale bytes lie row-major with a
 // row stride of cols/32 bytes, which no copy engine can turn into the layout the
 // tensor core wants (32 lanes x 16 bytes: byte 4j + b of lane l is group b of row l +
-// 32j), so warps of their own take them 32 bytes a row (four stages) and store them in that layout,
-// and tcgen05.cp moves them to tensor memory ahead of each stage's MMAs.  A slot of four
-// stages is handed over at a time: the proxy fence and the barriers cost several hundred
-// cycles, more than a stage has when few tokens stream through.
+// 32j), so warps of their own take them 32 bytes a row (four stages) and store them in
+// that layout, and tcgen05.cp moves them to tensor memory ahead of each stage's MMAs.  A
+// slot of four stages is handed over at a time: the proxy fence and the barriers cost
+// several hundred cycles, more than a stage has when few tokens stream through.
 //
-// One warp issues the copies, one the MMAs, two or three handle the scales, four or eight
-// read finished accumulators (two, in turn) and store them.  Persistent: CTA c
-// takes tiles c, c + grid, ...  With few tokens the tiles are too few to fill the SMs;
-// then a cluster of CTAs shares a tile, each a slice of K, and adds the partial sums
-// through distributed shared memory in rank order.
+// Warps have roles: copies, MMAs, scales, and the reading and storing of finished
+// accumulators (two, in turn).  Persistent: CTA c takes tiles c, c + grid, ...  With few
+// tokens the tiles are too few to fill the SMs; then a cluster of CTAs shares a tile, each
+// a slice of K, and adds the partial sums through distributed shared memory in rank order.
+//
+// What bounds it: many experts with few rows each, HBM (64 experts 2880x2880, 32 tokens,
+// top-4: 38 us, 6.5 TB/s).  Elsewhere the chain of barriers between the roles: without
+// copies, MMAs, scales and stores it took 420 cycles a stage of 256 columns (one barrier
+// for two stages now, where they fit), and a stage's copies, its MMAs (257 cycles at 128
+// tokens) and the last tile's stores are hidden behind it only in part.  One token
+// 14336x4096 7.0 us (weights from L2 in part); 2048 tokens 4096x4096 22.8 us, 3.0
+// PFLOP/s; 4096 tokens 4.2 PFLOP/s; 2048 tokens, top-4 of 64 experts 2880x2880, 66.7 us.
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land,
 // frees its tensor memory and returns.
@@ -312,9 +319,10 @@ __device__ __forceinline__ void store_scales(const Scales<kAhead>& s, int q, uin
 }
 
 // 32 outputs (TMEM lanes; `valid` of them exist) of every other 16 of n tokens (columns of
-// `src`, from c0) to y, tokens `pitch` elements apart.  FP32: a store is one token's 128 bytes.  BF16, even
-// pitch: lanes trade so that each holds four consecutive outputs of four tokens, and a
-// store is four tokens' 64 bytes (a store of two bytes a lane costs as much for a quarter).
+// `src`, from c0) to y, tokens `pitch` elements apart.  FP32: a store is one token's 128
+// bytes.  BF16, pitch a multiple of four: lanes trade so that each holds four consecutive
+// outputs of four tokens, and a store is four tokens' 64 bytes (a store of two bytes a lane
+// costs as much for a quarter).
 template <typename T>
 __device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int c0, int n,
                                            uint32_t src, int lane) {
@@ -456,11 +464,11 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     const int n_tiles = __shfl_sync(0xFFFFFFFFu, n_tiles_sh, 0);
     // (split) slices of whole pairs of stages, so that 16-byte scale loads stay aligned
     const int pairs = (a.n_steps + 1) / 2;
-    const int s_lo = kSplit ? 2 * static_cast<int>(static_cast<long long>(pairs) * rank / n_rank) : 0;
-    const int s_hi =
-        kSplit ? min(a.n_steps,
-                     2 * static_cast<int>(static_cast<long long>(pairs) * (rank + 1) / n_rank))
-               : a.n_steps;
+    auto slice = [&](int r) {
+        return 2 * static_cast<int>(static_cast<long long>(pairs) * r / n_rank);
+    };
+    const int s_lo = kSplit ? slice(rank) : 0;
+    const int s_hi = kSplit ? min(a.n_steps, slice(rank + 1)) : a.n_steps;
     // a cluster's tiles (split: one)
     const int tile0 = static_cast<int>(blockIdx.x) / n_rank;
     const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x) / n_rank;
@@ -653,8 +661,9 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
 #pragma unroll
                         for (int i = 0; i < kP; ++i)
                             if (i == 0 || s + i < s_hi)
-                                scales_to_tmem<NB>(sf_cols + (u0 * kP + i) * sf_stage,
-                                                   sf0 + ((slot * kSfSlot + (q + i) * kSfStage) >> 4));
+                                scales_to_tmem<NB>(
+                                    sf_cols + (u0 * kP + i) * sf_stage,
+                                    sf0 + ((slot * kSfSlot + (q + i) * kSfStage) >> 4));
                         issue(s, u0);
                         if (last) umma_commit_mx(&sf_empty[slot]);
                     }
@@ -748,8 +757,8 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         if (!ok) fail();
         __syncwarp();
     } else if (warp >= 2 && warp < 3 + NB) {
-        // --- scales of W (warp 2) or of 128 tokens of X (warps 3, 4), loaded four to eight stages ahead of
-        // their use and across tiles
+        // --- scales of W (warp 2) or of 128 tokens of X (warps 3, 4), loaded four to eight
+        // stages ahead of their use and across tiles
         const bool is_w = warp == 2;
         const int block = is_w ? 0 : warp - 3;
         const uint32_t second = kSfChunk * static_cast<uint32_t>(is_w ? 1 : NB);
@@ -773,7 +782,8 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 if (!ok) return;
                 const uint8_t* rows = sc_buf + static_cast<size_t>(buf) * a.sc_bytes;
                 if (!is_w)
-                    rows += a.sc_w + (static_cast<uint32_t>(static_cast<size_t>(ft.t0) * a.gpr) & 15u);
+                    rows += a.sc_w +
+                            (static_cast<uint32_t>(static_cast<size_t>(ft.t0) * a.gpr) & 15u);
                 load_scales<true>(r, rows, a.gpr, g0, 128 * block, row_end - row0, lane);
             } else {
                 const uint8_t* plane =
@@ -798,8 +808,9 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
             for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead) {
                 fetch(nxt);
                 const uint32_t slot = group & 1u;
-                ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_for(&sf_empty[slot],
-                                                                 ((group >> 1) & 1u) ^ 1u, kWaitMx));
+                ok = ok && __all_sync(0xFFFFFFFFu,
+                                      mbar_wait_for(&sf_empty[slot], ((group >> 1) & 1u) ^ 1u,
+                                                    kWaitMx));
                 if (!ok) break;
 #pragma unroll
                 for (int q = 0; q < kAhead; ++q)   // (stages past the tile's end: not read)
@@ -1017,8 +1028,10 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * 128u;
     const int n_acc = split > 1 ? 1 : 2;
     const size_t sf_bytes = 2u * (split > 1 ? 2 : 4) * 2u * kSfChunk * (1 + sf_blocks);
-    const size_t extra = sf_bytes + (split > 1 ? static_cast<size_t>(a.tn) * kM * 4
-                                   : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8 : 0);
+    const size_t extra =
+        sf_bytes + (split > 1            ? static_cast<size_t>(a.tn) * kM * 4
+                    : offsets != nullptr ? static_cast<size_t>(n_experts + 1) * 8
+                                         : 0);
     // Whole scale rows of a tile by bulk copies, two tiles deep, where rows of a tile are short
     // enough; else (long rows, slices of a split tile) loads a few stages ahead.
     if (split == 1 && static_cast<long>(kM + a.tn) * a.gpr <= 32 * 1024 - 64) {
@@ -1046,7 +1059,8 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
     // per KB at most) and none shares an SM with a kernel that takes them all.
     const size_t ring = static_cast<size_t>(a.n_stages) * a.stage_bytes +
                         static_cast<size_t>(a.n_sc) * a.sc_bytes + extra + 1024;
-    const size_t smem = split > 1 ? max(ring, static_cast<size_t>(40 * 1024)) : kSmemMax - kSmemSlack;
+    const size_t smem =
+        split > 1 ? std::max(ring, static_cast<size_t>(40 * 1024)) : kSmemMax - kSmemSlack;
     CUtensorMap wmap, xmap;
     if (!code_map(&wmap, bank, cols, rows, n_experts, stride, kM) ||
         !code_map(&xmap, xq, cols, n_rows, 0, 16, a.box))
@@ -1064,7 +1078,8 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
         auto launch = [&](auto kernel_launch) {
             return kernel_launch(wmap, xmap, a, y, grid, cluster, smem, s);
         };
-        if (split > 1) return pairs ? launch(launch_k<T, true, 1, 2>) : launch(launch_k<T, true, 1, 1>);
+        if (split > 1)
+            return pairs ? launch(launch_k<T, true, 1, 2>) : launch(launch_k<T, true, 1, 1>);
         if (sf_blocks == 2) return launch(launch_k<T, false, 2, 1>);
         return pairs ? launch(launch_k<T, false, 1, 2>) : launch(launch_k<T, false, 1, 1>);
     };

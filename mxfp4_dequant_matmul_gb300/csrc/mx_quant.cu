@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(kQThreads)
 // The same for aligned 16-bit rows, on the raw halves: with 16 bits an element the steps above
 // issue about 160 instructions per 8 elements, twice what HBM leaves time for.  Here amax is a
 // packed integer maximum of the magnitudes, and the rounded value is put together from the
-// code ([7996, 2880] bfloat16 gathered from 1999 rows, with the rounded values: 12.6 us, 5.5
-// TB/s; the steps above took 24.6).  For bfloat16 its two bytes by permutation out of a table of the eight magnitudes, x's
-// sign, and one packed product with the scale (a power of two, exact); for half the
-// hardware's E2M1 decode and two packed products, as 2^(k-127) alone may be below half's
-// range although the value is not.
+// code.  For bfloat16: its two bytes by permutation out of a table of the eight magnitudes, x's
+// sign, and one packed product with the scale (a power of two, exact); for half the hardware's
+// E2M1 decode and two packed products, as 2^(k-127) alone may be below half's range although
+// the value is not.  [7996, 2880] bfloat16 gathered from 1999 rows, with the rounded values:
+// 12.6 us, 5.5 TB/s (the steps above took 24.6).
 template <typename T>
 __device__ __forceinline__ uint4 rounded_values(uint32_t word, const uint32_t (&raw)[4],
                                                 uint32_t k);

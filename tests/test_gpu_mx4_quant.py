@@ -196,3 +196,33 @@ def test_swiglu_nonfinite(mx):
     mx.mxfp4_swiglu_quant(gate.cuda(), up.cuda(), 4, 32, 32, out)
     # row 1: silu(0) * inf = NaN; row 2: -inf / (1 + inf) = NaN
     assert host(out)[64:68].tolist() == [255, 255, 255, 0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("up_exp", [0, 60, 126])
+def test_swiglu_far_gates(mx, dtype, up_exp):
+    """Gates whose exponential is tiny, subnormal or nothing, under large ups: silu must fade out
+    through exp's whole range, not end early.  Beside the relative 2^-20 an exponential below
+    2^-126 is off by up to 2^-149."""
+    far = [-60.0, -80.0, -86.0, -87.0, -88.0, -88.5, -89.0, -92.0, -96.0, -100.0, -104.0, -200.0]
+    gate = torch.tensor(far).repeat_interleave(64).reshape(len(far), 64).to(dtype)
+    up = (torch.linspace(-1.9, 1.9, 64).repeat(len(far), 1) * 2.0**up_exp).to(dtype)
+    out = torch.zeros(ref.nbytes(len(far), 64), dtype=torch.uint8, device="cuda:0")
+    mx.mxfp4_swiglu_quant(gate.cuda(), up.cuda(), len(far), 64, 64, out)
+    g, u = gate.double().numpy(), up.double().numpy()
+    act = g / (1 + np.exp(-g)) * u
+    slack = np.abs(act) * 2.0**-20 + np.abs(g * u) * 2.0**-149 + 2.0**-149
+    o = host(out)
+    n = gate.numel()
+    byte = o[:n // 2].reshape(len(far), 32)
+    code = np.empty((len(far), 64), np.uint8)
+    code[:, 0::2], code[:, 1::2] = byte & 15, byte >> 4
+    k = o[n // 2:n * 17 // 32].reshape(len(far), 2)
+    # as above, on magnitudes (a result that may be zero may have either sign)
+    lo = ref.quantise(np.maximum(np.abs(act) - slack, 0.0))
+    hi = ref.quantise(np.abs(act) + slack)
+    assert ((k >= lo[1]) & (k <= hi[1])).all()
+    sure = np.repeat(lo[1] == hi[1], 32, axis=1)
+    mag = code & 7
+    assert ((mag >= lo[0]) & (mag <= hi[0]))[sure].all()
+    assert sure[:4].all()
