@@ -325,10 +325,10 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 
 // silu(gate) * up of aligned 16-bit rows: items as k_mx_quant16's, the act in FP32.  Bound by
 // issue (about 20 instructions an element, two of them on the special-function unit; HBM leaves
-// time for 16): [8192, 2880] bfloat16 19.8 us, 5.4 TB/s, against 29.7 us with 8 elements a
-// thread and exact divisions.
+// time for 16): [8192, 2880] bfloat16 18.9 us, 5.6 TB/s (19.7 with the 36 registers it takes if
+// it may), against 29.7 us with 8 elements a thread and exact divisions.
 template <typename T, bool kValues>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, 8)
     k_mx_swiglu16(const T* __restrict__ gate, const T* __restrict__ up, long long ld, float limit,
                   uint32_t row0, uint32_t items, FastDiv per_row, uint2* __restrict__ codes,
                   uint8_t* __restrict__ scales, T* __restrict__ values) {
