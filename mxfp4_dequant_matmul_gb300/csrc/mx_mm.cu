@@ -1052,7 +1052,11 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
                                                     : a.n_stages >= 6);
     if (pairs) a.n_stages &= ~1;
     a.tmem_cols = tmem_columns(n_acc * a.tn + a.n_stages * sf_cols);
-    if (a.n_stages < 1) return cudaErrorNotSupported;
+    // As many units as copy warps at least: a warp asks about its next unit with one parity bit,
+    // which must not answer for the round before.  (The shapes above leave three stages or more
+    // unsplit.)
+    const int copiers = split > 1 ? Roles<true>::kCopiers : Roles<false>::kCopiers;
+    if (a.n_stages / (pairs ? 2 : 1) < copiers) return cudaErrorNotSupported;
     // A CTA that waits for tensor memory must not hold up a cluster: an unsplit CTA takes
     // its SM's whole shared memory (and all 512 columns), and a split CTA at least 40 KB,
     // so that the columns of those that fit an SM together never exceed 512 (2.2 columns
