@@ -24,6 +24,8 @@
 namespace mxk {
 namespace {
 
+// These kernels do not let the next launch start early: what they write may be the weights of
+// an overlapped mxfp4_mv, which reads weights before it waits (and nothing was gained by it).
 constexpr int kQThreads = 256;
 
 // Two floats -> the byte of their E2M1 codes, `lo` in the low nibble; four such
@@ -130,7 +132,6 @@ __global__ void __launch_bounds__(kQThreads)
                const int32_t* __restrict__ row_of, float limit, uint32_t row0, uint32_t items,
                FastDiv per_row, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
                T* __restrict__ values) {
-    pdl_trigger();
     pdl_wait();
     const uint32_t i0 = blockIdx.x * (kQThreads * kU) + threadIdx.x;
     const size_t first = static_cast<size_t>(row0) * per_row.d;   // items of earlier launches
@@ -263,7 +264,6 @@ __global__ void __launch_bounds__(kQThreads)
                  const int32_t* __restrict__ row_of, uint32_t row0, uint32_t items,
                  FastDiv per_row, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                  T* __restrict__ values) {
-    pdl_trigger();
     pdl_wait();
     const uint32_t i0 = blockIdx.x * (kQThreads * kU) + threadIdx.x;
     const size_t first = static_cast<size_t>(row0) * per_row.d + i0;
@@ -332,7 +332,6 @@ __global__ void __launch_bounds__(kQThreads, 8)
     k_mx_swiglu16(const T* __restrict__ gate, const T* __restrict__ up, long long ld, float limit,
                   uint32_t row0, uint32_t items, FastDiv per_row, uint2* __restrict__ codes,
                   uint8_t* __restrict__ scales, T* __restrict__ values) {
-    pdl_trigger();
     pdl_wait();
     const uint32_t i = blockIdx.x * kQThreads + threadIdx.x;
     uint32_t rg[8] = {}, ru[8] = {};

@@ -226,3 +226,36 @@ def test_swiglu_far_gates(mx, dtype, up_exp):
     mag = code & 7
     assert ((mag >= lo[0]) & (mag <= hi[0]))[sure].all()
     assert sure[:4].all()
+
+
+def test_weights_quantised_ahead_of_an_overlapped_matvec(mx):
+    """mxfp4_mv with launch overlap reads weights before it waits for the kernel ahead of it: a
+    quantiser that writes them, directly ahead or with another launch between, has to be done."""
+    rows, cols = 4096, 4096
+    g = torch.Generator(device="cuda").manual_seed(3)
+    ws = [torch.randn(rows, cols, generator=g, device="cuda") for _ in range(4)]
+    x = torch.randn(cols, generator=g, device="cuda")
+    w = torch.zeros(ref.nbytes(rows, cols), dtype=torch.uint8, device="cuda:0")
+    xq = torch.zeros(ref.nbytes(1, cols), dtype=torch.uint8, device="cuda:0")
+    y4 = torch.zeros(1, rows, device="cuda")
+    mx.mxfp4_quant(x, 1, cols, cols, None, 1, xq)
+    want, got = [torch.zeros(rows, device="cuda") for _ in ws], []
+    for v, y in zip(ws, want):
+        mx.mxfp4_quant(v, rows, cols, cols, None, rows, w)
+        torch.cuda.synchronize()
+        mx.mxfp4_mv(w, rows, cols, x, y)
+    torch.cuda.synchronize()
+    mx.mxfp4_set_launch_overlap(True)
+    try:
+        for i in range(24):
+            y = torch.zeros(rows, device="cuda")
+            mx.mxfp4_quant(ws[i % 4], rows, cols, cols, None, rows, w)
+            if i % 8 >= 4:
+                mx.mxfp4_mm_mx(w, rows, cols, xq, 1, y4)
+            mx.mxfp4_mv(w, rows, cols, x, y)
+            got.append(y)
+        torch.cuda.synchronize()
+    finally:
+        mx.mxfp4_set_launch_overlap(False)
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 4]), i
