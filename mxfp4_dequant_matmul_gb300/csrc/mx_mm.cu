@@ -27,8 +27,8 @@
 // copies, MMAs, scales and stores it took 420 cycles a stage of 256 columns (one barrier
 // for two stages now, where they fit), and a stage's copies, its MMAs (257 cycles at 128
 // tokens) and the last tile's stores are hidden behind it only in part.  One token
-// 14336x4096 7.0 us (weights from L2 in part); 2048 tokens 4096x4096 22.8 us, 3.0
-// PFLOP/s; 4096 tokens 4.2 PFLOP/s; 2048 tokens, top-4 of 64 experts 2880x2880, 66.7 us.
+// 14336x4096 7.0 us (weights from L2 in part); 2048 tokens 4096x4096 21.8 us, 3.2
+// PFLOP/s; 4096 tokens 37.5 us, 3.7; 2048 tokens, top-4 of 64 experts 2880x2880, 66.7 us.
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land,
 // frees its tensor memory and returns.
@@ -60,8 +60,8 @@ constexpr int kGroupsStage = kK / kGroup;   // 8 scale bytes a row
 // stage whatever it does: a copy holds its registers for some 200 cycles after it is issued,
 // a poll answers after 100.  One copy warp for both operands needs 700, so three take the
 // stages in turn.  The epilogue has each TMEM lane quarter once, or twice: a warp's stores
-// wait for each other, 33 MB of FP32 results took 18.5 us by four warps an SM and 12.4 us by
-// eight.
+// wait for each other (33 MB of FP32 results, 128 bytes a store: 18.5 us by four warps an SM,
+// 12.4 us by eight).
 template <bool kSplit>
 struct Roles {
     static constexpr int kToTmem = 6, kCopiers = kSplit ? 1 : 3;
@@ -319,19 +319,43 @@ __device__ __forceinline__ void store_scales(const Scales<kAhead>& s, int q, uin
 }
 
 // 32 outputs (TMEM lanes; `valid` of them exist) of every other 16 of n tokens (columns of
-// `src`, from c0) to y, tokens `pitch` elements apart.  FP32: a store is one token's 128
-// bytes.  BF16, pitch a multiple of four: lanes trade so that each holds four consecutive
-// outputs of four tokens, and a store is four tokens' 64 bytes (a store of two bytes a lane
-// costs as much for a quarter).
+// `src`, from c0) to y, tokens `pitch` elements apart.  Where the pitch is a multiple of four,
+// lanes trade so that each holds four consecutive outputs of four tokens, and a store is four
+// tokens' 64 (BF16) or 128 bytes: a store costs about the same whatever a lane gives it (FP32,
+// 3000 tokens 8192x1024: 26.0 us, with one token's 128 bytes a store 35.9).
 template <typename T>
 __device__ __forceinline__ void store_tile(T* y, int pitch, int valid, int c0, int n,
                                            uint32_t src, int lane) {
     if (valid <= 0) return;
-    const bool quads = sizeof(T) == 2 && (pitch & 3) == 0 && valid == 32;
+    const bool quads = (pitch & 3) == 0 && valid == 32;
     for (int c = c0; c < n; c += 32) {
         uint32_t v[16];
         tmem_ld16(src + c, v);
-        if (quads) {
+        if (quads && sizeof(T) == 4) {
+            // lane pair (l, l ^ 1): both rows of columns 0..7 (even) or 8..15
+            float2 a[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t give = (lane & 1) ? v[i] : v[i + 8];
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, 1);
+                a[i].x = __uint_as_float((lane & 1) ? got : v[i]);
+                a[i].y = __uint_as_float((lane & 1) ? v[i + 8] : got);
+            }
+            // lane pair (l, l ^ 2): rows 0..3 of the quad for half of the eight columns
+            const int col0 = (lane & 1) * 8 + ((lane & 2) ? 4 : 0);
+            T* dst = y + static_cast<size_t>(c + col0) * pitch + (lane & ~3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 give = (lane & 2) ? a[i] : a[i + 4];
+                float2 got;
+                got.x = __shfl_xor_sync(0xFFFFFFFFu, give.x, 2);
+                got.y = __shfl_xor_sync(0xFFFFFFFFu, give.y, 2);
+                const float2 lo = (lane & 2) ? got : a[i], hi = (lane & 2) ? a[i + 4] : got;
+                if (c + col0 + i < n)
+                    *reinterpret_cast<float4*>(dst + static_cast<size_t>(i) * pitch) =
+                        make_float4(lo.x, lo.y, hi.x, hi.y);
+            }
+        } else if (quads) {
             // columns as BF16 pairs of this lane's row: u[i] = (column i, column i + 8)
             uint32_t u[8];
 #pragma unroll
@@ -998,9 +1022,9 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
         a.tn = std::min((n_rows + 15) / 16 * 16, kMaxTokens);
         if (n_rows > 64) {
             // token tiles: the fewest rounds of tiles over the SMs x columns per tile (and 32
-            // for what a tile costs by itself).  Within 3 % of the best width from 32 to 208 on
-            // eleven shapes swept, e.g. 4096x4096, 512 tokens: 128 columns 9.3 us (64: 12.2,
-            // 208: 11.3); 4096 tokens: 192 columns 32.9 us (128: 37.3)
+            // for what a tile costs by itself).  Within 4 % of the best width from 64 to 208 on
+            // eleven shapes swept, e.g. 4096x4096, 512 tokens: 128 columns 9.6 us (64: 11.3,
+            // 208: 11.7); 4096 tokens: 192 columns 37.5 us (128: 39.5)
             long best = -1;
             for (int tn = 32; tn <= kMaxTokens; tn += 16) {
                 const long tiles = static_cast<long>(a.n_rt) * ((n_rows + tn - 1) / tn);
