@@ -71,6 +71,7 @@ struct Roles {
 constexpr uint32_t kABytes = kM * kK / 2;
 constexpr uint32_t kSfChunk = 512;          // scale bytes of 128 rows x 4 groups
 constexpr int kMaxStages = 10;
+constexpr int kMaxSplit = 8;                // CTAs of a cluster sharing a tile
 constexpr int kTileTable = 64;              // this CTA's first tiles, worked out at the start
 constexpr int kMaxTokens = 208;             // two accumulators and the scales in 512 columns
 constexpr long long kWaitMx = 1ll << 32, kDrainMx = 1ll << 24;   // SM cycles: about 2 s and 8 ms
@@ -897,8 +898,13 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         for (int i = rank * Roles<kSplit>::kThreads + tid; i < n_out && !*abort_flag;
              i += n_rank * Roles<kSplit>::kThreads) {
             const int r = t.r0 + (i & (kM - 1)), tok = t.t0 + i / kM;
-            float sum = 0.0f;
-            for (int q = 0; q < n_rank; ++q) sum += cluster.map_shared_rank(part, q)[i];
+            float v[kMaxSplit], sum = 0.0f;   // all loads on their way before the first sum
+#pragma unroll
+            for (int q = 0; q < kMaxSplit; ++q)
+                v[q] = cluster.map_shared_rank(part, q < n_rank ? q : rank)[i];
+#pragma unroll
+            for (int q = 0; q < kMaxSplit; ++q)
+                if (q < n_rank) sum += v[q];
             if (r < a.rows) Y[static_cast<size_t>(tok) * a.rows + r] = from_f32<T>(sum);
         }
         cluster.sync();   // no rank leaves while its sums are being read
@@ -1040,7 +1046,7 @@ cudaError_t launch_mx_mm(const uint8_t* bank, int n_experts, int rows, int cols,
             // 8.0 unsplit, 6.2 split by 4, 6.0 by 8; 2880x2880, 4 tokens 7.4, 6.8, 5.9;
             // 8192x8192, 16 tokens 12.6, 10.7 by 4, 16.2 by 8; with 112 row tiles, 14336x4096,
             // 8.4 unsplit, 9.4 by 2)
-            while (split < 8 && 3 * a.n_rt < 2 * sms && a.n_rt * split * 2 <= 2 * sms &&
+            while (split < kMaxSplit && 3 * a.n_rt < 2 * sms && a.n_rt * split * 2 <= 2 * sms &&
                    split * 2 <= a.n_steps)
                 split *= 2;
             per_sm = std::min(4, (a.n_rt * split + sms - 1) / sms);
