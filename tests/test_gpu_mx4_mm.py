@@ -284,3 +284,34 @@ def test_many_experts(mx):
         part = slice(off[e], off[e + 1])
         wv = ref.values(*banks[e])
         check(got[part], xv[part] @ wv.T, np.abs(xv[part]) @ np.abs(wv).T, torch.float32)
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 7, 8, 9, 17, 32, 33])
+@pytest.mark.parametrize("copies,nb", [(1, 3), (100, 5), (1, 40), (1, 130), (2, 200)])
+def test_every_end_of_a_row_of_stages(mx, steps, copies, nb):
+    # rows of K that end in the first or the second stage of a unit, short of a stage or at its
+    # end, in slices of a split tile and (many rows, many tokens) in whole ones; sums exact in
+    # any order.  The same 130 rows `copies` times.
+    rng = np.random.default_rng(steps * 1000 + nb)
+    for short in (0, 32, 224):
+        cols, rows = 256 * steps - short, 130 * copies
+        w = ref.random_matrix(rng, 130, cols, 127, 128)
+        x = ref.random_matrix(rng, nb, cols, 127, 128)
+        one, n = ref.pack(*w), 130 * cols
+        many = np.zeros(ref.nbytes(rows, cols), np.uint8)
+        many[:rows * cols // 2] = np.tile(one[:n // 2], copies)
+        many[rows * cols // 2:rows * cols * 17 // 32] = np.tile(one[n // 2:n * 17 // 32], copies)
+        y = torch.zeros(nb, rows, device="cuda:0")
+        mx.mxfp4_mm_mx(to_dev(many), rows, cols, to_dev(ref.pack(*x)), nb, y)
+        assert np.array_equal(host(y), np.tile(both(w, x)[0], (1, copies)))
+
+
+@pytest.mark.parametrize("rows", [128, 132, 156, 160, 188, 252, 254, 255])
+@pytest.mark.parametrize("nb", [65, 97, 209])
+def test_stores_of_every_width(mx, rows, nb):
+    # FP32 and BF16 results in units of four rows where the row count allows it, else one by one
+    rng = np.random.default_rng(rows + nb)
+    w, x = ref.random_matrix(rng, rows, 96, 127, 128), ref.random_matrix(rng, nb, 96, 127, 128)
+    want, l1 = both(w, x)
+    assert np.array_equal(product(mx, w, x), want)
+    check(product(mx, w, x, torch.bfloat16), want, l1, torch.bfloat16, "bf16")
