@@ -9,6 +9,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "pdl.cuh"
+
 namespace mxk {
 
 __device__ __forceinline__ float to_f32(float v) { return v; }
@@ -61,18 +63,13 @@ struct Pack {
     }
 };
 
-// One load or store of a pack; data that is read once does not stay in L1.
+// One load (of what a kernel ahead may have written) or store of a pack; 32-byte units, each
+// read once, do not stay in L1.
 template <typename P>
 __device__ __forceinline__ P load_pack(const P* p) {
     P v;
-    if constexpr (sizeof(P) == 32) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(v.raw.w[0]), "=r"(v.raw.w[1]), "=r"(v.raw.w[2]), "=r"(v.raw.w[3]),
-                       "=r"(v.raw.w[4]), "=r"(v.raw.w[5]), "=r"(v.raw.w[6]), "=r"(v.raw.w[7])
-                     : "l"(p));
-    } else {
-        v.raw = __ldg(&p->raw);
-    }
+    if constexpr (sizeof(P) == 32) ld_dep_stream32(p, v.raw.w);
+    else v.raw = ld_dep(&p->raw);
     return v;
 }
 template <typename P>

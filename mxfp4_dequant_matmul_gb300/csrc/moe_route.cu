@@ -31,7 +31,7 @@ constexpr int kMaxExperts = 1024;
 constexpr int kSortCluster = 8;
 
 __global__ void __launch_bounds__(kSortThreads)
-    k_moe_sort(const int32_t* __restrict__ ids, int n_pairs, int top_k, int n_experts, int run,
+    k_moe_sort(const int32_t* ids, int n_pairs, int top_k, int n_experts, int run,
                int32_t* __restrict__ token_at, int32_t* __restrict__ pos_of,
                int32_t* __restrict__ offsets) {
     pdl_trigger();
@@ -52,9 +52,9 @@ __global__ void __launch_bounds__(kSortThreads)
     const int lo = static_cast<int>(min(p0, static_cast<long long>(n_pairs)));
     const int hi = static_cast<int>(min(p0 + run, static_cast<long long>(n_pairs)));
     // the ids of the run's first 32 pairs (all of it, often) stay in a register
-    const int id0 = lo + lane < hi ? __ldg(ids + lo + lane) : -1;
+    const int id0 = lo + lane < hi ? ld_dep(ids + lo + lane) : -1;
     auto id_of = [&](int p) {
-        const int id = p == lo ? id0 : p + lane < hi ? __ldg(ids + p + lane) : -1;
+        const int id = p == lo ? id0 : p + lane < hi ? ld_dep(ids + p + lane) : -1;
         return id >= 0 && id < n_experts ? id : -1;
     };
     for (int e = lane; e < n_experts; e += 32) mine[e] = 0;
@@ -160,8 +160,8 @@ constexpr int kUnits = sizeof(P) < 32 ? 4 : 1;
 // xs[i] = x[token_at[i]].
 template <typename P>
 __global__ void __launch_bounds__(kRThreads)
-    k_moe_dispatch(const P* __restrict__ x, int n_tokens, uint32_t row0, uint32_t units,
-                   FastDiv per_row, const int32_t* __restrict__ token_at, P* __restrict__ xs) {
+    k_moe_dispatch(const P* x, int n_tokens, uint32_t row0, uint32_t units,
+                   FastDiv per_row, const int32_t* token_at, P* __restrict__ xs) {
     pdl_trigger();
     pdl_wait();
     constexpr int kU = kUnits<P>;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kRThreads)
     for (int u = 0; u < kU; ++u) {
         const uint32_t i = i0 + u * kRThreads;
         const uint32_t row = per_row.of(i);
-        const int t = i < units ? __ldg(token_at + row0 + row) : -1;
+        const int t = i < units ? ld_dep(token_at + row0 + row) : -1;
         v[u].raw = {};
         if (t >= 0 && t < n_tokens)
             v[u] = load_pack(x + static_cast<size_t>(t) * per_row.d + (i - row * per_row.d));
@@ -187,9 +187,9 @@ __global__ void __launch_bounds__(kRThreads)
 // rows in flight.
 template <typename T, int N>
 __global__ void __launch_bounds__(kRThreads)
-    k_moe_gather_sum(const Pack<T, N>* __restrict__ o, int n_rows, int top_k, uint32_t row0,
-                     uint32_t units, FastDiv per_row, const int32_t* __restrict__ pos_of,
-                     const float* __restrict__ w, Pack<T, N>* __restrict__ y) {
+    k_moe_gather_sum(const Pack<T, N>* o, int n_rows, int top_k, uint32_t row0,
+                     uint32_t units, FastDiv per_row, const int32_t* pos_of,
+                     const float* w, Pack<T, N>* __restrict__ y) {
     pdl_trigger();
     pdl_wait();
     const uint32_t i = blockIdx.x * kRThreads + threadIdx.x;
@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(kRThreads)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool in = j0 + j < top_k;
-            pos[j] = in ? __ldg(pos_of + p0 + j0 + j) : -1;
-            wt[j] = in && w != nullptr ? __ldg(w + p0 + j0 + j) : 1.0f;
+            pos[j] = in ? ld_dep(pos_of + p0 + j0 + j) : -1;
+            wt[j] = in && w != nullptr ? ld_dep(w + p0 + j0 + j) : 1.0f;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(kRThreads)
 // unit of dy read once for the four.
 template <typename T, int N>
 __global__ void
-    k_moe_combine_grad(const Pack<T, N>* __restrict__ dy, const Pack<T, N>* __restrict__ o,
-                       int n_rows, int top_k, int per_row, const int32_t* __restrict__ pos_of,
-                       const float* __restrict__ w, Pack<T, N>* __restrict__ d_o,
+    k_moe_combine_grad(const Pack<T, N>* dy, const Pack<T, N>* o,
+                       int n_rows, int top_k, int per_row, const int32_t* pos_of,
+                       const float* w, Pack<T, N>* __restrict__ d_o,
                        float* __restrict__ d_w) {
     pdl_trigger();
     pdl_wait();
@@ -247,9 +247,9 @@ __global__ void
         float wt[4], acc[4] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            pos[j] = j0 + j < top_k ? __ldg(pos_of + p + j) : -1;
+            pos[j] = j0 + j < top_k ? ld_dep(pos_of + p + j) : -1;
             if (pos[j] >= n_rows) pos[j] = -1;
-            wt[j] = pos[j] >= 0 ? __ldg(w + p + j) : 0.0f;
+            wt[j] = pos[j] >= 0 ? ld_dep(w + p + j) : 0.0f;
         }
         for (int c = threadIdx.x; c < per_row; c += blockDim.x) {
             const Pack<T, N> a = load_pack(dy + t * per_row + c);

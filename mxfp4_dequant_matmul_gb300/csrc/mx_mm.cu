@@ -243,7 +243,7 @@ struct Scales {
 template <bool kShared, typename V>
 __device__ __forceinline__ V load_word(const V* p) {
     if constexpr (kShared) return *p;
-    else return __ldg(p);
+    else return ld_dep(p);
 }
 template <bool kShared, int kAhead>
 __device__ __forceinline__ void load_scales(Scales<kAhead>& s, const uint8_t* plane, int gpr,
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
     if (a.offsets != nullptr) {
         pdl_wait();
         for (int e = tid; e <= a.n_experts; e += Roles<kSplit>::kThreads)
-            off[e] = min(max(__ldg(a.offsets + e), 0), a.n_rows);
+            off[e] = min(max(ld_dep(a.offsets + e), 0), a.n_rows);
         __syncthreads();
         if (warp == 0) {   // first[e]: tiles of the experts before e
             int base = 0;

@@ -49,7 +49,7 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
 #pragma unroll
         for (int q = 0; q < 8 / kN; ++q) {
             Pack<T, kN> a;
-            a.raw = ldg_stream(reinterpret_cast<const uint4*>(p) + q);
+            a.raw = ld_dep_stream(reinterpret_cast<const uint4*>(p) + q);
             float f[kN];
             a.get(f);
 #pragma unroll
@@ -57,7 +57,12 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(p[i]);
+        for (int i = 0; i < 8; ++i) {
+            Pack<T, 1> a = load_pack(reinterpret_cast<const Pack<T, 1>*>(p + i));
+            float f[1];
+            a.get(f);
+            v[i] = f[0];
+        }
     }
 }
 
@@ -107,7 +112,7 @@ __device__ __forceinline__ void load_item(float (&v)[8], const T* x, const T* up
     const uint32_t c = (i - r * per_row.d) * 8;
     long long src = static_cast<long long>(row0) + r;
     if (row_of != nullptr) {
-        src = __ldg(row_of + src);
+        src = ld_dep(row_of + src);
         if (src < 0 || src >= x_rows) return;
     }
     load8<T, kVec>(x + src * ld + c, v);
@@ -128,8 +133,8 @@ __device__ __forceinline__ void load_item(float (&v)[8], const T* x, const T* up
 // apart, all loaded before the first is quantised.
 template <typename T, bool kAct, bool kVec, int kU>
 __global__ void __launch_bounds__(kQThreads)
-    k_mx_quant(const T* __restrict__ x, const T* __restrict__ up, int x_rows, long long ld,
-               const int32_t* __restrict__ row_of, float limit, uint32_t row0, uint32_t items,
+    k_mx_quant(const T* x, const T* up, int x_rows, long long ld,
+               const int32_t* row_of, float limit, uint32_t row0, uint32_t items,
                FastDiv per_row, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
                T* __restrict__ values) {
     pdl_wait();
@@ -244,13 +249,6 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-__device__ __forceinline__ void ldg_stream32(const void* p, uint32_t (&v)[8]) {
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
-                   "=r"(v[6]), "=r"(v[7])
-                 : "l"(p));
-}
-
 __device__ __forceinline__ void stg32(void* p, const uint4& a, const uint4& b) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y),
                  "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
@@ -260,8 +258,8 @@ __device__ __forceinline__ void stg32(void* p, const uint4& a, const uint4& b) {
 // An item is 16 elements (32 bytes, one access), two lanes a group.
 template <typename T, int kU, bool kValues>
 __global__ void __launch_bounds__(kQThreads)
-    k_mx_quant16(const T* __restrict__ x, int x_rows, long long ld,
-                 const int32_t* __restrict__ row_of, uint32_t row0, uint32_t items,
+    k_mx_quant16(const T* x, int x_rows, long long ld,
+                 const int32_t* row_of, uint32_t row0, uint32_t items,
                  FastDiv per_row, uint2* __restrict__ codes, uint8_t* __restrict__ scales,
                  T* __restrict__ values) {
     pdl_wait();
@@ -276,9 +274,9 @@ __global__ void __launch_bounds__(kQThreads)
         if (i < items) {
             const uint32_t r = per_row.of(i);
             int src = static_cast<int>(row0 + r);
-            if (row_of != nullptr) src = __ldg(row_of + src);
+            if (row_of != nullptr) src = ld_dep(row_of + src);
             if (src >= 0 && src < x_rows)
-                ldg_stream32(x + src * ld + (i - r * per_row.d) * 16, raw[u]);
+                ld_dep_stream32(x + src * ld + (i - r * per_row.d) * 16, raw[u]);
         }
     }
 #pragma unroll
@@ -329,7 +327,7 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 // it may), against 29.7 us with 8 elements a thread and exact divisions.
 template <typename T, bool kValues>
 __global__ void __launch_bounds__(kQThreads, 8)
-    k_mx_swiglu16(const T* __restrict__ gate, const T* __restrict__ up, long long ld, float limit,
+    k_mx_swiglu16(const T* gate, const T* up, long long ld, float limit,
                   uint32_t row0, uint32_t items, FastDiv per_row, uint2* __restrict__ codes,
                   uint8_t* __restrict__ scales, T* __restrict__ values) {
     pdl_wait();
@@ -338,8 +336,8 @@ __global__ void __launch_bounds__(kQThreads, 8)
     if (i < items) {
         const uint32_t r = per_row.of(i);
         const size_t at = static_cast<size_t>(row0 + r) * ld + (i - r * per_row.d) * 16;
-        ldg_stream32(gate + at, rg);
-        ldg_stream32(up + at, ru);
+        ld_dep_stream32(gate + at, rg);
+        ld_dep_stream32(up + at, ru);
     }
     float2 v[8];
     float top = 0.0f;

@@ -5,7 +5,14 @@
 // completed and its writes are visible, so a kernel that touches no global memory before it
 // (kernel parameters aside) behaves as if launched normally.  pdl_trigger() lets the next
 // launch do the same: it takes effect when every CTA of this grid has called it or ended.
+//
+// Such a kernel reads global memory by ld_dep(), plain loads that pdl_wait() orders behind
+// the kernel ahead.  Not by ld.global.nc (__ldg, or what the compiler may make of a const
+// __restrict__ pointer): that form is defined only for memory that nobody writes while the
+// kernel lives, and here it lives, waiting, while the kernel ahead writes what it will read.
 #pragma once
+
+#include <cstdint>
 
 #include <cuda_runtime.h>
 
@@ -16,6 +23,49 @@ __device__ __forceinline__ void pdl_wait() {
 }
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+__device__ __forceinline__ uint16_t ld_dep(const uint16_t* p) {
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_dep(const uint32_t* p) {
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int32_t ld_dep(const int32_t* p) {
+    return static_cast<int32_t>(ld_dep(reinterpret_cast<const uint32_t*>(p)));
+}
+__device__ __forceinline__ float ld_dep(const float* p) {
+    return __uint_as_float(ld_dep(reinterpret_cast<const uint32_t*>(p)));
+}
+__device__ __forceinline__ uint2 ld_dep(const uint2* p) {
+    uint2 v;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_dep(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+// Data that is read once does not stay in L1.
+__device__ __forceinline__ uint4 ld_dep_stream(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void ld_dep_stream32(const void* p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
 }
 
 template <typename... P, typename... A>
