@@ -368,12 +368,12 @@ __global__ void __launch_bounds__(kThreads) k_moe_pass(const Bank bank0, const B
 // in the bf16 mode the route weights are in the acts already and the sum of
 // the o's is rounded to bfloat16 (dsv4_global_down_mxfp4).  Pairs the plan left
 // out (invalid or cold) add nothing.
-__global__ void __launch_bounds__(256) k_moe_combine(const float* __restrict__ o_pairs,
-                                                     const int32_t* __restrict__ pair_slot,
-                                                     const float* __restrict__ route_w,
-                                                     int bf16, int n_tokens, int top_k,
-                                                     int hidden, float* __restrict__ y) {
-    // launched dependent on the down pass: its per-pair outputs after it completes
+__global__ void __launch_bounds__(256) k_moe_combine(const float* o_pairs,
+                                                     const int32_t* pair_slot,
+                                                     const float* route_w, int bf16, int n_tokens,
+                                                     int top_k, int hidden, float* y) {
+    // launched dependent on the down pass: its per-pair outputs after it completes (by plain
+    // loads: no const __restrict__, see pdl.cuh)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const size_t n = static_cast<size_t>(n_tokens) * hidden;
     for (size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(256) k_moe_combine(const float* __restrict__ o
         for (int j = 0; j < top_k; ++j) {
             const size_t p = t * top_k + j;
             if (pair_slot[p] < 0) continue;
-            const float o = __ldg(o_pairs + p * hidden + r);
-            acc = bf16 ? __fadd_rn(acc, o) : __fmaf_rn(__ldg(route_w + p), o, acc);
+            const float o = o_pairs[p * hidden + r];
+            acc = bf16 ? __fadd_rn(acc, o) : __fmaf_rn(route_w[p], o, acc);
         }
         y[i] = bf16 ? moe_bf16(acc) : acc;
     }

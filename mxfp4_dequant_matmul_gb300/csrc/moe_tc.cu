@@ -43,6 +43,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 
 namespace mxk {
 namespace {
@@ -105,7 +106,7 @@ __device__ __forceinline__ uint32_t pack_f16x2_e(float lo, float hi) {
 // that the pass launched after this kernel also sees the previous kernel done.
 constexpr int kSplitItems = (kGMaxE * 4 + kSplitThreads - 1) / kSplitThreads;
 
-__global__ void __launch_bounds__(kSplitThreads) k_moe_split(const float* __restrict__ vec,
+__global__ void __launch_bounds__(kSplitThreads) k_moe_split(const float* vec,
                                                              int n_vec, int cols,
                                                              uint8_t* __restrict__ frag,
                                                              int wait_first) {
@@ -130,8 +131,8 @@ __global__ void __launch_bounds__(kSplitThreads) k_moe_split(const float* __rest
             const int i = threadIdx.x + u * kSplitThreads;
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
             if (i < n_items) {
-                a = __ldg(src + 2 * i);
-                b = __ldg(src + 2 * i + 1);
+                a = ld_dep(src + 2 * i);
+                b = ld_dep(src + 2 * i + 1);
             }
             f[u][0] = a.x; f[u][1] = a.y; f[u][2] = a.z; f[u][3] = a.w;
             f[u][4] = b.x; f[u][5] = b.y; f[u][6] = b.z; f[u][7] = b.w;
@@ -215,7 +216,7 @@ template <int NM>
 __global__ void __launch_bounds__(kThreadsE, 1)
     k_moe_tc(const __grid_constant__ BankMaps tm0, const __grid_constant__ BankMaps tm1,
              const Bank bank0, const Bank bank1, int rows, int cols, int top_k, int n_experts,
-             const uint8_t* __restrict__ frag, PlanRef plan, MoeAct epi, float* __restrict__ out) {
+             const uint8_t* frag, PlanRef plan, MoeAct epi, float* __restrict__ out) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -275,9 +276,9 @@ __global__ void __launch_bounds__(kThreadsE, 1)
             const int u = 2 * tid + k;
             eu[k] = bu[k] = nu[k] = cu[k] = 0;
             if (u < n_touched) {
-                eu[k] = __ldg(plan.touched + u);
-                bu[k] = __ldg(plan.offsets + eu[k]);
-                nu[k] = __ldg(plan.offsets + eu[k] + 1) - bu[k];
+                eu[k] = ld_dep(plan.touched + u);
+                bu[k] = ld_dep(plan.offsets + eu[k]);
+                nu[k] = ld_dep(plan.offsets + eu[k] + 1) - bu[k];
                 cu[k] = (nu[k] + kTokSeg - 1) / kTokSeg * n_blocks;
             }
         }
@@ -647,10 +648,10 @@ __global__ void __launch_bounds__(kThreadsE, 1)
             if (tid == 0 && la_s < n_seg && la_step < 2) {
                 if (la_step == 0) {
                     while (segst[la_u + 1] <= la_s) ++la_u;
-                    la_e = __ldg(plan.touched + la_u);
+                    la_e = ld_dep(plan.touched + la_u);
                 } else {
-                    la_b0 = __ldg(plan.offsets + la_e);
-                    la_b1 = __ldg(plan.offsets + la_e + 1);
+                    la_b0 = ld_dep(plan.offsets + la_e);
+                    la_b1 = ld_dep(plan.offsets + la_e + 1);
                 }
                 ++la_step;
             }
@@ -665,11 +666,11 @@ __global__ void __launch_bounds__(kThreadsE, 1)
             if (la_s < n_seg) {
                 if (la_step < 1) {
                     while (segst[la_u + 1] <= la_s) ++la_u;
-                    la_e = __ldg(plan.touched + la_u);
+                    la_e = ld_dep(plan.touched + la_u);
                 }
                 if (la_step < 2) {
-                    la_b0 = __ldg(plan.offsets + la_e);
-                    la_b1 = __ldg(plan.offsets + la_e + 1);
+                    la_b0 = ld_dep(plan.offsets + la_e);
+                    la_b1 = ld_dep(plan.offsets + la_e + 1);
                 }
                 segmeta[bi * 8 + 0] = la_u;
                 segmeta[bi * 8 + 1] = la_e;

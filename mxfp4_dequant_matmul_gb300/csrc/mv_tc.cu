@@ -54,6 +54,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pdl.cuh"
 
 namespace mxk {
 namespace {
@@ -150,7 +151,7 @@ __host__ __device__ inline MvLayout mv_layout(int NT, int ng_max, int ru_cta, in
 template <int NT, int CL>
 __global__ void __launch_bounds__(kThreadsM, 1)
     k_mv_tc(const __grid_constant__ CUtensorMap tmap, const uint8_t* __restrict__ w, int rows,
-            int cols, const float* __restrict__ X, int nb, float* __restrict__ Y, int ru_cta,
+            int cols, const float* X, int nb, float* __restrict__ Y, int ru_cta,
             int ng_max, int stages, int overlap) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreadsM, 1)
                 const float4* src = reinterpret_cast<const float4*>(
                     X + static_cast<size_t>(t0 + tok) * cols + static_cast<size_t>(g_lo) * kGroup +
                     8 * rem);
-                const float4 a = __ldg(src), b = __ldg(src + 1);
+                const float4 a = ld_dep(src), b = ld_dep(src + 1);
                 xv[u][0] = a.x; xv[u][1] = a.y; xv[u][2] = a.z; xv[u][3] = a.w;
                 xv[u][4] = b.x; xv[u][5] = b.y; xv[u][6] = b.z; xv[u][7] = b.w;
             } else {

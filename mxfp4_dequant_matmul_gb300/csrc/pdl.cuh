@@ -25,6 +25,7 @@ __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Loads of what a kernel ahead may have written, after pdl_wait().
 __device__ __forceinline__ uint16_t ld_dep(const uint16_t* p) {
     uint16_t v;
     asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
@@ -52,6 +53,11 @@ __device__ __forceinline__ uint4 ld_dep(const uint4* p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
+}
+__device__ __forceinline__ float4 ld_dep(const float4* p) {
+    const uint4 v = ld_dep(reinterpret_cast<const uint4*>(p));
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                       __uint_as_float(v.w));
 }
 // Data that is read once does not stay in L1.
 __device__ __forceinline__ uint4 ld_dep_stream(const uint4* p) {
