@@ -64,8 +64,8 @@ int mxfp4_quant(const void* x, int type, int x_rows, int cols, long long ld,
  * FP32 (the act of mxfp4_moe_gate_up, to within 2^-20 of itself and, where exp(gate)
  * is subnormal, 2^-149 |gate up|): gate and up [rows, cols] of `type`, rows ld
  * elements apart.  swiglu_limit > 0 clamps up to
- * [-limit, limit] and gate to at most limit first; 0 turns the clamp off; NaN is
- * refused. */
+ * [-limit, limit] and gate to at most limit first (a NaN of either stays one); 0 or
+ * less turns the clamp off; NaN is refused. */
 int mxfp4_swiglu_quant(const void* gate, const void* up, int type, int rows, int cols,
                        long long ld, float swiglu_limit, void* out, void* values,
                        cudaStream_t stream);

@@ -88,8 +88,8 @@ __device__ __forceinline__ float2 swiglu(float2 g, float2 u, float limit) {
     if (limit > 0.0f) {
         u.x = u.x < -limit ? -limit : (u.x > limit ? limit : u.x);
         u.y = u.y < -limit ? -limit : (u.y > limit ? limit : u.y);
-        g.x = g.x < limit ? g.x : limit;
-        g.y = g.y < limit ? g.y : limit;
+        g.x = g.x > limit ? limit : g.x;   // (a NaN stays)
+        g.y = g.y > limit ? limit : g.y;
     }
     const float2 e = make_float2(expf(-fabsf(g.x)), expf(-fabsf(g.y)));
     float2 r = __fadd2_rn(e, make_float2(1.0f, 1.0f));

@@ -259,3 +259,26 @@ def test_weights_quantised_ahead_of_an_overlapped_matvec(mx):
         mx.mxfp4_set_launch_overlap(False)
     for i, y in enumerate(got):
         assert torch.equal(y, want[i % 4]), i
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("ld", [64, 67])
+def test_swiglu_nonfinite_under_a_limit(mx, dtype, ld):
+    """A NaN gate or up is no larger than any limit: its group is NaN.  Infinities are clamped,
+    but for a gate of -inf (-inf / (1 + inf) = NaN).  Aligned rows and others."""
+    nan, inf, rows = float("nan"), float("inf"), 8
+    gate, up = (torch.ones(rows, ld, dtype=dtype) for _ in range(2))
+    gate[0, 1], gate[1, 40], up[2, 31], up[3, 32] = nan, -nan, nan, -nan
+    gate[4, 0], up[5, 0], up[6, 0], gate[7, 63] = inf, inf, -inf, -inf
+    out = torch.zeros(ref.nbytes(rows, 64), dtype=torch.uint8, device="cuda:0")
+    values = torch.zeros(rows, 64, dtype=dtype, device="cuda:0")
+    mx.mxfp4_swiglu_quant(gate.cuda(), up.cuda(), rows, 64, ld, out, values, swiglu_limit=2.0)
+    k = host(out)[rows * 32:rows * 34].reshape(rows, 2)
+    bad = np.zeros((rows, 2), bool)
+    bad[[0, 1, 2, 3, 7], [0, 1, 0, 1, 1]] = True
+    assert np.array_equal(k == 255, bad)
+    v = values.double().cpu().numpy()
+    assert np.array_equal(np.isnan(v), np.repeat(bad, 32, axis=1))
+    assert not host(out)[:rows * 32].reshape(rows, 2, 16)[bad].any()   # codes of a NaN group: 0
+    # silu(2) and silu(1) * 2 lie in [1, 2): scale 2^-2, so they are 1.7616 / 0.25 -> 6 and 1.4621 / 0.25 -> 6
+    assert v[4, 0] == 1.5 and v[5, 0] == 1.5 and v[6, 0] == -1.5
