@@ -252,7 +252,8 @@ int mxfp4_moe_down(const void* down_bank, int n_experts, int hidden, int inter,
  *   mxg_bf16), act = bf16(w_tj * silu(g) * u) -- the route weight folded into
  *   the act -- and y[t] = bf16(sum_j o_tj) with o = down . act.
  * swiglu_limit > 0 (either mode): u is clamped to [-limit, limit] and g to at
- *   most limit before SiLU; 0 turns the clamp off; NaN is refused.
+ *   most limit before SiLU (a NaN of either stays one); 0 or less turns the clamp
+ *   off; NaN is refused.
  * A shared expert is one more slot of every token: give it a bank slot, an id
  * and route weight 1 (the page's frame routes its shared slot so).
  * Error bound: see the oracle's mxo_moe_forward_ex (FP32 dot products within

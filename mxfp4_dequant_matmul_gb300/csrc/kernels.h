@@ -70,7 +70,7 @@ __device__ __forceinline__ float moe_act(float g, float u, const MoeAct& epi, in
     if (epi.limit > 0.0f) {
         const float lim = epi.limit;
         u = u < -lim ? -lim : (u > lim ? lim : u);
-        g = g < lim ? g : lim;
+        g = g > lim ? lim : g;   // (a NaN of either stays one)
     }
     float a = __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
     if (epi.bf16) a = moe_bf16(__fmul_rn(__ldg(epi.route_w + pair), a));

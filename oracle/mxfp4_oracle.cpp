@@ -367,7 +367,7 @@ void mxo_moe_forward_ex(const uint8_t* gate_bank, const uint8_t* up_bank,
                     if (std::fabs(u) - lim > eu) eu = 0.0;
                     if (g - lim > eg) eg = 0.0;
                     u = u < -lim ? -lim : (u > lim ? lim : u);
-                    g = g < lim ? g : lim;
+                    g = g > lim ? lim : g;   // (a NaN of either stays one)
                 }
                 const double sg = mxo_silu(g);
                 double av = sg * u;

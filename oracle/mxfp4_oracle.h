@@ -136,7 +136,7 @@ void mxo_moe_forward(const uint8_t* gate_bank, const uint8_t* up_bank,
  * Per valid pair p = t*top_k + j with slot s and route weight w:
  *   g = gate_s . x_t, u = up_s . x_t                   (double)
  *   bf16 mode: g = bf16(g), u = bf16(u)                 (mxg_bf16 of the float)
- *   limit > 0: u = clamp(u, -limit, limit), g = min(g, limit)
+ *   limit > 0: u = clamp(u, -limit, limit), g = min(g, limit); a NaN stays NaN
  *   a = silu(g) * u; bf16 mode: a = bf16(w * a)         (route weight folded in)
  *   o_p = down_s . a                                    (double)
  *   out[t] = sum_j w_j o_p (generic) or bf16(sum_j o_p) (bf16 mode), slots in order.
