@@ -315,3 +315,38 @@ def test_stores_of_every_width(mx, rows, nb):
     want, l1 = both(w, x)
     assert np.array_equal(product(mx, w, x), want)
     check(product(mx, w, x, torch.bfloat16), want, l1, torch.bfloat16, "bf16")
+
+
+def stated_bound(cols):
+    """The error bound of include/mx4.h, in units of sum |W X|."""
+    import os
+    import re
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "mx4.h")) as f:
+        add, power = re.search(r"\(cols / 64 \+ (\d+)\) \* 2\^-(\d+) \* sum_c", f.read()).groups()
+    return (cols / 64 + int(add)) * 2.0**-int(power)
+
+
+@pytest.mark.parametrize("cols", [4096, 32768])
+@pytest.mark.parametrize("nb", [2, 70])
+def test_sums_with_a_dominant_first_block(mx, cols, nb):
+    # an element of 1, then 64 columns at a time that come to 63/64 of a last bit of the sum (2^-23):
+    # every addition may lose all of it.  Row 0: one sign; 1: the rest negative; 2: signs in turn;
+    # 3: an element of 1 at each eighth of the row, where slices of a split row begin; 4: as row 0
+    # with 3/4 of a last bit.
+    wc, wk = np.zeros((5, cols), np.uint8), np.full((5, cols // 32), 127 - 29, np.uint8)
+    for r, (n, sign) in enumerate([(63, "+"), (63, "-"), (63, "+-"), (63, "+"), (48, "+")]):
+        block = np.zeros(64, np.uint8)
+        block[:n] = 2
+        blocks = np.tile(block, (cols // 64, 1))
+        blocks[(slice(None) if sign == "-" else slice(1, None, 2)) if "-" in sign else slice(0)] |= 8
+        blocks = np.where(blocks == 8, 0, blocks)
+        for b in range(0, cols // 64, cols // 512 if r == 3 else cols):
+            blocks[b], wk[r, 2 * b:2 * b + 2] = 0, 127
+            blocks[b, 0] = 2
+        wc[r] = blocks.reshape(-1)
+    w, x = (wc, wk), (np.full((nb, cols), 2, np.uint8), np.full((nb, cols // 32), 127, np.uint8))
+    want, l1 = both(w, x)
+    bound = stated_bound(cols)
+    assert (np.abs(product(mx, w, x) - want) <= bound * l1).all()
+    # the input is one that tells the bound from half of it: what an unsplit row can lose
+    assert want[0, 0] - 1 > bound / 2
