@@ -359,11 +359,33 @@ def q4k_mm(w, rows, cols, X, nb, Y, stream=None):
 # --- microscaled 4-bit activations and their routing (include/mx4.h) -------------
 #
 # A call takes the GPU about as long as the host when there are few tokens, so each function
-# first tries the plain case, tensors of one dtype on torch's current stream, without the
-# helpers (a call 4.0 -> 3.6 us); anything else goes through them.
+# first tries the plain case, tensors of the right dtypes on torch's current stream, without the
+# helpers (a call 4.0 -> 3.6 us); anything else goes through them.  Index tensors have to be
+# int32 and route weights float32 whatever the dense arguments' type: the kernels would read
+# other ones as something else, or past their end.
 
 _TYPE_OF = {}
+_INT32 = _FLOAT32 = None       # torch's, from the first call on
 _NOT_PLAIN = (AttributeError, KeyError, TypeError, ctypes.ArgumentError)   # before the call
+
+
+def _dtypes():
+    global _INT32, _FLOAT32
+    import torch
+    _TYPE_OF.update({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
+                     torch.float16: TYPE_F16})
+    _INT32, _FLOAT32 = torch.int32, torch.float32
+
+
+def _refuse_other_than(fn, wanted, *tensors):
+    """Raises (status 1) where a tensor's dtype is not the one wanted; None and addresses pass."""
+    if not _TYPE_OF:
+        _dtypes()
+    wanted = _INT32 if wanted == "int32" else _FLOAT32
+    for t in tensors:
+        dtype = getattr(t, "dtype", None)
+        if dtype is not None and dtype is not wanted:
+            raise Mxfp4Error(fn, 1)
 
 
 def _type(given, *tensors):
@@ -372,9 +394,7 @@ def _type(given, *tensors):
     if given is not None:
         return given
     if not _TYPE_OF:
-        import torch
-        _TYPE_OF.update({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
-                         torch.float16: TYPE_F16})
+        _dtypes()
     code = None
     for t in tensors:
         dtype = getattr(t, "dtype", None)
@@ -391,6 +411,8 @@ def mxfp4_quant(x, x_rows, cols, ld, row_of, rows, out, values=None, type=None, 
     """x (x_rows rows, ld elements apart) or its rows row_of -> the MXFP4 matrix out [rows, cols];
     type (TYPE_*) defaults to x's dtype, which values shares."""
     try:
+        if row_of is not None and row_of.dtype is not _INT32:
+            raise TypeError
         dtype = x.dtype
         status = _lib.mxfp4_quant(
             x.data_ptr(),
@@ -400,6 +422,7 @@ def mxfp4_quant(x, x_rows, cols, ld, row_of, rows, out, values=None, type=None, 
             None if values is None else values.data_ptr(),
             _current_stream() if stream is None else _stream(stream))
     except _NOT_PLAIN:
+        _refuse_other_than("mxfp4_quant", "int32", row_of)
         status = lib().mxfp4_quant(
             _addr(x), _type(type, x, values), x_rows, cols, ld, _addr(row_of), rows, _addr(out),
             _addr(values), _stream(stream))
@@ -444,11 +467,14 @@ def mxfp4_moe_mm_mx(bank, n_experts, rows, cols, xq, n_rows, offsets, Y, y_type=
                     stream=None):
     """Each expert's rows offsets[e] .. offsets[e+1] of xq with that expert's matrix."""
     try:
+        if offsets.dtype is not _INT32:
+            raise TypeError
         status = _lib.mxfp4_moe_mm_mx(
             bank.data_ptr(), n_experts, rows, cols, xq.data_ptr(), n_rows, offsets.data_ptr(),
             Y.data_ptr(), _TYPE_OF[Y.dtype] if y_type is None else y_type,
             _current_stream() if stream is None else _stream(stream))
     except _NOT_PLAIN:
+        _refuse_other_than("mxfp4_moe_mm_mx", "int32", offsets)
         status = lib().mxfp4_moe_mm_mx(
             _addr(bank), n_experts, rows, cols, _addr(xq), n_rows, _addr(offsets), _addr(Y),
             _type(y_type, Y), _stream(stream))
@@ -460,11 +486,15 @@ def mxfp4_moe_sort(expert_ids, n_tokens, top_k, n_experts, token_at, pos_of, off
                    stream=None):
     """Pairs (token, choice) -> rows in expert order, and back."""
     try:
+        if (expert_ids.dtype is not _INT32 or token_at.dtype is not _INT32 or
+                pos_of.dtype is not _INT32 or offsets.dtype is not _INT32):
+            raise TypeError
         status = _lib.mxfp4_moe_sort(
             expert_ids.data_ptr(), n_tokens, top_k, n_experts, token_at.data_ptr(),
             pos_of.data_ptr(), offsets.data_ptr(),
             _current_stream() if stream is None else _stream(stream))
     except _NOT_PLAIN:
+        _refuse_other_than("mxfp4_moe_sort", "int32", expert_ids, token_at, pos_of, offsets)
         status = lib().mxfp4_moe_sort(
             _addr(expert_ids), n_tokens, top_k, n_experts, _addr(token_at), _addr(pos_of),
             _addr(offsets), _stream(stream))
@@ -475,12 +505,15 @@ def mxfp4_moe_sort(expert_ids, n_tokens, top_k, n_experts, token_at, pos_of, off
 def mxfp4_moe_dispatch(x, n_tokens, top_k, width, token_at, xs, type=None, stream=None):
     """xs[i] = x[token_at[i]]."""
     try:
+        if token_at.dtype is not _INT32:
+            raise TypeError
         dtype = x.dtype
         status = _lib.mxfp4_moe_dispatch(
             x.data_ptr(), _TYPE_OF[dtype if xs.dtype is dtype else None] if type is None else type,
             n_tokens, top_k, width, token_at.data_ptr(), xs.data_ptr(),
             _current_stream() if stream is None else _stream(stream))
     except _NOT_PLAIN:
+        _refuse_other_than("mxfp4_moe_dispatch", "int32", token_at)
         status = lib().mxfp4_moe_dispatch(
             _addr(x), _type(type, x, xs), n_tokens, top_k, width, _addr(token_at), _addr(xs),
             _stream(stream))
@@ -491,6 +524,8 @@ def mxfp4_moe_dispatch(x, n_tokens, top_k, width, token_at, xs, type=None, strea
 def mxfp4_moe_dispatch_grad(dxs, n_tokens, top_k, width, pos_of, dx, type=None, stream=None):
     """dx[t] = the sum of the token's rows of dxs."""
     try:
+        if pos_of.dtype is not _INT32:
+            raise TypeError
         dtype = dxs.dtype
         status = _lib.mxfp4_moe_dispatch_grad(
             dxs.data_ptr(),
@@ -498,6 +533,7 @@ def mxfp4_moe_dispatch_grad(dxs, n_tokens, top_k, width, pos_of, dx, type=None, 
             n_tokens, top_k, width, pos_of.data_ptr(), dx.data_ptr(),
             _current_stream() if stream is None else _stream(stream))
     except _NOT_PLAIN:
+        _refuse_other_than("mxfp4_moe_dispatch_grad", "int32", pos_of)
         status = lib().mxfp4_moe_dispatch_grad(
             _addr(dxs), _type(type, dxs, dx), n_tokens, top_k, width, _addr(pos_of), _addr(dx),
             _stream(stream))
@@ -508,12 +544,16 @@ def mxfp4_moe_dispatch_grad(dxs, n_tokens, top_k, width, pos_of, dx, type=None, 
 def mxfp4_moe_combine(o, n_tokens, top_k, width, pos_of, route_w, y, type=None, stream=None):
     """y[t] = the sum of route_w times the token's rows of o."""
     try:
+        if pos_of.dtype is not _INT32 or route_w.dtype is not _FLOAT32:
+            raise TypeError
         dtype = o.dtype
         status = _lib.mxfp4_moe_combine(
             o.data_ptr(), _TYPE_OF[dtype if y.dtype is dtype else None] if type is None else type,
             n_tokens, top_k, width, pos_of.data_ptr(), route_w.data_ptr(), y.data_ptr(),
             _current_stream() if stream is None else _stream(stream))
     except _NOT_PLAIN:
+        _refuse_other_than("mxfp4_moe_combine", "int32", pos_of)
+        _refuse_other_than("mxfp4_moe_combine", "float32", route_w)
         status = lib().mxfp4_moe_combine(
             _addr(o), _type(type, o, y), n_tokens, top_k, width, _addr(pos_of), _addr(route_w),
             _addr(y), _stream(stream))
@@ -525,6 +565,9 @@ def mxfp4_moe_combine_grad(dy, o, n_tokens, top_k, width, pos_of, route_w, d_o, 
                            type=None, stream=None):
     """d_o and d_route_w of mxfp4_moe_combine."""
     try:
+        if (pos_of.dtype is not _INT32 or route_w.dtype is not _FLOAT32 or
+                d_route_w.dtype is not _FLOAT32):
+            raise TypeError
         dtype = dy.dtype
         status = _lib.mxfp4_moe_combine_grad(
             dy.data_ptr(), o.data_ptr(),
@@ -533,6 +576,8 @@ def mxfp4_moe_combine_grad(dy, o, n_tokens, top_k, width, pos_of, route_w, d_o, 
             route_w.data_ptr(), d_o.data_ptr(), d_route_w.data_ptr(),
             _current_stream() if stream is None else _stream(stream))
     except _NOT_PLAIN:
+        _refuse_other_than("mxfp4_moe_combine_grad", "int32", pos_of)
+        _refuse_other_than("mxfp4_moe_combine_grad", "float32", route_w, d_route_w)
         status = lib().mxfp4_moe_combine_grad(
             _addr(dy), _addr(o), _type(type, dy, o, d_o), n_tokens, top_k, width, _addr(pos_of),
             _addr(route_w), _addr(d_o), _addr(d_route_w), _stream(stream))

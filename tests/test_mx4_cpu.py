@@ -123,3 +123,60 @@ def test_reference_agrees_with_the_oracle_decode(orc):
     code, k = ref.random_matrix(rng, 5, 96, 0, 255)
     got = orc.dequant(ref.pack(code, k), 5, 96)
     assert np.array_equal(got.astype(np.float64), ref.values(code, k))
+
+
+def test_binding_refuses_other_index_and_weight_types(mx):
+    """int64 ids (as topk gives them) would be read as pairs of halves, bfloat16 route weights past
+    their end.  Every call below has a misaligned or null pointer as well, so that nothing could be
+    launched: with the right dtypes that is what is refused (status 2)."""
+    torch = pytest.importorskip("torch")
+    i32, i64 = (lambda n, d=d: torch.zeros(n, dtype=d) for d in (torch.int32, torch.int64))
+    f32, bf16 = (lambda n, d=d: torch.zeros(n, dtype=d) for d in (torch.float32, torch.bfloat16))
+    odd = f32(65)[1:]                              # 4 bytes past a 16-byte boundary
+    u8 = torch.zeros(256, dtype=torch.uint8)
+
+    def sort(**kw):
+        a = {**dict(ids=i32(8), token_at=i32(8), pos_of=i32(8), offsets=i32(5)), **kw}
+        mx.mxfp4_moe_sort(a["ids"], 4, 2, 4, a["token_at"], a["pos_of"], a["offsets"], stream=0)
+
+    def quant(**kw):
+        mx.mxfp4_quant(f32(64), 2, 32, 32, kw.get("row_of", i32(2)), 2, u8[1:], stream=0)
+
+    def experts(**kw):
+        mx.mxfp4_moe_mm_mx(u8, 1, 2, 32, u8, 2, kw.get("offsets", i32(2)), odd, stream=0)
+
+    def dispatch(**kw):
+        mx.mxfp4_moe_dispatch(f32(64), 2, 1, 32, kw.get("token_at", i32(2)), odd, stream=0)
+
+    def dispatch_grad(**kw):
+        mx.mxfp4_moe_dispatch_grad(f32(64), 2, 1, 32, kw.get("pos_of", i32(2)), odd, stream=0)
+
+    def combine(**kw):
+        mx.mxfp4_moe_combine(f32(64), 2, 1, 32, kw.get("pos_of", i32(2)), kw.get("route_w", f32(2)), odd, stream=0)
+
+    def combine_grad(**kw):
+        mx.mxfp4_moe_combine_grad(f32(64), f32(64), 2, 1, 32, kw.get("pos_of", i32(2)), kw.get("route_w", f32(2)), odd,
+                                  kw.get("d_route_w", f32(2)), stream=0)
+
+    def status(call, **kw):
+        with pytest.raises(mx.Mxfp4Error) as e:
+            call(**kw)
+        return e.value.status
+
+    for call in (quant, experts, dispatch, dispatch_grad, combine, combine_grad):
+        assert status(call) == 2, call
+    assert status(sort, ids=None) == status(sort, offsets=None) == 2
+    for call, name in ((quant, "row_of"), (experts, "offsets"), (dispatch, "token_at"), (dispatch_grad, "pos_of"),
+                       (combine, "pos_of"), (combine_grad, "pos_of")):
+        for bad in (i64(8), f32(8), torch.zeros(8, dtype=torch.int16)):
+            assert status(call, **{name: bad}) == 1, (call, name)
+    for call, name in ((combine, "route_w"), (combine_grad, "route_w"), (combine_grad, "d_route_w")):
+        for bad in (bf16(8), torch.zeros(8, dtype=torch.float64), i32(8)):
+            assert status(call, **{name: bad}) == 1, (call, name)
+    for name in ("ids", "token_at", "pos_of", "offsets"):
+        other = "ids" if name != "ids" else "offsets"
+        assert status(sort, **{name: i64(8), other: None}) == 1, name
+    # addresses pass, whatever they point to
+    with pytest.raises(mx.Mxfp4Error) as e:
+        mx.mxfp4_moe_combine(f32(64), 2, 1, 32, A, A, odd, stream=0)
+    assert e.value.status == 2
