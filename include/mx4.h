@@ -55,8 +55,8 @@ enum {
  *            NULL: row i, and rows <= x_rows
  *   out      the MXFP4 matrix [rows, cols]
  *   values   nullable: the rounded values, [rows, cols] of `type` (exact in
- *            every type), e.g. for a forward pass through frozen roundings; NaN
- *            in a NaN group */
+ *            every type: x's own range holds them), e.g. for a forward pass
+ *            through frozen roundings; NaN in a NaN group */
 int mxfp4_quant(const void* x, int type, int x_rows, int cols, long long ld,
                 const int32_t* row_of, int rows, void* out, void* values, cudaStream_t stream);
 
@@ -65,7 +65,10 @@ int mxfp4_quant(const void* x, int type, int x_rows, int cols, long long ld,
  * is subnormal, 2^-149 |gate up|): gate and up [rows, cols] of `type`, rows ld
  * elements apart.  swiglu_limit > 0 clamps up to
  * [-limit, limit] and gate to at most limit first (a NaN of either stays one); 0 or
- * less turns the clamp off; NaN is refused. */
+ * less turns the clamp off; NaN is refused.  `values` are exact in F32 and BF16; an
+ * act of halves may leave their range although its codes hold it, so F16 values are
+ * rounded once more, to the nearest half (infinite from 65520 on, subnormal or zero
+ * below 2^-14): a pass through them then differs from one through the codes. */
 int mxfp4_swiglu_quant(const void* gate, const void* up, int type, int rows, int cols,
                        long long ld, float swiglu_limit, void* out, void* values,
                        cudaStream_t stream);

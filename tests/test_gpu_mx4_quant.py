@@ -282,3 +282,28 @@ def test_swiglu_nonfinite_under_a_limit(mx, dtype, ld):
     assert not host(out)[:rows * 32].reshape(rows, 2, 16)[bad].any()   # codes of a NaN group: 0
     # silu(2) and silu(1) * 2 lie in [1, 2): scale 2^-2, so they are 1.7616 / 0.25 -> 6 and 1.4621 / 0.25 -> 6
     assert v[4, 0] == 1.5 and v[5, 0] == 1.5 and v[6, 0] == -1.5
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("ld", [64, 69])
+@pytest.mark.parametrize("gate,up", [(300.0, 300.0), (2000.0, -4000.0), (0.01, 2.0**-14), (2.0**-12, 2.0**-12), (300.0, 218.5)])
+def test_swiglu_values_beyond_halves(mx, dtype, ld, gate, up):
+    """The values are the codes' values rounded once to the type: exact in float and bfloat16,
+    infinite, subnormal or zero in half where its range ends.  (The codes themselves: above.)"""
+    g = torch.Generator().manual_seed(6)
+    gt, u = (v * (1 - torch.rand(7, ld, generator=g) / 2) for v in (gate, up))
+    out = torch.zeros(ref.nbytes(7, 64), dtype=torch.uint8, device="cuda:0")
+    values = torch.zeros(7, 64, dtype=dtype, device="cuda:0")
+    mx.mxfp4_swiglu_quant(gt.to(dtype).cuda(), u.to(dtype).cuda(), 7, 64, ld, out, values)
+    o = host(out)
+    byte = o[:7 * 32].reshape(7, 32)
+    code = np.empty((7, 64), np.uint8)
+    code[:, 0::2], code[:, 1::2] = byte & 15, byte >> 4
+    exact = ref.values(code, o[7 * 32:7 * 34].reshape(7, 2))
+    assert np.isfinite(exact).all() and exact.any()
+    want = torch.from_numpy(exact).to(dtype)          # one rounding of an E2M1 value times a power of two
+    assert torch.equal(values.cpu(), want)
+    if dtype is not torch.float16:
+        assert np.array_equal(want.double().numpy(), exact)
+    elif gate == 300.0 and up == 300.0:
+        assert torch.isinf(want).any()
