@@ -294,8 +294,8 @@ __global__ void
 
 // Calls f(Pack<T, N>{}) with the widest unit that keeps every row of `width` elements
 // aligned: 32 (where `base`, the buffers' addresses together, allows it), 16, 8 or 4 bytes,
-// or one element.
-template <class F>
+// or one element; no more than kMost elements of 16-bit types.
+template <int kMost, class F>
 cudaError_t by_type(int type, int width, uintptr_t base, F&& f) {
     const bool wide =
         (base | static_cast<uintptr_t>(width) * static_cast<uintptr_t>(type_bytes(type))) % 32 == 0;
@@ -307,7 +307,9 @@ cudaError_t by_type(int type, int width, uintptr_t base, F&& f) {
     }
     auto half_width = [&](auto zero) {
         using T = decltype(zero);
-        if (wide) return f(Pack<T, 16>{});
+        if constexpr (kMost >= 16) {
+            if (wide) return f(Pack<T, 16>{});
+        }
         if (width % 8 == 0) return f(Pack<T, 8>{});
         if (width % 4 == 0) return f(Pack<T, 4>{});
         if (width % 2 == 0) return f(Pack<T, 2>{});
@@ -348,7 +350,7 @@ cudaError_t launch_moe_sort(const int32_t* ids, int n_pairs, int top_k, int n_ex
 
 cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_rows, int width,
                                 const int32_t* token_at, void* xs, cudaStream_t s) {
-    return by_type(type, width, bits(x) | bits(xs), [&](auto unit) {
+    return by_type<16>(type, width, bits(x) | bits(xs), [&](auto unit) {
         using P = decltype(unit);
         const int per_row = width / P::kN;
         const FastDiv div(static_cast<uint32_t>(per_row));
@@ -363,7 +365,7 @@ cudaError_t launch_moe_dispatch(const void* x, int type, int n_tokens, int n_row
 cudaError_t launch_moe_gather_sum(const void* o, int type, int n_tokens, int top_k, int width,
                                   const int32_t* pos_of, const float* route_w, void* y,
                                   cudaStream_t s) {
-    return by_type(type, width, bits(o) | bits(y), [&](auto unit) {
+    return by_type<16>(type, width, bits(o) | bits(y), [&](auto unit) {
         using P = decltype(unit);
         using T = typename P::Elem;
         const FastDiv div(static_cast<uint32_t>(width / P::kN));
@@ -381,8 +383,7 @@ cudaError_t launch_moe_combine_grad(const void* dy, const void* o, int type, int
                                     cudaStream_t s) {
     // (eight elements a unit at most: a thread holds six units, and 32 bytes of 16-bit elements
     // leave too few threads an SM)
-    const uintptr_t base = type == kTypeF32 ? bits(dy) | bits(o) | bits(d_o) : 16;
-    return by_type(type, width, base, [&](auto unit) {
+    return by_type<8>(type, width, bits(dy) | bits(o) | bits(d_o), [&](auto unit) {
         using P = decltype(unit);
         constexpr int kN = P::kN;
         using T = typename P::Elem;
