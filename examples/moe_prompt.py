@@ -50,6 +50,8 @@ class MoePrompt:
 
     def __init__(self, gate, up, down, n_experts, hidden, inter, top_k, max_tokens,
                  dtype=torch.bfloat16):
+        if dtype not in (torch.float32, torch.bfloat16):   # what the products write
+            raise ValueError(f"buffers of {dtype}: float32 or bfloat16")
         self.gate, self.up, self.down = gate, up, down
         self.n_experts, self.hidden, self.inter, self.top_k = n_experts, hidden, inter, top_k
         self.max_tokens, pairs = max_tokens, max_tokens * top_k
@@ -68,6 +70,13 @@ class MoePrompt:
         tokens, pairs = x.shape[0], x.shape[0] * self.top_k
         if tokens > self.max_tokens:
             raise ValueError(f"{tokens} tokens, room for {self.max_tokens}")
+        if x.shape[1] != self.hidden or x.stride(1) != 1:
+            raise ValueError(f"x {tuple(x.shape)}, strides {x.stride()}: rows of {self.hidden}")
+        for t, shape in ((expert_ids, (tokens, self.top_k)), (route_w, (tokens, self.top_k)),
+                         (y, (tokens, self.hidden))):
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"a contiguous {shape} instead of {tuple(t.shape)}, strides "
+                                 f"{t.stride()}")
         mx.mxfp4_moe_sort(expert_ids, tokens, self.top_k, self.n_experts, self.token_at,
                           self.pos_of, self.offsets)
         mx.mxfp4_quant(x, tokens, self.hidden, x.stride(0), self.token_at, pairs, self.xq)
