@@ -9,6 +9,7 @@
  * them in the stream finishes, but they read and write memory only after it has
  * completed.  The quantisers hold the launch behind them until they are done, so a
  * weight buffer may be written by one and read by mxfp4_mv with launch overlap on.
+ * A call's outputs overlap neither its inputs nor each other.
  *
  * An MXFP4 matrix here is a weight buffer of mxfp4.h, whatever it holds: [rows,
  * cols] with cols % 32 == 0, code plane then scale plane, mxfp4_nbytes(rows,

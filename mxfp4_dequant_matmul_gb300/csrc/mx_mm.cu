@@ -27,8 +27,9 @@
 // copies, MMAs, scales and stores it took 420 cycles a stage of 256 columns (one barrier
 // for two stages now, where they fit), and a stage's copies, its MMAs (257 cycles at 128
 // tokens) and the last tile's stores are hidden behind it only in part.  One token
-// 14336x4096 7.0 us (weights from L2 in part); 2048 tokens 4096x4096 21.8 us, 3.2
-// PFLOP/s; 4096 tokens 37.5 us, 3.7; 2048 tokens, top-4 of 64 experts 2880x2880, 66.7 us.
+// 14336x4096 8.4 us (13 matrices in turn, 407 MB: every weight from HBM; 7.7 where some lie in
+// L2); 2048 tokens 4096x4096 21.9 us, 3.1 PFLOP/s; 4096 tokens 37.4 us, 3.7; 2048 tokens, top-4
+// of 64 experts 2880x2880, 67.0 us.
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land,
 // frees its tensor memory and returns.

@@ -11,8 +11,9 @@
 // k_mx_quant takes any alignment.  Bound by HBM in FP32: each element is read once and 17/32
 // byte (and the rounded value) written.  A thread takes 8 elements, four lanes a group: amax
 // by two shuffles, one 32-bit word of codes per lane (128 bytes per warp) and the group's
-// scale byte from the first of the four.  [14336, 4096] floats and their rounded values: 73.4 us,
-// 6.8 TB/s.
+// scale byte from the first of the four.  [14336, 4096] floats and their rounded values: 73.7 us,
+// 6.8 TB/s; silu(gate) * up of [8192, 2880] floats 30.4 us, 6.6 TB/s, of
+// bfloat16 rows aligned to an element 27.3 us, 3.9 TB/s.
 #include <cstdint>
 
 #include "common.cuh"
@@ -323,8 +324,8 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 
 // silu(gate) * up of aligned 16-bit rows: items as k_mx_quant16's, the act in FP32.  Bound by
 // issue (about 20 instructions an element, two of them on the special-function unit; HBM leaves
-// time for 16): [8192, 2880] bfloat16 18.9 us, 5.6 TB/s (19.7 with the 36 registers it takes if
-// it may), against 29.7 us with 8 elements a thread and exact divisions.
+// time for 16): [8192, 2880] bfloat16 18.8 us, 5.7 TB/s (19.7 with the 36 registers it takes if
+// it may; 24.2 with a limit), against 29.7 us with 8 elements a thread and exact divisions.
 template <typename T, bool kValues>
 __global__ void __launch_bounds__(kQThreads, 8)
     k_mx_swiglu16(const T* gate, const T* up, long long ld, float limit,
