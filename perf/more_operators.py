@@ -1,0 +1,409 @@
+"""Cases that time and check the 8-bit block-scaled operators and the gradients of products.
+
+Five operators: quantisation to E4M3 with a scale for each block of 128 (rows, and 128x128 blocks of a matrix), the
+product of two such matrices, the product of each expert's rows with that expert's matrix, the gradient of both by
+their rows, and the gradient by the matrices.  `own` chooses between the plain form (elementary torch operations in 32
+bits) and the library's entry points; both take what `prepare` makes.
+
+Scales: a matrix [rows, cols] has [rows/128, cols/128] of them, rounded up (a bank of matrices one such table each);
+activations [rows, cols] have [cols/128, rows], block by block.
+"""
+import math
+
+import torch
+
+own = False
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+SIZE = {"f32": 4, "bf16": 2, "f16": 2}
+B = 128
+TOP = 448.0
+
+
+# --- cases ---------------------------------------------------------------------------------------
+
+
+def listed():
+    return [
+        # one token's activations, as each decoding step quantises them before a product: latency
+        {"name": "quant one token", "op": "quant", "rows": 1, "cols": 4096, "type": "bf16", "source": 1, "gather": False, "weights": 0},
+        # a prompt's activations put in expert order while they are quantised (top-4 of 1999 tokens)
+        {"name": "quant sorted prompt", "op": "quant", "rows": 7996, "cols": 2880, "type": "bf16", "source": 1999, "gather": True, "weights": 0},
+        # a weight matrix quantised from its f32 master copy, as after each optimizer step
+        {"name": "quant weights", "op": "quant", "rows": 14336, "cols": 4096, "type": "f32", "source": 14336, "gather": False, "weights": 1},
+        # a decoding step's projection, one token: latency, and the weights' bytes
+        {"name": "product one token", "op": "product", "rows": 14336, "cols": 4096, "tokens": 1, "out": "f32"},
+        # a ragged prompt on odd sizes: rows and columns that fill no tile and no block
+        {"name": "product ragged prompt", "op": "product", "rows": 2303, "cols": 2880, "tokens": 333, "out": "bf16"},
+        # a long prompt's projection
+        {"name": "product prompt", "op": "product", "rows": 4096, "cols": 14336, "tokens": 2048, "out": "bf16"},
+        # one decoding step of 32 requests through 64 experts: most experts see a row or two
+        {"name": "experts decode", "op": "experts", "experts": 64, "rows": 2880, "cols": 2880, "tokens": 32, "top_k": 4, "out": "bf16"},
+        # a prompt through the same experts
+        {"name": "experts prompt", "op": "experts", "experts": 64, "rows": 2880, "cols": 2880, "tokens": 2048, "top_k": 4, "out": "bf16"},
+        # the gradient of a training batch's projection by its input
+        {"name": "grad dense", "op": "grad", "experts": 0, "rows": 4096, "cols": 4096, "tokens": 4096, "top_k": 1, "out": "bf16"},
+        # the same through experts, ragged and odd
+        {"name": "grad ragged experts", "op": "grad", "experts": 23, "rows": 1040, "cols": 2000, "tokens": 1111, "top_k": 3, "out": "f32"},
+        # the gradient of a training batch by the experts' matrices, into f32
+        {"name": "weight grad experts", "op": "grad_w", "experts": 16, "rows": 2880, "cols": 2880, "tokens": 4096, "top_k": 4, "type": "bf16", "out": "f32"},
+        # a small ragged batch by odd matrices: experts with few rows or none
+        {"name": "weight grad ragged", "op": "grad_w", "experts": 9, "rows": 1048, "cols": 520, "tokens": 77, "top_k": 2, "type": "f16", "out": "bf16"},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(("quant", "product", "experts", "grad", "grad_w"))
+    if op == "quant":
+        cols = 16 * _log_int(rng, 1, 896)
+        weights = rng.choice((0, 0, 1, 3))
+        rows = _log_int(rng, 1, max(1, min(16384, 14336 * 4096 // (cols * max(1, weights)))))
+        gather = weights == 0 and rng.random() < 0.5
+        source = _log_int(rng, max(1, rows // 8), max(1, rows)) if gather else rows
+        return {"op": op, "rows": rows, "cols": cols, "type": rng.choice(("f32", "bf16", "f16")), "source": source,
+                "gather": gather, "weights": weights}
+    if op == "product":
+        cols = 16 * _log_int(rng, 8, 896)
+        rows = _log_int(rng, 16, min(16384, 14336 * 4096 // cols))
+        tokens = _log_int(rng, 1, max(1, min(4096, 4096 * 14336 * 2048 // (rows * cols))))
+        return {"op": op, "rows": rows, "cols": cols, "tokens": tokens, "out": rng.choice(("f32", "bf16"))}
+    if op == "experts":
+        cols = 16 * _log_int(rng, 8, 180)
+        rows = _log_int(rng, 16, 2880)
+        experts = _log_int(rng, 4, 64)
+        top_k = rng.randint(1, min(8, experts))
+        return {"op": op, "experts": experts, "rows": rows, "cols": cols, "tokens": _log_int(rng, 1, 8192 // top_k),
+                "top_k": top_k, "out": rng.choice(("f32", "bf16"))}
+    if op == "grad":
+        experts = rng.choice((0, _log_int(rng, 4, 64)))
+        top_k = rng.randint(1, min(4, experts)) if experts else 1
+        cols, rows = 16 * _log_int(rng, 1, 180), 16 * _log_int(rng, 8, 180)
+        return {"op": op, "experts": experts, "rows": rows, "cols": cols, "tokens": _log_int(rng, 1, 4096 // top_k),
+                "top_k": top_k, "out": rng.choice(("f32", "bf16"))}
+    experts = _log_int(rng, 1, 32)
+    top_k = rng.randint(1, min(4, experts))
+    return {"op": op, "experts": experts, "rows": 8 * _log_int(rng, 2, 256), "cols": 8 * _log_int(rng, 2, 256),
+            "tokens": _log_int(rng, 1, 8192 // top_k), "top_k": top_k, "type": rng.choice(("bf16", "f16")),
+            "out": rng.choice(("f32", "bf16"))}
+
+
+# --- the format, in 32-bit torch operations --------------------------------------------------------
+
+
+def _blocks(n):
+    return (n + B - 1) // B
+
+
+def _power(top):
+    """The least power of two s >= 2^-126 with top <= 448 s; NaN where top is not finite."""
+    m, e = torch.frexp(top)  # top = m 2^e, 0.5 <= m < 1; 448 = 0.875 * 2^9
+    k = torch.where(top > 0, e - 9 + (m > 0.875).int(), -126).clamp(min=-126)
+    s = ((k + 127) << 23).to(torch.int32).view(torch.float32)
+    return torch.where(torch.isfinite(top), s, float("nan"))
+
+
+def _codes(x, s):
+    """E4M3 codes of x / s (0 where s is NaN)."""
+    return torch.where(torch.isnan(s), 0.0, x / s).to(torch.float8_e4m3fn)
+
+
+def _encode_rows(x):
+    """[rows, cols] f32 -> (codes [rows, cols], scales [blocks, rows])."""
+    rows, cols = x.shape
+    wide = torch.nn.functional.pad(x, (0, _blocks(cols) * B - cols))
+    s = _power(wide.reshape(rows, -1, B).abs().amax(-1))
+    return _codes(x, s.repeat_interleave(B, 1)[:, :cols]), s.T.contiguous()
+
+
+def _encode_matrix(w):
+    """[n, rows, cols] f32 -> (codes, scales [n, row blocks, column blocks])."""
+    n, rows, cols = w.shape
+    wide = torch.nn.functional.pad(w, (0, _blocks(cols) * B - cols, 0, _blocks(rows) * B - rows))
+    s = _power(wide.reshape(n, _blocks(rows), B, _blocks(cols), B).abs().amax((2, 4)))
+    return _codes(w, _spread(s, rows, cols)), s
+
+
+def _spread(s, rows, cols):
+    return s.repeat_interleave(B, -2)[..., :rows, :].repeat_interleave(B, -1)[..., :cols]
+
+
+def _decode_rows(codes, s):
+    return codes.float() * s.T.repeat_interleave(B, 1)[:, : codes.shape[1]]
+
+
+def _decode_matrix(codes, s):
+    return codes.float() * _spread(s, codes.shape[-2], codes.shape[-1])
+
+
+# --- states ----------------------------------------------------------------------------------------
+
+
+def _generator(seed):
+    return torch.Generator(device="cuda").manual_seed(int(seed))
+
+
+def _activations(g, rows, cols):
+    """Normal values, a few channels much larger than the rest, and rows of different size, as a residual stream has them."""
+    x = torch.randn(rows, cols, generator=g, device="cuda")
+    channel = torch.where(torch.rand(cols, generator=g, device="cuda") < 0.01, 20.0, 1.0)
+    return x * channel * torch.exp2(torch.randn(rows, 1, generator=g, device="cuda"))
+
+
+def _weights(g, n, rows, cols):
+    """Rows of different size; a matrix at a time, so that a bank takes little beside itself."""
+    size = 0.02 * torch.exp2(torch.randn(n, rows, 1, generator=g, device="cuda"))
+    return [size[i] * torch.randn(rows, cols, generator=g, device="cuda") for i in range(n)]
+
+
+def _bank(g, n, rows, cols):
+    """A bank as a checkpoint brings it: scales that are no powers of two, each block's largest code 448."""
+    codes = torch.empty(n, rows, cols, dtype=torch.float8_e4m3fn, device="cuda")
+    scales = torch.empty(n, _blocks(rows), _blocks(cols), device="cuda")
+    size = 0.02 * torch.exp2(torch.randn(n, rows, 1, generator=g, device="cuda"))
+    for i in range(n):
+        w = size[i] * torch.randn(rows, cols, generator=g, device="cuda")
+        wide = torch.nn.functional.pad(w, (0, _blocks(cols) * B - cols, 0, _blocks(rows) * B - rows))
+        scales[i] = wide.reshape(_blocks(rows), B, _blocks(cols), B).abs().amax((1, 3)) / TOP
+        codes[i] = (w / _spread(scales[i], rows, cols)).clamp(-TOP, TOP).to(torch.float8_e4m3fn)
+    return codes, scales
+
+
+def _groups(g, case):
+    """Row offsets of the experts, some more popular than others, and the rows of the busiest one."""
+    tokens, top_k, n = case["tokens"], case["top_k"], case["experts"]
+    liking = 0.5 * torch.randn(n, generator=g, device="cuda")
+    u = torch.rand(tokens, n, generator=g, device="cuda")
+    ids = (liking - torch.log(-torch.log(u.clamp(1e-6, 1 - 1e-6)))).topk(top_k, dim=1).indices.reshape(-1)
+    count = torch.bincount(ids, minlength=n)
+    return torch.cat((torch.zeros(1, device="cuda"), count.cumsum(0))).to(torch.int32), int(count.max())
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    s = dict(case)
+    op, rows, cols = case["op"], case["rows"], case["cols"]
+    if op == "quant":
+        dtype, n = TYPES[case["type"]], case["weights"]
+        s["row_of"] = None
+        if n:
+            s["x"] = torch.stack(_weights(g, n, rows, cols)).to(dtype)
+            shape, scales = (n, rows, cols), (n, _blocks(rows), _blocks(cols))
+        else:
+            s["x"] = _activations(g, case["source"], cols).to(dtype)
+            if case["gather"]:
+                s["row_of"] = torch.randint(0, case["source"], (rows,), generator=g, device="cuda", dtype=torch.int32)
+            shape, scales = (rows, cols), (_blocks(cols), rows)
+        s["codes"] = torch.zeros(shape, dtype=torch.float8_e4m3fn, device="cuda")
+        s["scales"] = torch.zeros(scales, device="cuda")
+        s["values"] = torch.zeros(shape, dtype=dtype, device="cuda")
+        return s
+    grouped = case.get("experts", 0) > 0
+    pairs = case["tokens"] * case.get("top_k", 1)
+    if grouped:
+        s["offsets"], s["most"] = _groups(g, case)
+    if op == "grad_w":
+        dtype = TYPES[case["type"]]
+        s["x"] = _activations(g, pairs, cols).to(dtype)
+        s["dy"] = (0.1 * _activations(g, pairs, rows)).to(dtype)
+        s["dw"] = torch.zeros(case["experts"], rows, cols, dtype=TYPES[case["out"]], device="cuda")
+        return s
+    s["bank"], s["bank_scales"] = _bank(g, case["experts"] if grouped else 1, rows, cols)
+    s["x"], s["x_scales"] = _encode_rows(_activations(g, pairs, rows if op == "grad" else cols))
+    s["y"] = torch.zeros(pairs, cols if op == "grad" else rows, dtype=TYPES[case["out"]], device="cuda")
+    return s
+
+
+# --- one pass --------------------------------------------------------------------------------------
+
+
+def run(state):
+    return (_run_own if own else _run_plain)[state["op"]](state)
+
+
+def _quant_plain(s):
+    x = s["x"].float()
+    if s["weights"]:
+        codes, scales = _encode_matrix(x)
+        return {"values": _decode_matrix(codes, scales).to(s["x"].dtype), "scales": scales}
+    if s["row_of"] is not None:
+        x = x[s["row_of"]]
+    codes, scales = _encode_rows(x)
+    return {"values": _decode_rows(codes, scales).to(s["x"].dtype), "scales": scales}
+
+
+def _padded(s, x):
+    """Rows in expert order -> [experts, most, width], and each row's place in it."""
+    n, most = s["experts"], s["most"]
+    at = torch.arange(x.shape[0], device=x.device, dtype=torch.int32)
+    expert = torch.searchsorted(s["offsets"][1:], at, right=True)
+    place = expert * most + (at - s["offsets"][expert])
+    out = torch.zeros(n * most, x.shape[1], device=x.device)
+    out[place] = x
+    return out.reshape(n, most, -1), place
+
+
+def _product_plain(s):
+    w = _decode_matrix(s["bank"], s["bank_scales"])
+    x = _decode_rows(s["x"], s["x_scales"])
+    w = w.transpose(1, 2) if s["op"] != "grad" else w
+    if not s.get("experts"):
+        return {"y": (x @ w[0]).to(s["y"].dtype)}
+    padded, place = _padded(s, x)
+    y = torch.bmm(padded, w)
+    return {"y": y.reshape(-1, y.shape[-1])[place].to(s["y"].dtype)}
+
+
+def _grad_w_plain(s):
+    dy, _ = _padded(s, s["dy"].float())
+    x, _ = _padded(s, s["x"].float())
+    return {"dw": torch.bmm(dy.transpose(1, 2), x).to(s["dw"].dtype)}
+
+
+def _f8():
+    import mxfp4_dequant_matmul_gb300 as mx
+    return mx
+
+
+def _quant_own(s):
+    f8 = _f8()
+    if s["weights"]:
+        f8.f8_quant_weight(s["x"], s["weights"], s["rows"], s["cols"], s["codes"], s["scales"], s["values"])
+    else:
+        f8.f8_quant(s["x"], s["source"], s["cols"], s["cols"], s["row_of"], s["rows"], s["codes"], s["scales"], s["values"])
+    return {"values": s["values"], "scales": s["scales"]}
+
+
+def _product_own(s):
+    _f8().f8_mm(s["bank"], s["bank_scales"], s["rows"], s["cols"], s["x"], s["x_scales"], s["tokens"], s["y"])
+    return {"y": s["y"]}
+
+
+def _experts_own(s):
+    _f8().f8_moe_mm(s["bank"], s["bank_scales"], s["experts"], s["rows"], s["cols"], s["x"], s["x_scales"],
+                    s["tokens"] * s["top_k"], s["offsets"], s["y"])
+    return {"y": s["y"]}
+
+
+def _grad_own(s):
+    if s["experts"]:
+        _f8().f8_moe_mm_grad(s["bank"], s["bank_scales"], s["experts"], s["rows"], s["cols"], s["x"], s["x_scales"],
+                             s["tokens"] * s["top_k"], s["offsets"], s["y"])
+    else:
+        _f8().f8_mm_grad(s["bank"], s["bank_scales"], s["rows"], s["cols"], s["x"], s["x_scales"], s["tokens"], s["y"])
+    return {"y": s["y"]}
+
+
+def _grad_w_own(s):
+    _f8().f8_moe_mm_grad_w(s["dy"], s["x"], s["experts"], s["rows"], s["cols"], s["tokens"] * s["top_k"], s["offsets"],
+                           s["dw"])
+    return {"dw": s["dw"]}
+
+
+_run_plain = {"quant": _quant_plain, "product": _product_plain, "experts": _product_plain, "grad": _product_plain,
+              "grad_w": _grad_w_plain}
+_run_own = {"quant": _quant_own, "product": _product_own, "experts": _experts_own, "grad": _grad_own,
+            "grad_w": _grad_w_own}
+
+
+# --- what a pass cannot do without -------------------------------------------------------------------
+
+
+def work(case):
+    op, rows, cols = case["op"], case["rows"], case["cols"]
+    if op == "quant":
+        n, size, m = rows * cols, SIZE[case["type"]], max(1, case["weights"])
+        scales = _blocks(rows) * _blocks(cols) if case["weights"] else rows * _blocks(cols)
+        read = min(rows, case["source"]) * cols * size * m + (4 * rows if case["gather"] else 0)
+        return {"bytes": read + m * (n + 4 * scales + n * size), "flops": 2 * n * m}
+    pairs = case["tokens"] * case.get("top_k", 1)
+    n = case.get("experts", 0)
+    touched = n * (1 - (1 - case["top_k"] / n) ** case["tokens"]) if n else 1
+    flops = 2 * pairs * rows * cols
+    if op == "grad_w":
+        return {"bytes": pairs * (rows + cols) * SIZE[case["type"]] + n * rows * cols * SIZE[case["out"]], "flops": flops}
+    k, out = (rows, cols) if op == "grad" else (cols, rows)
+    return {"bytes": touched * (rows * cols + 4 * _blocks(rows) * _blocks(cols)) + pairs * (k + 4 * _blocks(k)) +
+            pairs * out * SIZE[case["out"]], "flops": flops}
+
+
+# --- the definition in 64 bits -------------------------------------------------------------------------
+
+
+def _nearest(a):
+    """E4M3 values nearest to doubles of magnitude 448 at most: steps of 2^-9 below 2^-6, 3 bits of fraction above."""
+    _, e = torch.frexp(a)  # |a| = m 2^e, 0.5 <= m < 1: floor(log2 |a|) = e - 1
+    step = torch.exp2((e - 1).clamp(min=-6).double() - 3)
+    return torch.round(a / step) * step  # torch.round is to even
+
+
+def _value(code):
+    """The values of E4M3 bytes: sign, exponent, fraction."""
+    b = torch.arange(256, device=code.device)
+    e, f = (b >> 3) & 15, (b & 7).double()
+    v = torch.where(e == 0, f / 512, (1 + f / 8) * torch.exp2(e.double() - 7))
+    v = torch.where((b & 127) == 127, float("nan"), v)
+    return torch.where(b >= 128, -v, v)[code.view(torch.uint8).int()]
+
+
+def _exact_matrix(codes, s):
+    rows, cols = codes.shape
+    r, c = torch.arange(rows, device=s.device) // B, torch.arange(cols, device=s.device) // B
+    return _value(codes) * s.double()[r][:, c]
+
+
+def _exact_rows(codes, s):
+    return _value(codes) * s.double().T[:, torch.arange(codes.shape[1], device=s.device) // B]
+
+
+def _exact_scale(top):
+    """The least of the powers of two from 2^-126 on with top <= 448 s, by trying the next larger."""
+    _, e = torch.frexp(top / TOP)
+    s = torch.exp2((e - 1).double().clamp(min=-126))
+    s = torch.where(top > TOP * s, 2 * s, s)
+    return torch.where(top > 0, s, 2.0 ** -126)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op, rows, cols = case["op"], case["rows"], case["cols"]
+    if op == "quant":
+        if case["weights"]:
+            values, scales = [], []
+            for w in s["x"].double():
+                sc = torch.zeros(_blocks(rows), _blocks(cols), dtype=torch.float64, device="cuda")
+                v = torch.zeros_like(w)
+                for i in range(_blocks(rows)):
+                    strip = w[i * B: (i + 1) * B]
+                    for j in range(_blocks(cols)):
+                        top = strip[:, j * B: (j + 1) * B].abs().max()
+                        sc[i, j] = _exact_scale(top)
+                    by = sc[i].repeat_interleave(B)[:cols]
+                    v[i * B: (i + 1) * B] = _nearest(strip / by) * by
+                values.append(v)
+                scales.append(sc)
+            return {"values": torch.stack(values), "scales": torch.stack(scales)}
+        x = s["x"].double()
+        x = x if s["row_of"] is None else x[s["row_of"].long()]
+        sc = torch.stack([_exact_scale(x[:, j * B: (j + 1) * B].abs().amax(1)) for j in range(_blocks(cols))])
+        by = sc.T[:, torch.arange(cols, device="cuda") // B]
+        return {"values": _nearest(x / by) * by, "scales": sc}
+    n = case.get("experts", 0)
+    off = s["offsets"].tolist() if n else [0, case["tokens"]]
+    if op == "grad_w":
+        dw = torch.zeros(n, rows, cols, dtype=torch.float64, device="cuda")
+        for e in range(n):
+            i, j = off[e], off[e + 1]
+            dw[e] = s["dy"][i:j].double().T @ s["x"][i:j].double()
+        return {"dw": dw}
+    x = _exact_rows(s["x"], s["x_scales"])
+    y = torch.zeros(s["y"].shape, dtype=torch.float64, device="cuda")
+    for e in range(max(1, n)):
+        i, j = off[e], off[e + 1]
+        if j > i:
+            w = _exact_matrix(s["bank"][e], s["bank_scales"][e])
+            y[i:j] = x[i:j] @ (w if op == "grad" else w.T)
+    return {"y": y}
