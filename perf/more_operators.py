@@ -263,42 +263,42 @@ def _grad_w_plain(s):
     return {"dw": torch.bmm(dy.transpose(1, 2), x).to(s["dw"].dtype)}
 
 
-def _f8():
+def _mx():
     import mxfp4_dequant_matmul_gb300 as mx
     return mx
 
 
 def _quant_own(s):
-    f8 = _f8()
+    mx = _mx()
     if s["weights"]:
-        f8.f8_quant_weight(s["x"], s["weights"], s["rows"], s["cols"], s["codes"], s["scales"], s["values"])
+        mx.mxfp4_f8_quant_weight(s["x"], s["weights"], s["rows"], s["cols"], s["codes"], s["scales"], s["values"])
     else:
-        f8.f8_quant(s["x"], s["source"], s["cols"], s["cols"], s["row_of"], s["rows"], s["codes"], s["scales"], s["values"])
+        mx.mxfp4_f8_quant(s["x"], s["source"], s["cols"], s["cols"], s["row_of"], s["rows"], s["codes"], s["scales"], s["values"])
     return {"values": s["values"], "scales": s["scales"]}
 
 
 def _product_own(s):
-    _f8().f8_mm(s["bank"], s["bank_scales"], s["rows"], s["cols"], s["x"], s["x_scales"], s["tokens"], s["y"])
+    _mx().mxfp4_f8_mm(s["bank"], s["bank_scales"], s["rows"], s["cols"], s["x"], s["x_scales"], s["tokens"], s["y"])
     return {"y": s["y"]}
 
 
 def _experts_own(s):
-    _f8().f8_moe_mm(s["bank"], s["bank_scales"], s["experts"], s["rows"], s["cols"], s["x"], s["x_scales"],
-                    s["tokens"] * s["top_k"], s["offsets"], s["y"])
+    _mx().mxfp4_f8_moe_mm(s["bank"], s["bank_scales"], s["experts"], s["rows"], s["cols"], s["x"], s["x_scales"],
+                          s["tokens"] * s["top_k"], s["offsets"], s["y"])
     return {"y": s["y"]}
 
 
 def _grad_own(s):
     if s["experts"]:
-        _f8().f8_moe_mm_grad(s["bank"], s["bank_scales"], s["experts"], s["rows"], s["cols"], s["x"], s["x_scales"],
-                             s["tokens"] * s["top_k"], s["offsets"], s["y"])
+        _mx().mxfp4_f8_moe_mm_grad(s["bank"], s["bank_scales"], s["experts"], s["rows"], s["cols"], s["x"], s["x_scales"],
+                                   s["tokens"] * s["top_k"], s["offsets"], s["y"])
     else:
-        _f8().f8_mm_grad(s["bank"], s["bank_scales"], s["rows"], s["cols"], s["x"], s["x_scales"], s["tokens"], s["y"])
+        _mx().mxfp4_f8_mm_grad(s["bank"], s["bank_scales"], s["rows"], s["cols"], s["x"], s["x_scales"], s["tokens"], s["y"])
     return {"y": s["y"]}
 
 
 def _grad_w_own(s):
-    _f8().f8_moe_mm_grad_w(s["dy"], s["x"], s["experts"], s["rows"], s["cols"], s["tokens"] * s["top_k"], s["offsets"],
+    _mx().mxfp4_moe_mm_grad_w(s["dy"], s["x"], s["experts"], s["rows"], s["cols"], s["tokens"] * s["top_k"], s["offsets"],
                            s["dw"])
     return {"dw": s["dw"]}
 
