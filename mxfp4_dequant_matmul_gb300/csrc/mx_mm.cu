@@ -34,18 +34,16 @@
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land,
 // frees its tensor memory and returns.
 #include <cooperative_groups.h>
-#include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstdint>
-#include <mutex>
 
 #include "common.cuh"
 #include "elem.cuh"
 #include "kernels.h"
 #include "mx4_kernels.h"
 #include "pdl.cuh"
+#include "tc5.cuh"
 
 namespace mxk {
 namespace {
@@ -99,37 +97,7 @@ struct alignas(16) Tile {
     int e, r0, t0, t1;
 };
 
-__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                      uint64_t* bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                      uint64_t* bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
-__device__ __forceinline__ uint64_t l2_evict_normal() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-
-// Shared-memory matrix descriptors: operands K-major with 128-byte swizzle (8-row groups
-// 1024 bytes apart); scale chunks unswizzled 8 x 16-byte core matrices 128 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
+// Scale chunks in shared memory: unswizzled 8 x 16-byte core matrices 128 bytes apart.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) |
            (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
@@ -164,64 +132,6 @@ __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc) {
 #pragma unroll
     for (uint32_t i = 0; i < 2u * (1 + NB); ++i)
         cp_scales(taddr + 4u * i, desc + i * (kSfChunk >> 4));
-}
-
-__device__ __forceinline__ void umma_commit_mx(uint64_t* bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void fence_after_mx() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_before_mx() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(p));
-    return p != 0;
-}
-
-// One poll that does not suspend.  Its answer takes about a hundred cycles: a role asks
-// about its next stage before it issues the current one.
-__device__ __forceinline__ bool mbar_ready(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-// Wait for the phase with the given parity, for at most `cycles` SM cycles (a poll may
-// itself be suspended for a while, so polls are not counted).
-__device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, long long cycles) {
-    if (mbar_wait(bar, parity, 1)) return true;
-    const long long t0 = clock64();
-    do {
-        if (mbar_wait(bar, parity, 1)) return true;
-    } while (clock64() - t0 < cycles);
-    return false;
-}
-
-// 16 accumulator columns of this warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void sts128_mx(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
@@ -452,9 +362,9 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&wmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
     }
-    fence_before_mx();
+    tc_fence_before();
     __syncthreads();
-    fence_after_mx();
+    tc_fence_after();
     // the next launch may be placed now that this CTA has its tensor memory (a CTA of the
     // next one that waits for columns then waits for CTAs that need nothing more)
     pdl_trigger();
@@ -652,7 +562,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
             if (j >= kAcc)
                 ok = mbar_wait_for(&acc_empty[ab], static_cast<uint32_t>(j / kAcc - 1) & 1u,
                                    kWaitMx);
-            fence_after_mx();
+            tc_fence_after();
             const uint32_t d = tmem + ab * a.tn;
             // four MMAs of K = 64 a stage and the unit's release; the last stage of a row may
             // hold fewer
@@ -671,7 +581,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                     if (kk_end > 2) umma_mxf4(d, ad + 4, bd + 4, id0, sfa + 4u, sfb2, 1u);
                     if (kk_end > 3) umma_mxf4(d, ad + 6, bd + 6, id2, sfa + 4u, sfb2, 1u);
                 }
-                umma_commit_mx(&empty[unit]);
+                umma_commit(&empty[unit]);
             };
             for (int s = s_lo; s < s_hi && ok;) {
                 const uint32_t u0 = un, phase0 = phase;
@@ -681,7 +591,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                     if (q == 0) ok = mbar_wait_for(&sf_full[slot], (group >> 1) & 1u, kWaitMx);
                     ok = ok && mbar_wait_for(&full[u0], phase0, kWaitMx);
                     if (!ok) break;
-                    fence_after_mx();
+                    tc_fence_after();
                     const bool last = q + kP == kAhead || s + kP >= s_hi;
                     if (leader) {
 #pragma unroll
@@ -691,7 +601,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                                     sf_cols + (u0 * kP + i) * sf_stage,
                                     sf0 + ((slot * kSfSlot + (q + i) * kSfStage) >> 4));
                         issue(s, u0);
-                        if (last) umma_commit_mx(&sf_empty[slot]);
+                        if (last) umma_commit(&sf_empty[slot]);
                     }
                     __syncwarp();
                     group += last ? 1u : 0u;
@@ -699,7 +609,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 } else if constexpr (kP > 1) {
                     ok = mbar_wait_for(&full[u0], phase0, kWaitMx);
                     if (!ok) break;
-                    fence_after_mx();
+                    tc_fence_after();
                     if (leader) issue(s, u0);
                     __syncwarp();
                     s += kP;
@@ -711,7 +621,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                     ok = mbar_wait_for(&full[u0], phase0, kWaitMx);
                     if (!ok) break;
                     both = __all_sync(0xFFFFFFFFu, both && there);
-                    fence_after_mx();
+                    tc_fence_after();
                     if (both) {
                         next_of(un, phase);
                         if (leader) {
@@ -726,12 +636,12 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                     __syncwarp();
                 }
             }
-            if (ok && leader) umma_commit_mx(&acc_full[ab]);
+            if (ok && leader) umma_commit(&acc_full[ab]);
             ok = ok && !*abort_flag;
         }
         if (!ok) {
             fail();
-            if (leader) umma_commit_mx(&drain);
+            if (leader) umma_commit(&drain);
             mbar_wait_for(&drain, 0u, kWaitMx);
         }
         __syncwarp();
@@ -747,7 +657,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 if (i == 0 || q + i < n_q)
                     scales_to_tmem<NB>(sf_cols + (unit * kP + i) * sf_stage,
                                        sf0 + ((slot * kSfSlot + (q + i) * kSfStage) >> 4));
-            umma_commit_mx(&full[unit]);
+            umma_commit(&full[unit]);
         };
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s0 = s_lo; s0 < s_hi && ok; s0 += kAhead, ++group) {
@@ -764,11 +674,11 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                     ok = mbar_wait_for(&empty[u0], phase0, kWaitMx);
                     if (!ok) break;
                     both = __all_sync(0xFFFFFFFFu, both && q + kP < n_q);
-                    fence_after_mx();
+                    tc_fence_after();
                     if (leader) {
                         copy(u0, slot, q, n_q);
                         if (both) copy(un, slot, q + kP, n_q);
-                        if (q + (both ? 2 * kP : kP) >= n_q) umma_commit_mx(&sf_empty[slot]);
+                        if (q + (both ? 2 * kP : kP) >= n_q) umma_commit(&sf_empty[slot]);
                     }
                     __syncwarp();
                     if (both && ++un == n_units) {
@@ -864,7 +774,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 fail();
                 break;
             }
-            fence_after_mx();
+            tc_fence_after();
             const int n = t.t1 - t.t0;
             const uint32_t src =
                 tmem + ab * a.tn + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -883,7 +793,7 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
                 store_tile(Y + static_cast<size_t>(t.t0) * a.rows + t.r0 + quarter * 32, a.rows,
                            min(32, a.rows - t.r0 - quarter * 32), 16 * half, n, src, lane);
             }
-            fence_before_mx();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_m(&acc_empty[ab]);
         }
@@ -915,10 +825,10 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
         // a CTA that gave up: its copies in flight land long before this
         for (const long long t0 = clock64(); clock64() - t0 < kDrainMx;) __nanosleep(1000);
     }
-    fence_before_mx();
+    tc_fence_before();
     __syncthreads();
     if (warp == 1) {
-        fence_after_mx();
+        tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                      "r"(a.tmem_cols)
                      : "memory");
@@ -926,20 +836,6 @@ __global__ void __launch_bounds__(Roles<kSplit>::kThreads, kSplit ? 3 : 1)
 }
 
 // --- host side --------------------------------------------------------------------------
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
 
 // Code planes of `experts` matrices [rows][cols/2] bytes, `stride` bytes apart; copies of
 // 128 bytes x box_rows.
@@ -957,17 +853,6 @@ bool code_map(CUtensorMap* map, const void* base, int cols, int rows, int expert
               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int sm_count() {
-    static PerDevice memo;
-    return memo.get([] {
-        int dev = 0, n = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
-            n = 1;
-        return n;
-    });
 }
 
 constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 2048;   // (the static arrays)
