@@ -1,4 +1,4 @@
-"""Python binding of libmxfp4.so (the C ABI in include/mxfp4.h, include/q4k.h and include/mx4.h).
+"""Python binding of libmxfp4.so (the C ABI in include/mxfp4.h, q4k.h, mx4.h and f8.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of the library.  Tensors are torch CUDA tensors (device memory and
@@ -24,6 +24,8 @@ __all__ = [
     "mxfp4_quant", "mxfp4_swiglu_quant", "mxfp4_mm_mx", "mxfp4_moe_mm_mx", "mxfp4_moe_sort",
     "mxfp4_moe_dispatch", "mxfp4_moe_dispatch_grad", "mxfp4_moe_combine",
     "mxfp4_moe_combine_grad", "TYPE_F32", "TYPE_BF16", "TYPE_F16", "MOE_MAX_SORTED_EXPERTS",
+    "mxfp4_f8_quant", "mxfp4_f8_quant_weight", "mxfp4_f8_mm", "mxfp4_f8_moe_mm",
+    "mxfp4_f8_mm_grad", "mxfp4_f8_moe_mm_grad", "mxfp4_mm_grad_w", "mxfp4_moe_mm_grad_w",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -82,6 +84,15 @@ _SIG = {
     "mxfp4_moe_dispatch_grad": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
     "mxfp4_moe_combine": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P]),
     "mxfp4_moe_combine_grad": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    # 8-bit codes with a scale for each block of 128, and gradients of products (include/f8.h)
+    "mxfp4_f8_quant": (_I, [_P, _I, _I, _I, _LL, _P, _I, _P, _P, _P, _P]),
+    "mxfp4_f8_quant_weight": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "mxfp4_f8_mm": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _I, _P]),
+    "mxfp4_f8_moe_mm": (_I, [_P, _P, _I, _I, _I, _P, _P, _I, _P, _P, _I, _P]),
+    "mxfp4_f8_mm_grad": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _I, _P]),
+    "mxfp4_f8_moe_mm_grad": (_I, [_P, _P, _I, _I, _I, _P, _P, _I, _P, _P, _I, _P]),
+    "mxfp4_mm_grad_w": (_I, [_P, _P, _I, _I, _I, _I, _P, _I, _P]),
+    "mxfp4_moe_mm_grad_w": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P]),
 }
 EXPORTED_SYMBOLS = tuple(_SIG)
 _lib = None
@@ -583,3 +594,145 @@ def mxfp4_moe_combine_grad(dy, o, n_tokens, top_k, width, pos_of, route_w, d_o, 
             _addr(route_w), _addr(d_o), _addr(d_route_w), _stream(stream))
     if status:
         _check("mxfp4_moe_combine_grad", status)
+
+
+# --- 8-bit codes with a scale for each block of 128 (include/f8.h) -----------------
+#
+# Codes are torch.float8_e4m3fn (or uint8) tensors.  A tensor of another dtype, on another device
+# than the current one, too small, or with strides where the library takes contiguous rows (a
+# transposed table of scales) is refused (status 1): the kernels would read it as something else
+# or past its end.  Addresses pass, as everywhere.
+
+_F8 = None       # torch's dtypes of codes, from the first call on
+_current_device = None
+
+
+def _f8_types():
+    global _F8, _current_device
+    import torch
+    if not _TYPE_OF:
+        _dtypes()
+    _F8 = (torch.float8_e4m3fn, torch.uint8)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _need(fn, *wanted):
+    """wanted: (tensor, dtypes, elements) each; None and addresses pass."""
+    device = None
+    for t, dtypes, n in wanted:
+        if t is None or isinstance(t, int):
+            continue
+        if device is None:
+            device = _current_device() if t.is_cuda else -2
+        if (t.dtype not in dtypes or t.get_device() != device or t.numel() < n or
+                not t.is_contiguous()):
+            raise Mxfp4Error(fn, 1)
+
+
+def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None, type=None,
+                   stream=None):
+    """x (x_rows rows, ld elements apart) or its rows row_of -> codes [rows, cols] and scales
+    [ceil(cols/128), rows]; type (TYPE_*) defaults to x's dtype, which values shares."""
+    if _F8 is None:
+        _f8_types()
+    _need("mxfp4_f8_quant", (codes, _F8, rows * cols), (scales, (_FLOAT32,), _blocks(cols) * rows),
+          (row_of, (_INT32,), rows), (values, _TYPE_OF, rows * cols))
+    if not isinstance(x, int) and x.get_device() != _current_device():
+        raise Mxfp4Error("mxfp4_f8_quant", 1)
+    status = lib().mxfp4_f8_quant(_addr(x), _type(type, x, values), x_rows, cols, ld, _addr(row_of),
+                                  rows, _addr(codes), _addr(scales), _addr(values), _stream(stream))
+    if status:
+        _check("mxfp4_f8_quant", status)
+
+
+def mxfp4_f8_quant_weight(w, n_matrices, rows, cols, codes, scales, values=None, type=None,
+                          stream=None):
+    """w [n_matrices, rows, cols] -> codes of the same shape and scales [n_matrices,
+    ceil(rows/128), ceil(cols/128)]."""
+    if _F8 is None:
+        _f8_types()
+    n = n_matrices * rows * cols
+    _need("mxfp4_f8_quant_weight", (w, _TYPE_OF, n), (codes, _F8, n), (values, _TYPE_OF, n),
+          (scales, (_FLOAT32,), n_matrices * _blocks(rows) * _blocks(cols)))
+    status = lib().mxfp4_f8_quant_weight(_addr(w), _type(type, w, values), n_matrices, rows, cols,
+                                         _addr(codes), _addr(scales), _addr(values),
+                                         _stream(stream))
+    if status:
+        _check("mxfp4_f8_quant_weight", status)
+
+
+def _f8_product(fn, bank, bank_scales, n_experts, rows, cols, xq, x_scales, n_rows, offsets, Y,
+                y_type, stream, k, n_out):
+    if _F8 is None:
+        _f8_types()
+    _need(fn, (bank, _F8, max(n_experts or 1, 1) * rows * cols),
+          (bank_scales, (_FLOAT32,), max(n_experts or 1, 1) * _blocks(rows) * _blocks(cols)),
+          (xq, _F8, n_rows * k), (x_scales, (_FLOAT32,), _blocks(k) * n_rows),
+          (Y, _TYPE_OF, n_rows * n_out),
+          (offsets, (_INT32,), 0 if n_experts is None else n_experts + 1))
+    y_type = _type(y_type, Y)
+    call = getattr(lib(), fn)
+    if n_experts is None:
+        status = call(_addr(bank), _addr(bank_scales), rows, cols, _addr(xq), _addr(x_scales),
+                      n_rows, _addr(Y), y_type, _stream(stream))
+    else:
+        status = call(_addr(bank), _addr(bank_scales), n_experts, rows, cols, _addr(xq),
+                      _addr(x_scales), n_rows, _addr(offsets), _addr(Y), y_type, _stream(stream))
+    if status:
+        _check(fn, status)
+
+
+def mxfp4_f8_mm(w, w_scales, rows, cols, xq, x_scales, nb, Y, y_type=None, stream=None):
+    """Y [nb, rows] = X W^T of 8-bit codes; y_type defaults to Y's dtype."""
+    _f8_product("mxfp4_f8_mm", w, w_scales, None, rows, cols, xq, x_scales, nb, None, Y, y_type,
+                stream, cols, rows)
+
+
+def mxfp4_f8_moe_mm(bank, bank_scales, n_experts, rows, cols, xq, x_scales, n_rows, offsets, Y,
+                    y_type=None, stream=None):
+    """Each expert's rows offsets[e] .. offsets[e+1] of xq with that expert's matrix."""
+    _f8_product("mxfp4_f8_moe_mm", bank, bank_scales, n_experts, rows, cols, xq, x_scales, n_rows,
+                offsets, Y, y_type, stream, cols, rows)
+
+
+def mxfp4_f8_mm_grad(w, w_scales, rows, cols, dyq, dy_scales, nb, dX, dx_type=None, stream=None):
+    """dX [nb, cols] = dY W: the gradient of mxfp4_f8_mm by its rows, dY [nb, rows] as codes."""
+    _f8_product("mxfp4_f8_mm_grad", w, w_scales, None, rows, cols, dyq, dy_scales, nb, None, dX,
+                dx_type, stream, rows, cols)
+
+
+def mxfp4_f8_moe_mm_grad(bank, bank_scales, n_experts, rows, cols, dyq, dy_scales, n_rows, offsets,
+                         dX, dx_type=None, stream=None):
+    """The gradient of mxfp4_f8_moe_mm by its rows."""
+    _f8_product("mxfp4_f8_moe_mm_grad", bank, bank_scales, n_experts, rows, cols, dyq, dy_scales,
+                n_rows, offsets, dX, dx_type, stream, rows, cols)
+
+
+def mxfp4_mm_grad_w(dy, x, rows, cols, n_rows, dW, type=None, dw_type=None, stream=None):
+    """dW [rows, cols] = dY^T X of 16-bit dY [n_rows, rows] and X [n_rows, cols]."""
+    if _F8 is None:
+        _f8_types()
+    _need("mxfp4_mm_grad_w", (dy, _TYPE_OF, n_rows * rows), (x, _TYPE_OF, n_rows * cols),
+          (dW, _TYPE_OF, rows * cols))
+    status = lib().mxfp4_mm_grad_w(_addr(dy), _addr(x), _type(type, dy, x), rows, cols, n_rows,
+                                   _addr(dW), _type(dw_type, dW), _stream(stream))
+    if status:
+        _check("mxfp4_mm_grad_w", status)
+
+
+def mxfp4_moe_mm_grad_w(dy, x, n_experts, rows, cols, n_rows, offsets, dW, type=None, dw_type=None,
+                        stream=None):
+    """dW [n_experts, rows, cols]: each expert's, from its rows offsets[e] .. offsets[e+1]."""
+    if _F8 is None:
+        _f8_types()
+    _need("mxfp4_moe_mm_grad_w", (dy, _TYPE_OF, n_rows * rows), (x, _TYPE_OF, n_rows * cols),
+          (offsets, (_INT32,), n_experts + 1), (dW, _TYPE_OF, n_experts * rows * cols))
+    status = lib().mxfp4_moe_mm_grad_w(_addr(dy), _addr(x), _type(type, dy, x), n_experts, rows,
+                                       cols, n_rows, _addr(offsets), _addr(dW),
+                                       _type(dw_type, dW), _stream(stream))
+    if status:
+        _check("mxfp4_moe_mm_grad_w", status)

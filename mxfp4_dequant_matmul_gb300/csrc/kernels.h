@@ -146,6 +146,8 @@ cudaError_t read_fault_prefill(int* value, bool reset);
 cudaError_t read_fault_mvtc(int* value, bool reset);
 cudaError_t read_fault_moetc(int* value, bool reset);
 cudaError_t read_fault_mx(int* value, bool reset);
+cudaError_t read_fault_f8(int* value, bool reset);
+cudaError_t read_fault_grad_w(int* value, bool reset);
 
 // Records a CUDA error for mxfp4_last_cuda_error() (this thread).
 void record_cuda_error(int err);
