@@ -9,14 +9,15 @@
 // scale blocks are square, so the codes serve both, and only the operand's descriptor (which
 // side is contiguous) and the strides of the scales change.
 //
-// The matrix's outputs are the MMA's 128 rows and the tokens its columns: one scale of W for
-// a whole tile and block, one of X for a column.
+// Two kernels, by the number of tokens; in both, warps have roles: copies (TMA, 128-byte swizzled
+// rows), MMAs, scales (asynchronous copies of 4 bytes, several blocks ahead: fetched when they
+// are needed, their latency bounded a block), and eight warps for the sums.
 //
-// Warps have roles: copies (TMA, 128-byte swizzled rows: a ring stage is one block of 128 of
-// both operands), MMAs, scales (by asynchronous copies of 4 bytes, 16 blocks ahead), and the sums
-// (eight warps: each quarter of the lanes twice, each half of the columns).  Persistent: CTA c
-// takes tiles c, c + grid, ...  With few tiles a cluster of CTAs shares one, each a slice
-// of the blocks, and adds the partial sums through distributed shared memory in rank order.
+// What bounds them: few tokens, HBM (64 experts 2880x2880, 32 tokens, top-4: 69 us, 6.6 TB/s; one
+// token 14336x4096 12.8 us, of which the stream of the weights is 8.8); many tokens, about 1000 cycles a
+// block of 128 x 256 sums: copies and MMAs without the sums take 935, as either brings 48 KB of
+// operands through shared memory a block (2048 tokens 4096x14336: 123 us, 1.95 PFLOP/s; 4096 tokens
+// 4096x4096 by its rows' gradient 78 us).
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land, frees its
 // tensor memory and returns.
@@ -37,12 +38,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// --- few tokens -------------------------------------------------------------------------
+//
+// The matrix's outputs are the MMA's 128 rows and the tokens its columns: one scale of W for a
+// whole tile and block, one of X for a column.  A warp has a quarter of the rows and half of the
+// columns.  Persistent: CTA c takes tiles c, c + grid, ...  With few tiles a cluster of CTAs
+// shares one, each a slice of the blocks, and adds the partial sums through distributed
+// shared memory in rank order.
+
 constexpr int kM = 128;                      // outputs per tile
 constexpr uint32_t kABytes = kM * kF8Block;  // W's part of a stage
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplit = 8;                 // CTAs of a cluster sharing a tile
 constexpr int kTileTable = 64;               // this CTA's first tiles, worked out at the start
-constexpr int kFac = 16;                     // blocks whose scales are held ahead
+constexpr int kFac = 8;                      // units whose scales are held ahead
 constexpr int kThreads = 384, kEpiWarp = 4, kEpiWarps = 8;
 constexpr long long kWait = 1ll << 32, kDrain = 1ll << 24;   // SM cycles: about 2 s and 8 ms
 
@@ -64,6 +73,68 @@ struct F8Args {
 struct alignas(16) Tile {
     int e, r0, t0, t1;
 };
+
+// The experts' row offsets, and the tiles of the experts before each, in shared memory (all
+// threads; *n_tiles is there after the next barrier).
+template <int kN>
+__device__ __forceinline__ void read_experts(const F8Args& a, int32_t* off, int32_t* first,
+                                             int* n_tiles) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int e = tid; e <= a.n_experts; e += kN)
+        off[e] = min(max(ld_dep(a.offsets + e), 0), a.n_rows);
+    __syncthreads();
+    if (tid < 32) {
+        int base = 0;
+        for (int e0 = 0; e0 < a.n_experts; e0 += 32) {
+            const int e = e0 + lane;
+            int n = 0;
+            if (e < a.n_experts) n = a.n_rt * ((max(off[e + 1] - off[e], 0) + a.tn - 1) / a.tn);
+            int sum = n;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+                if (lane >= d) sum += o;
+            }
+            if (e < a.n_experts) first[e] = base + sum - n;
+            base += __shfl_sync(0xFFFFFFFFu, sum, 31);
+        }
+        if (lane == 0) {
+            first[a.n_experts] = base;
+            *n_tiles = base;
+        }
+    }
+}
+
+// Tile `tile` of `width` outputs.  An output tile's token tiles come one after the other, so that
+// its part of the matrix is read again from L2; an expert's rows are cut into equal tiles of a
+// multiple of 16.
+__device__ __forceinline__ Tile locate(const F8Args& a, const int32_t* off, const int32_t* first,
+                                       int tile, int width) {
+    Tile t;
+    if (a.offsets == nullptr) {
+        t.e = 0;
+        const int rt = tile / a.n_tt;
+        t.r0 = rt * width;
+        t.t0 = (tile - rt * a.n_tt) * a.tn;
+        t.t1 = min(t.t0 + a.tn, a.n_rows);
+    } else {
+        int lo = 0, hi = a.n_experts;   // first[lo] <= tile < first[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= tile) lo = mid;
+            else hi = mid;
+        }
+        t.e = lo;
+        const int n = off[lo + 1] - off[lo];
+        const int n_tt = (n + a.tn - 1) / a.tn;
+        const int per = ((n + n_tt - 1) / n_tt + 15) & ~15;
+        const int local = tile - first[lo], rt = local / n_tt;
+        t.r0 = rt * width;
+        t.t0 = off[lo] + (local - rt * n_tt) * per;
+        t.t1 = min(t.t0 + per, off[lo + 1]);
+    }
+    return t;
+}
 
 // Instruction descriptor: D = F32, A = B = E4M3; W (A) by its contiguous side.
 template <bool kGrad>
@@ -91,17 +162,19 @@ __device__ __forceinline__ void async_arrive(uint64_t* bar) {
                  : "memory");
 }
 
-// NC: most tokens of a tile.  kAcc accumulators of NC columns.
+// NC: most tokens of a tile.  A ring stage is a unit of kU blocks (one barrier each way for
+// both), and so is an accumulator: kAcc of them, kU * NC columns each.
 template <int NC, bool kSplit>
 struct Shape {
-    static constexpr int kAcc = NC == 16 ? 8 : kSplit && NC == 128 ? 2 : 4;
-    static constexpr uint32_t kTmem = kAcc * NC;
+    static constexpr int kU = NC <= 64 ? 2 : 1;
+    static constexpr int kAcc = NC == 16 || (NC == 32 && !kSplit) ? 4 : 2;
+    static constexpr uint32_t kUnit = kU * NC, kTmem = kAcc * kUnit;   // columns
     static constexpr int kHalf = NC / 2;      // columns a warp
     static constexpr int kFacRow = NC + 4;    // floats of a block's scales: X's, then W's
 };
 
 template <typename T, int NC, bool kSplit, bool kGrad>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, NC <= 32 ? 2 : 1)
     k_f8_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
             const F8Args a, T* __restrict__ Y) {
     using S = Shape<NC, kSplit>;
@@ -110,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[S::kAcc], acc_empty[S::kAcc];
     __shared__ uint64_t fac_full[kFac], fac_empty[kFac], drain;
-    __shared__ __align__(16) float fac[kFac][S::kFacRow];
+    __shared__ __align__(16) float fac[kFac][S::kU][S::kFacRow];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word, n_tiles_sh;
     __shared__ Tile table[kTileTable];
@@ -136,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&acc_empty[i], kEpiWarps);
         }
         for (int i = 0; i < kFac; ++i) {
-            mbar_init(&fac_full[i], 32);
+            mbar_init(&fac_full[i], 64);
             mbar_init(&fac_empty[i], kEpiWarps);
         }
         mbar_init(&drain, 1);
@@ -155,30 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     if (a.offsets != nullptr) {
         pdl_wait();
-        for (int e = tid; e <= a.n_experts; e += kThreads)
-            off[e] = min(max(ld_dep(a.offsets + e), 0), a.n_rows);
-        __syncthreads();
-        if (warp == 0) {   // first[e]: tiles of the experts before e
-            int base = 0;
-            for (int e0 = 0; e0 < a.n_experts; e0 += 32) {
-                const int e = e0 + lane;
-                int n = 0;
-                if (e < a.n_experts)
-                    n = a.n_rt * ((max(off[e + 1] - off[e], 0) + a.tn - 1) / a.tn);
-                int sum = n;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-                    if (lane >= d) sum += o;
-                }
-                if (e < a.n_experts) first[e] = base + sum - n;
-                base += __shfl_sync(0xFFFFFFFFu, sum, 31);
-            }
-            if (lane == 0) {
-                first[a.n_experts] = base;
-                n_tiles_sh = base;
-            }
-        }
+        read_experts<kThreads>(a, off, first, &n_tiles_sh);
     }
     __syncthreads();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
@@ -190,43 +240,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tile0 = static_cast<int>(blockIdx.x) / n_rank;
     const int tile_step = kSplit ? n_tiles : static_cast<int>(gridDim.x);
 
-    // An output tile's token tiles come one after the other, so that its part of the matrix is
-    // read again from L2; an expert's rows are cut into equal tiles of a multiple of 16.
-    auto locate = [&](int tile) {
-        Tile t;
-        if (a.offsets == nullptr) {
-            t.e = 0;
-            const int rt = tile / a.n_tt;
-            t.r0 = rt * kM;
-            t.t0 = (tile - rt * a.n_tt) * a.tn;
-            t.t1 = min(t.t0 + a.tn, a.n_rows);
-        } else {
-            int lo = 0, hi = a.n_experts;   // first[lo] <= tile < first[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (first[mid] <= tile) lo = mid;
-                else hi = mid;
-            }
-            t.e = lo;
-            const int n = off[lo + 1] - off[lo];
-            const int n_tt = (n + a.tn - 1) / a.tn;
-            const int per = ((n + n_tt - 1) / n_tt + 15) & ~15;
-            const int local = tile - first[lo], rt = local / n_tt;
-            t.r0 = rt * kM;
-            t.t0 = off[lo] + (local - rt * n_tt) * per;
-            t.t1 = min(t.t0 + per, off[lo + 1]);
-        }
-        return t;
-    };
     if (tid < kTileTable && tile0 + tid * tile_step < n_tiles)
-        table[tid] = locate(tile0 + tid * tile_step);
+        table[tid] = locate(a, off, first, tile0 + tid * tile_step, kM);
     __syncthreads();
     if (a.offsets == nullptr) pdl_wait();   // nothing in memory was needed so far
-    auto tile_at = [&](int tile, int j) { return j < kTileTable ? table[j] : locate(tile); };
+    auto tile_at = [&](int tile, int j) {
+        return j < kTileTable ? table[j] : locate(a, off, first, tile, kM);
+    };
     auto fail = [&]() {
         *abort_flag = 1;
         atomicOr(&g_fault_f8, 1);
     };
+    const uint32_t block_bytes = kABytes + static_cast<uint32_t>(a.tn) * kF8Block;
 
     if (warp == 0) {
         // --- copies (the whole warp walks, one elected lane issues)
@@ -243,19 +268,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Tile t = tile_at(tile, j);
             const int n_box = (t.t1 - t.t0 + a.box - 1) / a.box;
             const uint32_t bytes = kABytes + static_cast<uint32_t>(n_box) * box_bytes;
-            for (int s = s_lo; s < s_hi; ++s) {
+            for (int s0 = s_lo; s0 < s_hi; s0 += S::kU) {
                 ok = mbar_wait_for(&empty[st], phase, kWait);
                 if (!ok) break;
                 if (leader) {
-                    mbar_arrive_expect_tx(&full[st], bytes);
-                    const uint32_t dst = ring + st * a.stage_bytes;
-                    if constexpr (kGrad)
-                        tma3d(dst, &wmap, t.r0, s * kF8Block, t.e, &full[st], w_policy);
-                    else
-                        tma3d(dst, &wmap, s * kF8Block, t.r0, t.e, &full[st], w_policy);
-                    for (int b = 0; b < n_box; ++b)
-                        tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap,
-                              s * kF8Block, t.t0 + b * a.box, &full[st], keep);
+                    const int n_s = min(S::kU, s_hi - s0);
+                    mbar_arrive_expect_tx(&full[st], n_s * bytes);
+#pragma unroll
+                    for (int u = 0; u < S::kU; ++u) {
+                        if (u == n_s) break;
+                        const uint32_t dst = ring + st * a.stage_bytes + u * block_bytes;
+                        const int k = (s0 + u) * kF8Block;
+                        if constexpr (kGrad) tma3d(dst, &wmap, t.r0, k, t.e, &full[st], w_policy);
+                        else tma3d(dst, &wmap, k, t.r0, t.e, &full[st], w_policy);
+                        for (int b = 0; b < n_box; ++b)
+                            tma2d(dst + kABytes + static_cast<uint32_t>(b) * box_bytes, &xmap, k,
+                                  t.t0 + b * a.box, &full[st], keep);
+                    }
                 }
                 __syncwarp();
                 if (++st == static_cast<uint32_t>(a.n_stages)) {
@@ -268,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) fail();
         __syncwarp();
     } else if (warp == 1) {
-        // --- MMAs: a block's four of K = 32 into the next accumulator
+        // --- MMAs: a block's four of K = 32 each into its accumulator
         const bool leader = elect_one();
         const uint32_t ring = smem_u32(smem);
         const uint64_t a0 = kGrad ? operand_desc_mn(ring, kABytes) : operand_desc(ring);
@@ -282,19 +311,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Tile t = tile_at(tile, j);
             const uint32_t id =
                 idesc_f8<kGrad>(__shfl_sync(0xFFFFFFFFu, (t.t1 - t.t0 + 15) & ~15, 0));
-            for (int s = s_lo; s < s_hi; ++s) {
-                ok = mbar_wait_for(&acc_empty[ab], acc_phase, kWait) &&
-                     mbar_wait_for(&full[st], phase, kWait);
+            for (int s0 = s_lo; s0 < s_hi; s0 += S::kU) {
+                // (both polls at once, by lane)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(lane == 0 ? &full[st] : &acc_empty[ab],
+                                                           lane == 0 ? phase : acc_phase, kWait));
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
                     const uint32_t at = st * (a.stage_bytes >> 4);
-                    const uint32_t d = tmem + ab * NC;
 #pragma unroll
-                    for (uint32_t q = 0; q < 4; ++q)
-                        umma_f8(d, a0 + at + q * kAStep, b0 + at + q * 2, id, q);
-                    umma_commit(&empty[st]);
+                    for (int u = 0; u < S::kU; ++u) {
+                        if (u > 0 && s0 + u >= s_hi) break;
+                        const uint32_t d = tmem + ab * S::kUnit + u * NC;
+                        const uint32_t at_u = at + u * (block_bytes >> 4);
+#pragma unroll
+                        for (uint32_t q = 0; q < 4; ++q)
+                            umma_f8(d, a0 + at_u + q * kAStep, b0 + at_u + q * 2, id, q);
+                    }
                     umma_commit(&acc_full[ab]);
+                    umma_commit(&empty[st]);
                 }
                 __syncwarp();
                 if (++st == static_cast<uint32_t>(a.n_stages)) {
@@ -314,9 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_for(&drain, 0u, kWait);
         }
         __syncwarp();
-    } else if (warp == 2) {
-        // --- scales
-        const uint32_t slots = smem_u32(&fac[0][0]);
+    } else if (warp < kEpiWarp) {
+        // --- scales (two warps)
+        const uint32_t slots = smem_u32(&fac[0][0][0]);
         uint32_t f = 0, phase = 1;
         int j = 0;
         bool ok = true;
@@ -325,14 +360,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float* w = a.w_scales + t.e * a.sw_expert +
                              static_cast<long long>(t.r0 / kM) * a.sw_out;
             const int n = t.t1 - t.t0;
-            for (int s = s_lo; s < s_hi; ++s) {
+            for (int s0 = s_lo; s0 < s_hi; s0 += S::kU) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&fac_empty[f], phase, kWait));
                 if (!ok) break;
-                const uint32_t dst = slots + f * (S::kFacRow * 4);
-                const float* x = a.x_scales + static_cast<size_t>(s) * a.n_rows + t.t0;
-                for (int i = lane; i < n; i += 32) copy4(dst + i * 4, x + i);
-                if (lane == 0)
-                    copy4(dst + NC * 4, w + static_cast<long long>(s) * a.sw_k);
+                const int n_s = min(S::kU, s_hi - s0);
+#pragma unroll
+                for (int i0 = 0; i0 < S::kU * NC; i0 += 64) {
+                    const int u = (i0 + tid - 64) / NC, c = (i0 + tid - 64) % NC;
+                    if (c < n && u < n_s)
+                        copy4(slots + ((f * S::kU + u) * S::kFacRow + c) * 4,
+                              a.x_scales + static_cast<size_t>(s0 + u) * a.n_rows + t.t0 + c);
+                }
+                if (warp == 3 && lane < n_s)
+                    copy4(slots + ((f * S::kU + lane) * S::kFacRow + NC) * 4,
+                          w + static_cast<long long>(s0 + lane) * a.sw_k);
                 async_arrive(&fac_full[f]);
                 if (++f == kFac) {
                     f = 0;
@@ -347,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= kEpiWarp) {
         // --- sums: lane = output, columns half * kHalf on = tokens
         const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
-        constexpr int kChunk = S::kHalf < 32 ? S::kHalf : 32;
+        constexpr int kLd = S::kHalf < 32 ? S::kHalf : 32;
         uint32_t ab = 0, acc_phase = 0, f = 0, fac_phase = 0;
         int j = 0;
         bool ok = true;
@@ -357,40 +398,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 sum[S::kHalf / 2];
 #pragma unroll
             for (int i = 0; i < S::kHalf / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
-            for (int s = s_lo; s < s_hi; ++s) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&fac_full[f], fac_phase, kWait) &&
-                                                 mbar_wait_for(&acc_full[ab], acc_phase, kWait));
+            for (int s0 = s_lo; s0 < s_hi; s0 += S::kU) {
+                // (both polls at once, by lane)
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait_for(lane == 0 ? &acc_full[ab] : &fac_full[f],
+                                              lane == 0 ? acc_phase : fac_phase, kWait));
                 if (!ok) break;
                 tc_fence_after();
-                const float w = fac[f][NC];
+                uint32_t v[S::kU][S::kHalf];
 #pragma unroll
-                for (int c = 0; c < S::kHalf; c += kChunk) {
-                    if (c >= n) break;
-                    uint32_t v[kChunk];
-                    tmem_ld<kChunk>(tmem + ab * NC + half * S::kHalf + c +
-                                        (static_cast<uint32_t>(quarter * 32) << 16),
-                                    v);
-                    tmem_ld_wait();
-                    const float4* x = reinterpret_cast<const float4*>(&fac[f][half * S::kHalf + c]);
+                for (int u = 0; u < S::kU; ++u)
 #pragma unroll
-                    for (int i = 0; i < kChunk / 4; ++i) {
-                        const float4 p = x[i];
-                        float2& s0 = sum[c / 2 + 2 * i];
-                        float2& s1 = sum[c / 2 + 2 * i + 1];
-                        s0 = __ffma2_rn(make_float2(__uint_as_float(v[4 * i]),
-                                                    __uint_as_float(v[4 * i + 1])),
-                                        __fmul2_rn(make_float2(p.x, p.y), make_float2(w, w)), s0);
-                        s1 = __ffma2_rn(make_float2(__uint_as_float(v[4 * i + 2]),
-                                                    __uint_as_float(v[4 * i + 3])),
-                                        __fmul2_rn(make_float2(p.z, p.w), make_float2(w, w)), s1);
-                    }
-                }
+                    for (int c = 0; c < S::kHalf; c += kLd)
+                        if (c < n && (u == 0 || s0 + u < s_hi))
+                            tmem_ld<kLd>(tmem + ab * S::kUnit + u * NC + half * S::kHalf + c +
+                                             (static_cast<uint32_t>(quarter * 32) << 16),
+                                         &v[u][c]);
+                tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_m(&acc_empty[ab]);
-                    mbar_arrive_m(&fac_empty[f]);
+                if (lane == 0) mbar_arrive_m(&acc_empty[ab]);
+#pragma unroll
+                for (int u = 0; u < S::kU; ++u) {
+                    if (n <= 0 || (u > 0 && s0 + u >= s_hi)) break;
+                    const float w = fac[f][u][NC];
+                    const float4* x = reinterpret_cast<const float4*>(&fac[f][u][half * S::kHalf]);
+#pragma unroll
+                    for (int i = 0; i < S::kHalf / 4; ++i) {
+                        const float4 p = x[i];
+                        float2& s_0 = sum[2 * i];
+                        float2& s_1 = sum[2 * i + 1];
+                        s_0 = __ffma2_rn(make_float2(__uint_as_float(v[u][4 * i]),
+                                                     __uint_as_float(v[u][4 * i + 1])),
+                                         __fmul2_rn(make_float2(p.x, p.y), make_float2(w, w)), s_0);
+                        s_1 = __ffma2_rn(make_float2(__uint_as_float(v[u][4 * i + 2]),
+                                                     __uint_as_float(v[u][4 * i + 3])),
+                                         __fmul2_rn(make_float2(p.z, p.w), make_float2(w, w)), s_1);
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_m(&fac_empty[f]);
                 if (++ab == S::kAcc) {
                     ab = 0;
                     acc_phase ^= 1u;
@@ -458,37 +505,373 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// --- many tokens ------------------------------------------------------------------------
+//
+// The other way round: 128 tokens are the MMA's rows and 256 outputs its columns, so that in
+// the sums one thread has one token, and a block's two scales are one factor for all its
+// columns.  Eight warps hold the 128 x 256 sums (128 columns a thread); tensor memory holds two
+// blocks of the tile, in halves of 128 outputs that are handed over one by one, each to four of the
+// warps: multiplying, handing over and reading overlap.
+//
+// Pairs of CTAs sharing each MMA (256 x 256, half of the copies) were no faster: the hand-over then
+// crosses the pair (2048 tokens 4096x14336: 116 to 128 us, a prompt's experts 157 to 168 against 129).
+constexpr int kWN = 256;
+constexpr uint32_t kWHalf = kM * kF8Block, kWStage = 3 * kWHalf;   // X, W's two halves
+constexpr int kWStages = 4, kWThreads = 384, kWEpiWarp = 4, kWEpiWarps = 8, kWCols = 128;
+constexpr int kWFac = 8;           // blocks whose scales are held
+constexpr int kWPatch = 32 * 16;   // floats a warp turns round for rows that are not aligned
+
+// 16 of a lane's sums (its row's outputs c0 .. c0 + 15, of which n exist) for rows of any
+// alignment: turned round in shared memory, so that a store is two rows' 16 outputs.
+template <typename T>
+__device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const float2* sum,
+                                             int n, float* patch, int lane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        patch[lane * 16 + ((2 * i) ^ (lane >> 1 & 15))] = sum[i].x;
+        patch[lane * 16 + ((2 * i + 1) ^ (lane >> 1 & 15))] = sum[i].y;
+    }
+    __syncwarp();
+    const int c = lane & 15;
+    if (c < n)
+        for (int r = lane >> 4; r < rows; r += 2)
+            y[static_cast<size_t>(r) * pitch + c] =
+                from_f32<T>(patch[r * 16 + (c ^ (r >> 1 & 15))]);
+    __syncwarp();
+}
+
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kWThreads, 1)
+    k_f8_wide(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
+              const F8Args a, T* __restrict__ Y) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    __shared__ uint64_t full[kWStages], empty[kWStages], acc_full[2], acc_empty[4], fac_full[kWFac], fac_empty[kWFac], drain;
+    __shared__ float fac[kWFac][kM + 4];   // a block's scales: X's, then W's two
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_word, n_tiles_sh;
+    __shared__ Tile table[kTileTable];
+    volatile int* abort_flag = &abort_word;
+    float* patches = reinterpret_cast<float*>(smem + kWStages * kWStage);
+    int32_t* off = reinterpret_cast<int32_t*>(patches + kWEpiWarps * kWPatch);
+    int32_t* first = off + a.n_experts + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == 1) tmem_take(&tmem_base, 2 * kWN);
+    if (tid == 0) {
+        for (int i = 0; i < kWStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {   // [two blocks][two halves of the outputs]
+            if (i < 2) mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kWEpiWarps / 2);
+        }
+        for (int i = 0; i < kWFac; ++i) {
+            mbar_init(&fac_full[i], 64);
+            mbar_init(&fac_empty[i], kWEpiWarps);
+        }
+        mbar_init(&drain, 1);
+        abort_word = 0;
+        n_tiles_sh = a.n_rt * a.n_tt;
+        fence_mbar_init();
+    }
+    if (tid == 32 * 2) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&wmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    if (a.offsets != nullptr) {
+        pdl_wait();
+        read_experts<kWThreads>(a, off, first, &n_tiles_sh);
+    }
+    __syncthreads();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
+    const int n_tiles = __shfl_sync(0xFFFFFFFFu, n_tiles_sh, 0);
+    const int tile0 = static_cast<int>(blockIdx.x), tile_step = static_cast<int>(gridDim.x);
+    if (tid < kTileTable && tile0 + tid * tile_step < n_tiles)
+        table[tid] = locate(a, off, first, tile0 + tid * tile_step, kWN);
+    __syncthreads();
+    if (a.offsets == nullptr) pdl_wait();   // nothing in memory was needed so far
+    auto tile_at = [&](int tile, int j) {
+        return j < kTileTable ? table[j] : locate(a, off, first, tile, kWN);
+    };
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(&g_fault_f8, 1);
+    };
+
+    // 384 threads of 168 registers: the sums' warps take what the others do not need
+    if (warp < kWEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+        // --- copies
+        const bool leader = elect_one();
+        const uint64_t keep = l2_evict_last(), w_policy = l2_evict_normal();
+        const uint32_t ring = smem_u32(smem);
+        uint32_t st = 0, phase = 1;   // the first round of the ring passes at once
+        int j = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
+            const Tile t = tile_at(tile, j);
+            for (int s = 0; s < a.n_k; ++s) {
+                ok = mbar_wait_for(&empty[st], phase, kWait);
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive_expect_tx(&full[st], kWStage);
+                    const uint32_t dst = ring + st * kWStage;
+                    const int k = s * kF8Block;
+                    tma2d(dst, &xmap, k, t.t0, &full[st], keep);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t w = dst + (1 + h) * kWHalf;
+                        const int out = t.r0 + h * kM;
+                        if constexpr (kGrad) tma3d(w, &wmap, out, k, t.e, &full[st], w_policy);
+                        else tma3d(w, &wmap, k, out, t.e, &full[st], w_policy);
+                    }
+                }
+                __syncwarp();
+                if (++st == kWStages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+            }
+            ok = ok && !*abort_flag;
+        }
+        if (!ok) fail();
+        __syncwarp();
+    } else if (warp == 2 || warp == 3) {
+        // --- scales (two warps): a block's 128 of X and two of W
+        const int at = tid - 64;
+        uint32_t f = 0, phase = 1;
+        int j = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
+            const Tile t = tile_at(tile, j);
+            const float* xs[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                xs[i] = a.x_scales + min(t.t0 + 64 * i + at, a.n_rows - 1);
+            const float* ws = a.w_scales + t.e * a.sw_expert +
+                              static_cast<long long>(t.r0 / kF8Block) * a.sw_out +
+                              (at == 1 && t.r0 + kF8Block < a.n_out ? a.sw_out : 0);
+            for (int s = 0; s < a.n_k; ++s) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&fac_empty[f], phase, kWait));
+                if (!ok) break;
+                const uint32_t dst = smem_u32(&fac[f][0]) + at * 4;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    copy4(dst + i * 256, xs[i]);
+                    xs[i] += a.n_rows;
+                }
+                if (at < 2) copy4(dst + kM * 4, ws);
+                ws += a.sw_k;
+                async_arrive(&fac_full[f]);
+                if (++f == kWFac) {
+                    f = 0;
+                    phase ^= 1u;
+                }
+            }
+            ok = ok && !*abort_flag;
+        }
+        if (!ok) fail();
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+    } else if (warp == 1) {
+        // --- MMAs
+        const bool leader = elect_one();
+        const uint32_t ring = smem_u32(smem);
+        const uint64_t a0 = operand_desc(ring);
+        const uint64_t b0 =
+            kGrad ? operand_desc_mn(ring + kWHalf, kWHalf) : operand_desc(ring + kWHalf);
+        constexpr uint32_t kBStep = kGrad ? 32 * kF8Block / 16 : 2;
+        // D = F32, A = B = E4M3, W (B) by its contiguous side
+        constexpr uint32_t id = (1u << 4) | (kGrad ? 1u << 16 : 0u) |
+                                (static_cast<uint32_t>(kWN / 2 >> 3) << 17) |
+                                (static_cast<uint32_t>(kM >> 4) << 24);
+        uint32_t st = 0, phase = 0, ab = 0, acc_phase = 1;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
+            for (int s = 0; s < a.n_k; ++s) {
+                const uint32_t at = st * (kWStage >> 4);
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {
+                    // (both polls at once, by lane)
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    mbar_wait_for(h == 0 && lane == 0 ? &full[st] : &acc_empty[2 * ab + h],
+                                                  h == 0 && lane == 0 ? phase : acc_phase, kWait));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint32_t d = tmem + ab * kWN + h * (kWN / 2);
+                        const uint64_t bh = b0 + at + h * (kWHalf >> 4);
+#pragma unroll
+                        for (uint32_t q = 0; q < 4; ++q)
+                            umma_f8(d, a0 + at + q * 2, bh + q * kBStep, id, q);
+                        umma_commit(h == 0 ? &acc_full[ab] : &empty[st]);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (++st == kWStages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+                ab ^= 1u;
+                acc_phase ^= ab ^ 1u;
+            }
+            ok = ok && !*abort_flag;
+        }
+        if (!ok) {
+            fail();
+            if (leader) umma_commit(&drain);
+            mbar_wait_for(&drain, 0u, kWait);
+        }
+        __syncwarp();
+    } else if (warp >= kWEpiWarp) {
+        // --- sums: lane = token, 128 outputs a warp
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int quarter = warp & 3, group = (warp - kWEpiWarp) >> 2;
+        const uint32_t src =
+            tmem + group * kWCols + (static_cast<uint32_t>(quarter * 32) << 16);
+        const bool aligned =
+            (reinterpret_cast<uintptr_t>(Y) | static_cast<size_t>(a.n_out) * sizeof(T)) % 32 == 0;
+        float* patch = patches + (warp - kWEpiWarp) * kWPatch;
+        uint32_t ab = 0, acc_phase = 0, st = 0, phase = 0, slot = 0, fac_phase = 0;
+        int j = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
+            const Tile t = tile_at(tile, j);
+            const int row0 = t.t0 + quarter * 32, c0 = t.r0 + group * kWCols;
+            const int rows = min(t.t1 - row0, 32);   // of this warp's (may be none)
+            float2 sum[kWCols / 2];
+#pragma unroll
+            for (int i = 0; i < kWCols / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
+            for (int s = 0; s < a.n_k; ++s) {
+                // (both polls at once, by lane)
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(lane != 0 ? &fac_full[slot] : group == 0 ? &acc_full[ab] : &empty[st],
+                                                           lane != 0 ? fac_phase : group == 0 ? acc_phase : phase, kWait));
+                if (!ok) break;
+                tc_fence_after();
+                const float f = fac[slot][quarter * 32 + lane] * fac[slot][kM + group];
+
+                constexpr int kC = 64;
+#pragma unroll
+                for (int c = 0; c < kWCols; c += kC) {
+                    uint32_t u[kC];
+                    if (rows > 0) {
+                        tmem_ld<32>(src + ab * kWN + c, u);
+                        tmem_ld<32>(src + ab * kWN + c + 32, u + 32);
+                    }
+                    tmem_ld_wait();
+                    if (c + kC >= kWCols) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive_m(&acc_empty[2 * ab + group]);
+                            mbar_arrive_m(&fac_empty[slot]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kC / 2; ++i)
+                        sum[c / 2 + i] = __ffma2_rn(make_float2(__uint_as_float(u[2 * i]),
+                                                                __uint_as_float(u[2 * i + 1])),
+                                                    make_float2(f, f), sum[c / 2 + i]);
+                }
+                acc_phase ^= ab;
+                ab ^= 1u;
+                if (++st == kWStages) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+                if (++slot == kWFac) {
+                    slot = 0;
+                    fac_phase ^= 1u;
+                }
+            }
+            if (!ok) {
+                fail();
+                break;
+            }
+            T* dst = Y + static_cast<size_t>(row0) * a.n_out + c0;
+            if (aligned && a.n_out - c0 >= kWCols) {
+                constexpr int kN = 32 / sizeof(T);
+                Pack<T, kN>* out =
+                    reinterpret_cast<Pack<T, kN>*>(dst + static_cast<size_t>(lane) * a.n_out);
+                if (lane < rows) {
+#pragma unroll
+                    for (int q = 0; q < kWCols / kN; ++q) {
+                        float f[kN];
+#pragma unroll
+                        for (int i = 0; i < kN; ++i)
+                            f[i] = i % 2 ? sum[(q * kN + i) / 2].y : sum[(q * kN + i) / 2].x;
+                        Pack<T, kN> p;
+                        p.set(f);
+                        store_pack(out + q, p);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kWCols; c += 16)
+                    if (c0 + c < a.n_out)
+                        store_turned(dst + c, static_cast<size_t>(a.n_out), rows, &sum[c / 2],
+                                     a.n_out - c0 - c, patch, lane);
+            }
+            ok = !*abort_flag;
+        }
+    }
+
+    __syncthreads();
+    if (*abort_flag && tid == 0) {
+        // a CTA that gave up: its copies in flight land long before this
+        for (const long long t0 = clock64(); clock64() - t0 < kDrain;) __nanosleep(1000);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_give(tmem, 2 * kWN);
+    }
+}
+
 // --- host side --------------------------------------------------------------------------
 
-// `n` matrices of codes [rows][cols], copies of 128 columns x box_rows.
-bool code_map(CUtensorMap* map, const void* base, int cols, int rows, int n, int box_rows) {
+// `n` matrices of codes [rows][cols], copies of box_rows x box_cols (128 or 64, as is the swizzle).
+bool code_map(CUtensorMap* map, const void* base, int cols, int rows, int n, int box_rows,
+              int box_cols = kF8Block) {
     auto fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(n)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols),
                                    static_cast<cuuint64_t>(cols) * rows};
-    const cuuint32_t box[3] = {kF8Block, static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows),
+                               1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, n > 0 ? 3 : 2, const_cast<void*>(base), dims,
-              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_cols == kF8Block ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 12 * 1024;   // (the static arrays)
+constexpr size_t kSmemMax = 227 * 1024, kSmemSlack = 8 * 1024;   // (the static arrays)
 
 template <typename T, int NC, bool kSplit, bool kGrad>
 cudaError_t launch_k(const F8Product& p, F8Args a, int split, int per_sm, unsigned grid,
                      cudaStream_t s) {
-    a.stage_bytes = kABytes + static_cast<uint32_t>(a.tn) * kF8Block;
+    using S = Shape<NC, kSplit>;
+    a.stage_bytes = S::kU * (kABytes + static_cast<uint32_t>(a.tn) * kF8Block);
     const size_t extra =
         p.offsets != nullptr ? static_cast<size_t>(p.n_experts + 1) * 8 : 0;
     const size_t budget = kSmemMax / per_sm - kSmemSlack - 1024 - extra;
     a.n_stages = std::min(kMaxStages, static_cast<int>(budget / a.stage_bytes));
     if (kSplit) {
         // no more stages than a slice has, but room for the partial sums
-        const int most = (a.n_k + split - 1) / split;
+        const int most = ((a.n_k + split - 1) / split + S::kU - 1) / S::kU;
         const int sums = (a.tn * kM * 4 + static_cast<int>(a.stage_bytes) - 1) /
                          static_cast<int>(a.stage_bytes);
         a.n_stages = std::min(a.n_stages, std::max(std::max(most, sums), 2));
@@ -496,8 +879,7 @@ cudaError_t launch_k(const F8Product& p, F8Args a, int split, int per_sm, unsign
     const size_t ring = static_cast<size_t>(a.n_stages) * a.stage_bytes + extra + 1024;
     // CTAs that share an SM never ask for more than its 512 columns of tensor memory together (2.25
     // a KB): one that waits for columns must not hold up its cluster
-    const size_t smem = kSplit ? std::max(ring, static_cast<size_t>(Shape<NC, kSplit>::kTmem) *
-                                                    1024 * 4 / 9)
+    const size_t smem = kSplit ? std::max(ring, static_cast<size_t>(S::kTmem) * 1024 * 4 / 9)
                                : kSmemMax - kSmemSlack;
     auto kernel = k_f8_mm<T, NC, kSplit, kGrad>;
     static PerDevice memo;
@@ -514,6 +896,30 @@ cudaError_t launch_k(const F8Product& p, F8Args a, int split, int per_sm, unsign
         return cudaErrorNotSupported;
     return launch_after(kernel, dim3(grid), kThreads, smem, s, static_cast<unsigned>(split), wmap,
                         xmap, a, static_cast<T*>(p.y));
+}
+
+template <typename T, bool kGrad>
+cudaError_t launch_wide(const F8Product& p, F8Args a, cudaStream_t s) {
+    constexpr size_t kSmem = kWStages * kWStage + kWEpiWarps * kWPatch * 4 + 1024;
+    const size_t extra = p.offsets != nullptr ? static_cast<size_t>(p.n_experts + 1) * 8 : 0;
+    auto kernel = k_f8_wide<T, kGrad>;
+    static PerDevice memo;
+    const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([&] {
+        return static_cast<int>(
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSmemMax - kSmemSlack)));
+    }));
+    if (attr_err != cudaSuccess) return attr_err;
+    CUtensorMap wmap, xmap;
+    const int k = p.grad ? p.rows : p.cols;
+    if (!code_map(&wmap, p.bank, p.cols, p.rows, p.n_experts, kM) ||
+        !code_map(&xmap, p.x, k, p.n_rows, 0, kM))
+        return cudaErrorNotSupported;
+    const long tiles = static_cast<long>(a.n_rt) * a.n_tt, sms = sm_count();
+    const unsigned grid =
+        static_cast<unsigned>(p.offsets != nullptr || tiles > sms ? sms : tiles);
+    return launch_after(kernel, dim3(grid), kWThreads, kSmem + extra, s, 1, wmap, xmap, a,
+                        static_cast<T*>(p.y));
 }
 
 }  // namespace
@@ -533,24 +939,48 @@ cudaError_t launch_f8_mm(const F8Product& p, cudaStream_t s) {
     a.sw_out = p.grad ? 1 : col_blocks;
     a.sw_k = p.grad ? col_blocks : 1;
     a.n_rt = f8_blocks(a.n_out);
+    const int mean = (p.n_rows + p.n_experts - 1) / p.n_experts;
     int split = 1, per_sm = 1;
+    bool wide;
     if (p.offsets != nullptr) {
-        const int mean = (p.n_rows + p.n_experts - 1) / p.n_experts;
-        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : 128;
+        // the narrowest tile that takes the mean expert's rows; past 48 of them the tiles of 128
+        // tokens (us, 64 experts 2880x2880: 32 rows each 91 in tiles of 64, 105 in tiles of 128;
+        // 48 rows 98 and 105; 64 rows 143 and 106)
+        wide = mean > 48;
+        a.tn = mean <= 8 ? 16 : mean <= 24 ? 32 : 64;
         a.box = 16;
         a.n_tt = 0;
     } else {
         a.tn = p.n_rows <= 16 ? 16 : p.n_rows <= 32 ? 32 : p.n_rows <= 64 ? 64 : 128;
         a.box = std::min(a.tn, (p.n_rows + 15) / 16 * 16);
         a.n_tt = (p.n_rows + a.tn - 1) / a.tn;
+        // tiles for less than two thirds of the SMs: slices of the sum over a cluster, as many as
+        // fit at once (us: 4096x14336, one token 23.1 unsplit, 15.0 by 2, 13.6 by 4; 4096x4096, 128
+        // tokens 21.1, 18.3 and 12.8; with 112 tiles, 14336x4096, one token, 12.8, by 2 13.6)
         const int fit = a.tn <= 32 ? 2 : 1;   // CTAs whose registers an SM holds
-        while (a.n_tt == 1 && split < kMaxSplit && 3 * a.n_rt < 2 * sms &&
-               a.n_rt * split * 2 <= fit * sms && split * 2 <= a.n_k)
+        const long tiles = static_cast<long>(a.n_rt) * a.n_tt;
+        while (split < kMaxSplit && 3 * tiles < 2 * sms && tiles * split * 2 <= fit * sms &&
+               split * 2 <= a.n_k)
             split *= 2;
-        if (split > 1) per_sm = (a.n_rt * split + sms - 1) / sms;
+        if (split > 1) per_sm = static_cast<int>((tiles * split + sms - 1) / sms);
+        // Past 64 tokens either kernel takes about as long for a block of its tile (1000 cycles),
+        // and the other one's tiles are twice as large: it is slower only where this one is split
+        // (us: 4096x4096, 256 tokens 18.4 by 2, 21.8 the other; 512 tokens, not split, 22.0 the
+        // other; 2303x2880, 333 tokens 15.9 by 2 and 21.5).
+        wide = a.tn == 128 && split == 1;
+    }
+    if (wide) {
+        a.tn = kM;
+        a.n_rt = (a.n_out + kWN - 1) / kWN;
+        a.n_tt = p.offsets != nullptr ? 0 : (p.n_rows + kM - 1) / kM;
+        auto go = [&](auto one) {
+            using T = decltype(one);
+            return p.grad ? launch_wide<T, true>(p, a, s) : launch_wide<T, false>(p, a, s);
+        };
+        return p.y_type == kTypeF32 ? go(float{}) : go(__nv_bfloat16{});
     }
     const long tiles = static_cast<long>(a.n_rt) * a.n_tt;
-    const unsigned grid = split > 1                 ? static_cast<unsigned>(a.n_rt * split)
+    const unsigned grid = split > 1                 ? static_cast<unsigned>(tiles * split)
                           : p.offsets != nullptr || tiles > sms ? static_cast<unsigned>(sms)
                                                                 : static_cast<unsigned>(tiles);
     auto by_grad = [&](auto one, auto nc, auto sp) {
@@ -566,7 +996,7 @@ cudaError_t launch_f8_mm(const F8Product& p, cudaStream_t s) {
             case 16: return by_split(one, std::integral_constant<int, 16>{});
             case 32: return by_split(one, std::integral_constant<int, 32>{});
             case 64: return by_split(one, std::integral_constant<int, 64>{});
-            default: return by_split(one, std::integral_constant<int, 128>{});
+            default: return by_grad(one, std::integral_constant<int, 128>{}, std::true_type{});
         }
     };
     return p.y_type == kTypeF32 ? by_width(float{}) : by_width(__nv_bfloat16{});
