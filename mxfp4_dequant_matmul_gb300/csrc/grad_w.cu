@@ -5,16 +5,24 @@
 // outermost, so each copy brings 64 rows of 64 elements (128 bytes) as they are, and the
 // descriptors say that the M and N sides are contiguous: nothing is transposed.
 //
-// A tile is 128 rows by 256 columns of a dW_e, its sum the rows of expert e, 64 a ring stage.
+// A tile is 256 rows by 256 columns of a dW_e, its sum the rows of expert e, 64 a ring stage.  A
+// pair of CTAs shares its MMAs: either brings 128 of the tile's rows and of its columns, and gets
+// its 128 rows' sums, so that each operand byte is fetched for twice the products.  The tensor
+// core's FP32 sums lose up to a bit with each addition; after 256 rows (four stages) they are added,
+// rounded to nearest, to sums that eight warps hold in registers (two accumulators, in turn).
+//
 // Rows past the expert's end (another expert's, or none) are no part of it: the MMAs stop at the
 // last 16 rows that hold one of its own, and what follows in those 16 is overwritten by zeros in
-// shared memory (in both operands: zero times whatever lies there may be NaN).
+// shared memory (in both operands: zero times whatever lies there may be NaN).  That last stage
+// lands on a barrier of its own CTA, a warp of which writes the zeros before it reports the stage.
 //
-// Warps: copies, MMAs (and those zeros), eight that store the accumulators (two, in turn).
-// Persistent: CTA c takes tiles c, c + grid, ...
+// Warps: copies, MMAs (rank 0), those zeros, eight for the sums.  Persistent: pair c takes tiles
+// c, c + pairs, ...
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land, frees its
 // tensor memory and returns.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <cstdint>
 
@@ -28,12 +36,15 @@
 namespace mxk {
 namespace {
 
-constexpr int kM = 128, kN = 256, kK = 64;    // rows and columns of a tile, rows of a stage
+namespace cg = cooperative_groups;
+
+constexpr int kM = 128, kN = 256, kK = 64;    // a CTA's rows, a tile's columns, rows of a stage
 constexpr int kBox = 64;                      // elements of a copied row (128 bytes)
 constexpr uint32_t kBoxBytes = kBox * kK * 2;
-constexpr uint32_t kABytes = kM / kBox * kBoxBytes, kStageBytes = kABytes + kN / kBox * kBoxBytes;
-constexpr int kStages = 4;
-constexpr int kThreads = 320, kEpiWarp = 2, kEpiWarps = 8;
+constexpr uint32_t kABytes = 2 * kBoxBytes, kStageBytes = 2 * kABytes;   // of dY; and of X
+constexpr int kStages = 6, kChunk = 4;        // ring; stages an accumulator takes
+constexpr int kPatch = 32 * 64;               // bytes a warp turns round
+constexpr int kThreads = 384, kEpiWarp = 4, kEpiWarps = 8, kCols = 128;
 constexpr int kMaxExperts = 1024;
 constexpr long long kWait = 1ll << 32, kDrain = 1ll << 24;   // SM cycles: about 2 s and 8 ms
 
@@ -47,27 +58,53 @@ struct WArgs {
     int wide;                 // rows of dW are 32-byte aligned
 };
 
-__device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void pair_umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-// n elements (a multiple of 8) of the 32 in v.
-template <typename T, int kN>
-__device__ __forceinline__ void store_row(T* dst, const uint32_t (&v)[32], int n) {
+// 64 bytes of outputs of each lane's row (n elements of them exist, a multiple of 8) for `rows`
+// rows, turned round in shared memory, so that a store is 64 bytes of 16 rows and not 32 of 32:
+// the stores of a tile are waited for by the next tile's sums.  Rows are 16-byte aligned, or 32
+// (wide).
+template <typename T>
+__device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const float2* sum,
+                                             int n, uint8_t* patch, int lane, bool wide) {
+    constexpr int kE = 16 / sizeof(T);   // elements of a 16-byte unit
 #pragma unroll
-    for (int q = 0; q < 32 / kN; ++q) {
-        float f[kN];
+    for (int q = 0; q < 4; ++q) {
+        float f[kE];
 #pragma unroll
-        for (int i = 0; i < kN; ++i) f[i] = __uint_as_float(v[q * kN + i]);
-        Pack<T, kN> p;
+        for (int i = 0; i < kE; ++i)
+            f[i] = i % 2 ? sum[(q * kE + i) / 2].y : sum[(q * kE + i) / 2].x;
+        Pack<T, kE> p;
         p.set(f);
-        if (q * kN < n) store_pack(reinterpret_cast<Pack<T, kN>*>(dst) + q, p);
+        *reinterpret_cast<uint4*>(patch + lane * 64 + (q ^ (lane >> 1 & 3)) * 16) = p.raw;
     }
+    __syncwarp();
+    const int c = lane % 2 * 2;          // this lane's first unit of a row
+#pragma unroll
+    for (int r = lane / 2; r < 32; r += 16) {
+        const uint4 lo =
+            *reinterpret_cast<const uint4*>(patch + r * 64 + (c ^ (r >> 1 & 3)) * 16);
+        const uint4 hi =
+            *reinterpret_cast<const uint4*>(patch + r * 64 + ((c + 1) ^ (r >> 1 & 3)) * 16);
+        if (r >= rows) break;
+        uint4* dst = reinterpret_cast<uint4*>(y + static_cast<size_t>(r) * pitch + c * kE);
+        if (wide && (c + 2) * kE <= n) {
+            Pack<T, 2 * kE> p;
+            p.raw = Raw32{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+            store_pack(reinterpret_cast<Pack<T, 2 * kE>*>(dst), p);
+        } else {
+            if (c * kE < n) dst[0] = lo;
+            if ((c + 1) * kE < n) dst[1] = hi;
+        }
+    }
+    __syncwarp();
 }
 
 template <typename T>
@@ -77,22 +114,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drain;
+    __shared__ uint64_t full[kStages], empty[kStages], last_full[kStages], acc_full[2], acc_empty[2];
+    __shared__ uint64_t drain;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word;
     __shared__ int32_t off[kMaxExperts + 1];
     volatile int* abort_flag = &abort_word;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank());
 
-    if (warp == 1) tmem_take(&tmem_base, 2 * kN);
+    if (warp == 1) pair_tmem_take(&tmem_base, 2 * kN);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 2);        // (the leader's) both CTAs' parts
             mbar_init(&empty[i], 1);
+            mbar_init(&last_full[i], 1);   // a stage with rows to be zeroed
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], kEpiWarps);
+            mbar_init(&acc_empty[i], 2 * kEpiWarps);   // (the leader's) both CTAs' warps
         }
         mbar_init(&drain, 1);
         abort_word = 0;
@@ -103,9 +144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
     }
     tc_fence_before();
-    __syncthreads();
+    cluster.sync();   // both CTAs' barriers and tensor memory are there
     tc_fence_after();
-    pdl_trigger();   // (this CTA has its tensor memory)
+    pdl_trigger();
     pdl_wait();
     for (int e = tid; e <= a.n_experts; e += kThreads)
         off[e] = a.offsets == nullptr ? e * a.n_rows
@@ -117,12 +158,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         int e, r0, c0, i0, m;
     };
     const int per_e = a.n_rt * a.n_ct, n_tiles = per_e * a.n_experts;
-    const int tile0 = static_cast<int>(blockIdx.x), tile_step = static_cast<int>(gridDim.x);
+    const int tile0 = static_cast<int>(blockIdx.x >> 1), tile_step = static_cast<int>(gridDim.x >> 1);
     auto tile_at = [&](int tile) {
         Tile t;
         t.e = tile / per_e;
         const int local = tile - t.e * per_e, rt = local / a.n_ct;
-        t.r0 = rt * kM;
+        t.r0 = rt * 2 * kM;
         t.c0 = (local - rt * a.n_ct) * kN;
         t.i0 = off[t.e];
         t.m = max(off[t.e + 1] - t.i0, 0);
@@ -133,29 +174,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicOr(&g_fault_grad_w, 1);
     };
 
+    // 384 threads of 168 registers: the sums' warps take what the others do not need
+    if (warp < kEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
         // --- copies
         const bool leader = elect_one();
         const uint64_t policy = l2_evict_normal();
-        const uint32_t ring = smem_u32(smem);
+        const uint32_t ring = smem_u32(smem), full0 = leader_addr(&full[0]);
         uint32_t st = 0, phase = 1;   // the first round of the ring passes at once
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             const Tile t = tile_at(tile);
+            const int r = t.r0 + rank * kM, c = t.c0 + rank * (kN / 2);
             for (int i = 0; i < t.m; i += kK) {
                 ok = mbar_wait_for(&empty[st], phase, kWait);
                 if (!ok) break;
                 if (leader) {
-                    mbar_arrive_expect_tx(&full[st], kStageBytes);
+                    const bool zeros = i + kK > t.m && (t.m & 15) != 0;
+                    uint32_t bar = full0 + st * 8;
+                    if (zeros) bar = smem_u32(&last_full[st]);
+                    if (zeros) mbar_arrive_expect_tx(&last_full[st], kStageBytes);
+                    else pair_arrive_expect_tx(bar, kStageBytes);
                     const uint32_t dst = ring + st * kStageBytes;
 #pragma unroll
-                    for (int b = 0; b < kM / kBox; ++b)
-                        tma2d(dst + b * kBoxBytes, &dymap, t.r0 + b * kBox, t.i0 + i, &full[st],
-                              policy);
-#pragma unroll
-                    for (int b = 0; b < kN / kBox; ++b)
-                        tma2d(dst + kABytes + b * kBoxBytes, &xmap, t.c0 + b * kBox, t.i0 + i,
-                              &full[st], policy);
+                    for (int b = 0; b < 2; ++b) {
+                        pair_tma2d(dst + b * kBoxBytes, &dymap, r + b * kBox, t.i0 + i, bar, policy);
+                        pair_tma2d(dst + kABytes + b * kBoxBytes, &xmap, c + b * kBox, t.i0 + i,
+                                   bar, policy);
+                    }
                 }
                 __syncwarp();
                 if (++st == kStages) {
@@ -165,51 +211,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ok = ok && !*abort_flag;
         }
+        // the pair's last arrivals on these barriers land before this CTA may leave
+        for (int i = 0; i < kStages && ok; ++i) {
+            ok = mbar_wait_for(&empty[st], phase, kWait);
+            if (++st == kStages) {
+                st = 0;
+                phase ^= 1u;
+            }
+        }
         if (!ok) fail();
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
         // --- MMAs
         const bool leader = elect_one();
         const uint32_t ring = smem_u32(smem);
         const uint64_t a0 = operand_desc_mn(ring, kBoxBytes);
         const uint64_t b0 = operand_desc_mn(ring + kABytes, kBoxBytes);
-        uint32_t st = 0, phase = 0;
-        int j = 0;
+        uint32_t st = 0, phase = 0, ab = 0, acc_phase = 1;
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             const Tile t = tile_at(tile);
-            if (t.m == 0) continue;
-            const int ab = j & 1;
-            ok = mbar_wait_for(&acc_empty[ab], (static_cast<uint32_t>(j >> 1) & 1u) ^ 1u, kWait);
-            ++j;
-            for (int i = 0; i < t.m && ok; i += kK) {
-                ok = mbar_wait_for(&full[st], phase, kWait);
+            int in_chunk = 0;
+            for (int i = 0; i < t.m; i += kK) {
+                ok = in_chunk > 0 || mbar_wait_for(&acc_empty[ab], acc_phase, kWait);
+                ok = ok && mbar_wait_for(&full[st], phase, kWait);
                 if (!ok) break;
                 const int steps = min(kK, t.m - i + 15) >> 4;   // of 16 rows
-                if (t.m - i < kK && (t.m & 15) != 0) {
-                    // zeros behind the expert's last row, up to the next multiple of 16
-                    const int n = (16 - (t.m & 15)) * 8;   // 16-byte units a box
-                    uint8_t* from = smem + st * kStageBytes + (t.m & (kK - 1)) * 128;
-                    for (int u = lane; u < n; u += 32)
-#pragma unroll
-                        for (int b = 0; b < (kM + kN) / kBox; ++b)
-                            *reinterpret_cast<uint4*>(from + b * kBoxBytes + u * 16) =
-                                make_uint4(0u, 0u, 0u, 0u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
+                const bool done = in_chunk + 1 == kChunk || i + kK >= t.m;
                 tc_fence_after();
                 if (leader) {
                     const uint32_t at = st * (kStageBytes >> 4);
 #pragma unroll
                     for (int q = 0; q < kK / 16; ++q)   // 16 rows of 128 bytes
                         if (q < steps)
-                            umma_f16(tmem + ab * kN, a0 + at + q * 128, b0 + at + q * 128,
-                                     a.idesc, i + q);
-                    umma_commit(&empty[st]);
-                    if (i + kK >= t.m) umma_commit(&acc_full[ab]);
+                            pair_umma_f16(tmem + ab * kN, a0 + at + q * 128, b0 + at + q * 128,
+                                          a.idesc, in_chunk + q);
+                    pair_commit(&empty[st]);
+                    if (done) pair_commit(&acc_full[ab]);
                 }
                 __syncwarp();
+                ++in_chunk;
+                if (done) {
+                    in_chunk = 0;
+                    ab ^= 1u;
+                    acc_phase ^= ab ^ 1u;
+                }
                 if (++st == kStages) {
                     st = 0;
                     phase ^= 1u;
@@ -219,51 +265,88 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) {
             fail();
-            if (leader) umma_commit(&drain);
+            if (leader) pair_commit(&drain);
             mbar_wait_for(&drain, 0u, kWait);
         }
         __syncwarp();
-    } else {
-        // --- accumulators to memory: lane = row, 128 columns a warp
-        const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
-        int j = 0;
-        for (int tile = tile0; tile < n_tiles && !*abort_flag; tile += tile_step) {
+    } else if (warp == 2) {
+        // --- zeros behind an expert's last row, up to the next multiple of 16
+        uint32_t st = 0, phases = 0;   // the last stage of the tiles so far; a bit a barrier
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             const Tile t = tile_at(tile);
-            const int ab = j & 1;
-            if (t.m > 0) {
-                if (!__all_sync(0xFFFFFFFFu,
-                                mbar_wait_for(&acc_full[ab], static_cast<uint32_t>(j >> 1) & 1u,
-                                              kWait))) {
-                    fail();
-                    break;
-                }
-                ++j;
-                tc_fence_after();
-            }
-            const int r = t.r0 + quarter * 32 + lane, c0 = t.c0 + half * (kN / 2);
-            T* dst = dw + (static_cast<size_t>(t.e) * a.rows + r) * a.cols + c0;
-#pragma unroll 1
-            for (int c = 0; c < kN / 2 && c0 + c < a.cols; c += 32) {
-                uint32_t v[32];
-                if (t.m > 0) {
-                    tmem_ld<32>(tmem + ab * kN + half * (kN / 2) + c +
-                                    (static_cast<uint32_t>(quarter * 32) << 16),
-                                v);
-                    tmem_ld_wait();
-                } else {
+            st = (st + static_cast<uint32_t>((t.m + kK - 1) / kK)) % kStages;
+            if ((t.m & 15) == 0) continue;
+            const uint32_t last = (st + kStages - 1) % kStages;
+            ok = __all_sync(0xFFFFFFFFu,
+                            mbar_wait_for(&last_full[last], (phases >> last) & 1u, kWait));
+            if (!ok) break;
+            phases ^= 1u << last;
+            const int n = (16 - (t.m & 15)) * 8;   // 16-byte units a box
+            uint8_t* from = smem + last * kStageBytes + (t.m & (kK - 1)) * 128;
+            for (int u = lane; u < n; u += 32)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
+                for (int b = 0; b < 4; ++b)
+                    *reinterpret_cast<uint4*>(from + b * kBoxBytes + u * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) pair_arrive_release(leader_addr(&full[last]));
+            ok = !*abort_flag;
+        }
+        if (!ok) fail();
+        __syncwarp();
+    } else if (warp >= kEpiWarp) {
+        // --- sums: lane = row, 128 columns a warp
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
+        const uint32_t src = tmem + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t done = leader_addr(&acc_empty[0]);
+        uint8_t* patch = smem + kStages * kStageBytes + (warp - kEpiWarp) * kPatch;
+        uint32_t ab = 0, acc_phase = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
+            const Tile t = tile_at(tile);
+            float2 sum[kCols / 2];
+#pragma unroll
+            for (int i = 0; i < kCols / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
+            for (int i = 0; i < t.m; i += kK * kChunk) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&acc_full[ab], acc_phase, kWait));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < kCols; c += 64) {
+                    uint32_t v[64];
+                    tmem_ld<32>(src + ab * kN + c, v);
+                    tmem_ld<32>(src + ab * kN + c + 32, v + 32);
+                    tmem_ld_wait();
+                    if (c + 64 == kCols) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) pair_arrive(done + ab * 8);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 32; ++q)
+                        sum[c / 2 + q] = __fadd2_rn(sum[c / 2 + q],
+                                                    make_float2(__uint_as_float(v[2 * q]),
+                                                                __uint_as_float(v[2 * q + 1])));
                 }
-                if (r < a.rows) {
-                    if (a.wide) store_row<T, 32 / sizeof(T)>(dst + c, v, a.cols - c0 - c);
-                    else store_row<T, 16 / sizeof(T)>(dst + c, v, a.cols - c0 - c);
-                }
+                ab ^= 1u;
+                acc_phase ^= ab ^ 1u;
             }
-            if (t.m > 0) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_m(&acc_empty[ab]);
+            if (!ok) {
+                fail();
+                break;
             }
+            const int r = t.r0 + rank * kM + quarter * 32, c0 = t.c0 + half * kCols;
+            T* dst = dw + (static_cast<size_t>(t.e) * a.rows + r) * a.cols + c0;
+            constexpr int kE = 64 / sizeof(T);
+#pragma unroll
+            for (int c = 0; c < kCols; c += kE)
+                if (c0 + c < a.cols && r < a.rows)
+                    store_turned(dst + c, static_cast<size_t>(a.cols), a.rows - r, &sum[c / 2],
+                                 a.cols - c0 - c, patch, lane, a.wide != 0);
+            ok = !*abort_flag;
         }
     }
 
@@ -273,10 +356,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (const long long t0 = clock64(); clock64() - t0 < kDrain;) __nanosleep(1000);
     }
     tc_fence_before();
-    __syncthreads();
+    cluster.sync();   // neither leaves while the other still multiplies from its memory
     if (warp == 1) {
         tc_fence_after();
-        tmem_give(tmem, 2 * kN);
+        pair_tmem_give(tmem, 2 * kN);
     }
 }
 
@@ -298,7 +381,7 @@ bool row_map(CUtensorMap* map, const void* base, int width, int n_rows, int type
 template <typename T>
 cudaError_t launch_t(const CUtensorMap& dymap, const CUtensorMap& xmap, WArgs a, void* dw,
                      cudaStream_t s) {
-    constexpr size_t kSmem = kStages * kStageBytes + 1024;
+    constexpr size_t kSmem = kStages * kStageBytes + kEpiWarps * kPatch + 1024;
     static PerDevice memo;
     const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
         return static_cast<int>(cudaFuncSetAttribute(
@@ -307,8 +390,9 @@ cudaError_t launch_t(const CUtensorMap& dymap, const CUtensorMap& xmap, WArgs a,
     if (attr_err != cudaSuccess) return attr_err;
     a.wide = (reinterpret_cast<uintptr_t>(dw) | static_cast<uintptr_t>(a.cols) * sizeof(T)) % 32 == 0;
     const int tiles = a.n_rt * a.n_ct * a.n_experts;
-    return launch_after(k_grad_w<T>, dim3(static_cast<unsigned>(std::min(tiles, sm_count()))),
-                        kThreads, kSmem, s, 1, dymap, xmap, a, static_cast<T*>(dw));
+    return launch_after(k_grad_w<T>,
+                        dim3(2u * static_cast<unsigned>(std::min(tiles, sm_count() / 2))), kThreads,
+                        kSmem, s, 2, dymap, xmap, a, static_cast<T*>(dw));
 }
 
 }  // namespace
@@ -322,12 +406,12 @@ cudaError_t launch_mm_grad_w(const void* dy, const void* x, int type, int n_expe
     a.rows = rows;
     a.cols = cols;
     a.n_rows = n_rows;
-    a.n_rt = (rows + kM - 1) / kM;
+    a.n_rt = (rows + 2 * kM - 1) / (2 * kM);
     a.n_ct = (cols + kN - 1) / kN;
     // D = F32, A and B both of `type` and contiguous along M and N
     const uint32_t t = type == kTypeBF16 ? 1u : 0u;
     a.idesc = (1u << 4) | (t << 7) | (t << 10) | (1u << 15) | (1u << 16) |
-              (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(kM >> 4) << 24);
+              (static_cast<uint32_t>(kN >> 3) << 17) | (static_cast<uint32_t>(2 * kM >> 4) << 24);
     CUtensorMap dymap, xmap;
     if (!row_map(&dymap, dy, rows, n_rows, type) || !row_map(&xmap, x, cols, n_rows, type))
         return cudaErrorNotSupported;
