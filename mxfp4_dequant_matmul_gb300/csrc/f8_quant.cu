@@ -9,6 +9,7 @@
 // Bound by HBM: each element is read once, its code (and rounded value) written.  A thread takes 16
 // elements, eight lanes a block.
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -35,6 +36,13 @@ __device__ __forceinline__ float scale_value(uint32_t field) {
     return __uint_as_float(field == 255u ? 0x7FC00000u : field << 23);
 }
 
+// Packed maximum of unsigned halves.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Two floats -> two E4M3 codes, `lo` in the low byte.
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
     uint16_t r;
@@ -47,36 +55,84 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
     return f16x2_to_f32x2(h);
 }
 
-// 16 elements at p; kVec: p is 32-byte aligned.
-template <typename T, bool kVec>
-__device__ __forceinline__ void load16(const T* p, float (&v)[kItem]) {
-    constexpr int kN = kVec ? 32 / static_cast<int>(sizeof(T)) : 1;
-#pragma unroll
-    for (int q = 0; q < kItem / kN; ++q) {
-        float f[kN];
-        load_pack(reinterpret_cast<const Pack<T, kN>*>(p) + q).get(f);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[q * kN + i] = f[i];
-    }
-}
+// A thread's 16 elements as they lie in memory: 16-bit ones stay packed until they are quantised
+// (half the registers on the way, and their largest magnitude takes one operation a pair).
+template <typename T>
+struct Item {
+    static constexpr int kWords = kItem * static_cast<int>(sizeof(T)) / 4;
+    uint32_t w[kWords];
 
-__device__ __forceinline__ uint32_t magnitude(const float (&v)[kItem]) {
-    uint32_t top = 0;
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < kItem; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    return top;
+        for (int i = 0; i < kWords; ++i) w[i] = 0u;
+    }
+    // kVec: p is 32-byte aligned
+    template <bool kVec>
+    __device__ __forceinline__ void load(const T* p) {
+        if constexpr (kVec) {
+#pragma unroll
+            for (int q = 0; q < kWords / 8; ++q) {
+                uint32_t r[8];
+                ld_dep_stream32(reinterpret_cast<const uint32_t*>(p) + 8 * q, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[8 * q + i] = r[i];
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < kItem; ++i) w[i] = ld_dep(reinterpret_cast<const uint32_t*>(p) + i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kItem / 2; ++i) {
+                const uint16_t lo = ld_dep(reinterpret_cast<const uint16_t*>(p) + 2 * i);
+                const uint16_t hi = ld_dep(reinterpret_cast<const uint16_t*>(p) + 2 * i + 1);
+                w[i] = lo | (static_cast<uint32_t>(hi) << 16);
+            }
+        }
+    }
+    // The largest magnitude, as bits of T (two halves to be compared where T has 16).
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) m = max(m, w[i] & 0x7FFFFFFFu);
+            else m = max_u16x2(m, w[i] & 0x7FFF7FFFu);
+        }
+        return m;
+    }
+    __device__ __forceinline__ float2 pair(int i) const {
+        if constexpr (sizeof(T) == 4)
+            return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else if constexpr (std::is_same_v<T, __half>) return f16x2_to_f32x2(w[i]);
+        else return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t max_top(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return max(a, b);
+    else return max_u16x2(a, b);
+}
+// Bits of the float that the largest magnitude is.
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    else {
+        const uint32_t h = max(m & 0xFFFFu, m >> 16);
+        if constexpr (std::is_same_v<T, __half>) return __float_as_uint(f16x2_to_f32x2(h).x);
+        else return h << 16;
+    }
 }
 
 // The codes of 16 elements (0 in a NaN block), and what they stand for; kVec: values are
 // 32-byte aligned, else 16.
 template <typename T, bool kVec>
-__device__ __forceinline__ void store16(const float (&v)[kItem], uint32_t field, uint8_t* codes,
+__device__ __forceinline__ void store16(const Item<T>& v, uint32_t field, uint8_t* codes,
                                         T* values) {
     const float inv = __uint_as_float((254u - field) << 23);
     uint32_t pair[kItem / 2];
 #pragma unroll
     for (int i = 0; i < kItem / 2; ++i) {
-        const float2 s = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(inv, inv));
+        const float2 s = __fmul2_rn(v.pair(i), make_float2(inv, inv));
         pair[i] = field == 255u ? 0u : to_e4m3x2(s.x, s.y);
     }
     *reinterpret_cast<uint4*>(codes) =
@@ -113,19 +169,19 @@ __global__ void __launch_bounds__(kQThreads)
     const uint32_t c = unit * kItem;
     const size_t row = static_cast<size_t>(row0) + r;
     const bool in = i < items && c < static_cast<uint32_t>(cols);
-    float v[kItem];
-#pragma unroll
-    for (int q = 0; q < kItem; ++q) v[q] = 0.0f;
+    Item<T> v;
+    v.clear();
     if (in) {
         long long src = static_cast<long long>(row);
         if (row_of != nullptr) src = ld_dep(row_of + row);
-        if (src >= 0 && src < x_rows) load16<T, kVec>(x + src * ld + c, v);
+        if (src >= 0 && src < x_rows) v.template load<kVec>(x + src * ld + c);
     }
-    uint32_t top = magnitude(v);
+    uint32_t top = v.top();
 #pragma unroll
-    for (int d = 1; d < kLanes; d <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    for (int d = 1; d < kLanes; d <<= 1)
+        top = max_top<T>(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
     if (!in) return;
-    const uint32_t field = scale_field(top);
+    const uint32_t field = scale_field(top_bits<T>(top));
     if (unit % kLanes == 0)
         scales[static_cast<size_t>(unit / kLanes) * rows + row] = scale_value(field);
     const size_t at = row * cols + c;
@@ -144,19 +200,18 @@ __global__ void __launch_bounds__(kQThreads)
     const int r0 = rb * kF8Block + threadIdx.x / kLanes;
     const int c = cb * kF8Block + threadIdx.x % kLanes * kItem;
     const size_t base = static_cast<size_t>(blockIdx.z) * rows * cols;
-    float v[kU][kItem];
+    Item<T> v[kU];
     uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-#pragma unroll
-        for (int q = 0; q < kItem; ++q) v[u][q] = 0.0f;
+        v[u].clear();
         const int r = r0 + u * kRows;
         if (r < rows && c < cols)
-            load16<T, kVec>(w + base + static_cast<size_t>(r) * cols + c, v[u]);
+            v[u].template load<kVec>(w + base + static_cast<size_t>(r) * cols + c);
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) top = max(top, magnitude(v[u]));
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    for (int u = 0; u < kU; ++u) top = max_top<T>(top, v[u].top());
+    top = __reduce_max_sync(0xFFFFFFFFu, top_bits<T>(top));
     if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
     __syncthreads();
     top = tops[0];
