@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 #include "elem.cuh"
@@ -529,16 +530,26 @@ __global__ void __launch_bounds__(kThreads, NC <= 32 ? 2 : 1)
 // The other way round: 128 tokens are the MMA's rows and 256 outputs its columns, so that in
 // the sums one thread has one token, and a block's two scales are one factor for all its
 // columns.  Eight warps hold the 128 x 256 sums (128 columns a thread); tensor memory holds two
-// blocks of the tile, in halves of 128 outputs that are handed over one by one, each to four of the
-// warps: multiplying, handing over and reading overlap.
+// blocks of the tile, in halves of 128 outputs, each with a warp that multiplies it and four that
+// add it: multiplying, handing over and reading overlap.
 //
-// Pairs of CTAs sharing each MMA (256 x 256, half of the copies) were no faster: the hand-over then
-// crosses the pair (2048 tokens 4096x14336: 116 to 128 us, a prompt's experts 157 to 168 against 129).
+// kPair: two CTAs share each MMA (256 tokens; either brings its 128 and half of the outputs'
+// rows), so that an operand byte is fetched for twice the products.  Then the hand-over crosses the
+// pair, and tiles are coarser: better for one matrix with many tokens, not for experts (us: 2048
+// tokens 4096x14336 110, single CTAs 123; a prompt's experts 147 and 131).
 constexpr int kWN = 256;
-constexpr uint32_t kWHalf = kM * kF8Block, kWStage = 3 * kWHalf;   // X, W's two halves
-constexpr int kWStages = 4, kWThreads = 384, kWEpiWarp = 4, kWEpiWarps = 8, kWCols = 128;
+constexpr uint32_t kWHalf = kM * kF8Block;   // 128 rows of a stage
+constexpr int kWThreads = 384, kWEpiWarp = 4, kWEpiWarps = 8, kWCols = 128;
 constexpr int kWFac = 8;           // blocks whose scales are held
 constexpr int kWPatch = 32 * 16;   // floats a warp turns round for rows that are not aligned
+template <bool kPair>
+struct Wide {
+    static constexpr uint32_t kWRows = kPair ? kM : kWN;   // outputs that a CTA brings
+    static constexpr uint32_t kStage = kWHalf + kWRows * kF8Block;
+    static constexpr int kStages = kPair ? 6 : 4;
+    static constexpr int kBox = kPair ? 64 : 128;          // outputs of a copy: a CTA's of a half
+    static constexpr size_t kSmem = kStages * kStage + kWEpiWarps * kWPatch * 4 + 1024;
+};
 
 // 16 of a lane's sums (its row's outputs c0 .. c0 + 15, of which n exist) for rows of any
 // alignment: turned round in shared memory, so that a store is two rows' 16 outputs.
@@ -559,36 +570,63 @@ __device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const
     __syncwarp();
 }
 
-template <typename T, bool kGrad>
+template <bool kPair>
+__device__ __forceinline__ void wide_umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else umma_f8(d, a, b, idesc, accumulate);
+}
+template <bool kPair>
+__device__ __forceinline__ void wide_commit(uint64_t* bar) {
+    if constexpr (kPair) pair_commit(bar);
+    else umma_commit(bar);
+}
+
+template <typename T, bool kGrad, bool kPair>
 __global__ void __launch_bounds__(kWThreads, 1)
     k_f8_wide(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
               const F8Args a, T* __restrict__ Y) {
+    using S = Wide<kPair>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    __shared__ uint64_t full[kWStages], empty[kWStages], acc_full[2], acc_empty[4], fac_full[kWFac], fac_empty[kWFac], drain;
+    __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[4], acc_empty[4];
+    __shared__ uint64_t fac_full[kWFac], fac_empty[kWFac], drain;
     __shared__ float fac[kWFac][kM + 4];   // a block's scales: X's, then W's two
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word, n_tiles_sh;
     __shared__ Tile table[kTileTable];
     volatile int* abort_flag = &abort_word;
-    float* patches = reinterpret_cast<float*>(smem + kWStages * kWStage);
+    float* patches = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
     int32_t* off = reinterpret_cast<int32_t*>(patches + kWEpiWarps * kWPatch);
     int32_t* first = off + a.n_experts + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = kPair ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
+    auto sync_all = [] {   // of the pair
+        if constexpr (kPair) cg::this_cluster().sync();
+        else __syncthreads();
+    };
 
-    if (warp == 1) tmem_take(&tmem_base, 2 * kWN);
+    if (warp == 1) {
+        if constexpr (kPair) pair_tmem_take(&tmem_base, 2 * kWN);
+        else tmem_take(&tmem_base, 2 * kWN);
+    }
     if (tid == 0) {
-        for (int i = 0; i < kWStages; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&full[i], 1);    // (a pair's: rank 0's, for both CTAs' copies)
+            mbar_init(&empty[i], 2);   // both halves' MMAs
         }
         for (int i = 0; i < 4; ++i) {   // [two blocks][two halves of the outputs]
-            if (i < 2) mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_empty[i], kWEpiWarps / 2);
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], kWEpiWarps / 2 * (kPair ? 2 : 1));   // (a pair's: rank 0's)
         }
         for (int i = 0; i < kWFac; ++i) {
-            mbar_init(&fac_full[i], 64);
+            mbar_init(&fac_full[i], 32);
             mbar_init(&fac_empty[i], kWEpiWarps);
         }
         mbar_init(&drain, 1);
@@ -601,7 +639,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
     }
     tc_fence_before();
-    __syncthreads();
+    sync_all();   // barriers and tensor memory are there
     tc_fence_after();
     pdl_trigger();
     if (a.offsets != nullptr) {
@@ -611,7 +649,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     __syncthreads();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, tmem_base, 0);
     const int n_tiles = __shfl_sync(0xFFFFFFFFu, n_tiles_sh, 0);
-    const int tile0 = static_cast<int>(blockIdx.x), tile_step = static_cast<int>(gridDim.x);
+    constexpr int kCtas = kPair ? 2 : 1;
+    const int tile0 = static_cast<int>(blockIdx.x) / kCtas;
+    const int tile_step = static_cast<int>(gridDim.x) / kCtas;
     if (tid < kTileTable && tile0 + tid * tile_step < n_tiles)
         table[tid] = locate(a, off, first, tile0 + tid * tile_step, kWN);
     __syncthreads();
@@ -627,66 +667,80 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // 384 threads of 168 registers: the sums' warps take what the others do not need
     if (warp < kWEpiWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
-        // --- copies
+        // --- copies: this CTA's 128 tokens (where it has any) and its outputs of both halves
         const bool leader = elect_one();
         const uint64_t keep = l2_evict_last(), w_policy = l2_evict_normal();
         const uint32_t ring = smem_u32(smem);
+        const uint32_t full0 = kPair ? leader_addr(&full[0]) : smem_u32(&full[0]);
         uint32_t st = 0, phase = 1;   // the first round of the ring passes at once
         int j = 0;
         bool ok = true;
+        auto next = [&]() {
+            if (++st == S::kStages) {
+                st = 0;
+                phase ^= 1u;
+            }
+        };
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
+            const bool both = kPair && t.t0 + kM < t.t1;
+            const uint32_t bytes = kWN * kF8Block + (both ? 2 : 1) * kWHalf;
             for (int s = 0; s < a.n_k; ++s) {
                 ok = mbar_wait_for(&empty[st], phase, kWait);
                 if (!ok) break;
                 if (leader) {
-                    mbar_arrive_expect_tx(&full[st], kWStage);
-                    const uint32_t dst = ring + st * kWStage;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                    const uint32_t bar = full0 + st * 8, dst = ring + st * S::kStage;
                     const int k = s * kF8Block;
-                    tma2d(dst, &xmap, k, t.t0, &full[st], keep);
+                    if constexpr (kPair) {
+                        if (rank == 0 || both)
+                            pair_tma2d(dst, &xmap, k, t.t0 + rank * kM, bar, keep);
+                    } else {
+                        tma2d(dst, &xmap, k, t.t0, &full[st], keep);
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t w = dst + (1 + h) * kWHalf;
-                        const int out = t.r0 + h * kM;
-                        if constexpr (kGrad) tma3d(w, &wmap, out, k, t.e, &full[st], w_policy);
-                        else tma3d(w, &wmap, k, out, t.e, &full[st], w_policy);
+                        const uint32_t w = dst + kWHalf + h * S::kBox * kF8Block;
+                        const int out = t.r0 + h * kM + rank * S::kBox;
+                        const int x = kGrad ? out : k, y = kGrad ? k : out;
+                        if constexpr (kPair) pair_tma3d(w, &wmap, x, y, t.e, bar, w_policy);
+                        else tma3d(w, &wmap, x, y, t.e, &full[st], w_policy);
                     }
                 }
                 __syncwarp();
-                if (++st == kWStages) {
-                    st = 0;
-                    phase ^= 1u;
-                }
+                next();
             }
             ok = ok && !*abort_flag;
         }
+        if constexpr (kPair)   // the pair's last arrivals here land before this CTA may leave
+            for (int i = 0; i < S::kStages && ok; ++i, next())
+                ok = mbar_wait_for(&empty[st], phase, kWait);
         if (!ok) fail();
         __syncwarp();
-    } else if (warp == 2 || warp == 3) {
-        // --- scales (two warps): a block's 128 of X and two of W
-        const int at = tid - 64;
+    } else if (warp == 2) {
+        // --- scales: a block's 128 of X and two of W
         uint32_t f = 0, phase = 1;
         int j = 0;
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
-            const float* xs[2];
+            const float* xs[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                xs[i] = a.x_scales + min(t.t0 + 64 * i + at, a.n_rows - 1);
+            for (int i = 0; i < 4; ++i)
+                xs[i] = a.x_scales + min(t.t0 + rank * kM + 32 * i + lane, a.n_rows - 1);
             const float* ws = a.w_scales + t.e * a.sw_expert +
                               static_cast<long long>(t.r0 / kF8Block) * a.sw_out +
-                              (at == 1 && t.r0 + kF8Block < a.n_out ? a.sw_out : 0);
+                              (lane == 1 && t.r0 + kF8Block < a.n_out ? a.sw_out : 0);
             for (int s = 0; s < a.n_k; ++s) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&fac_empty[f], phase, kWait));
                 if (!ok) break;
-                const uint32_t dst = smem_u32(&fac[f][0]) + at * 4;
+                const uint32_t dst = smem_u32(&fac[f][0]) + lane * 4;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    copy4(dst + i * 256, xs[i]);
+                for (int i = 0; i < 4; ++i) {
+                    copy4(dst + i * 128, xs[i]);
                     xs[i] += a.n_rows;
                 }
-                if (at < 2) copy4(dst + kM * 4, ws);
+                if (lane < 2) copy4(dst + kM * 4, ws);
                 ws += a.sw_k;
                 async_arrive(&fac_full[f]);
                 if (++f == kWFac) {
@@ -699,43 +753,43 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (!ok) fail();
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncwarp();
-    } else if (warp == 1) {
-        // --- MMAs
+    } else if (warp < kWEpiWarp && rank == 0) {
+        // --- MMAs: warp 1 the first half of the outputs, warp 3 the second
+        const uint32_t h = warp == 1 ? 0u : 1u;
         const bool leader = elect_one();
         const uint32_t ring = smem_u32(smem);
+        const uint32_t w = ring + kWHalf + h * S::kBox * kF8Block;
         const uint64_t a0 = operand_desc(ring);
-        const uint64_t b0 =
-            kGrad ? operand_desc_mn(ring + kWHalf, kWHalf) : operand_desc(ring + kWHalf);
-        constexpr uint32_t kBStep = kGrad ? 32 * kF8Block / 16 : 2;
+        const uint64_t b0 = !kGrad  ? operand_desc(w)
+                            : kPair ? operand_desc_mn64(w)
+                                    : operand_desc_mn(w, kWHalf);
+        // K = 32: 32 bytes of a row, or 32 rows of a copy
+        constexpr uint32_t kBStep = kGrad ? 32 * S::kBox / 16 : 2;
         // D = F32, A = B = E4M3, W (B) by its contiguous side
         constexpr uint32_t id = (1u << 4) | (kGrad ? 1u << 16 : 0u) |
                                 (static_cast<uint32_t>(kWN / 2 >> 3) << 17) |
-                                (static_cast<uint32_t>(kM >> 4) << 24);
+                                (static_cast<uint32_t>(kCtas * kM >> 4) << 24);
         uint32_t st = 0, phase = 0, ab = 0, acc_phase = 1;
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s = 0; s < a.n_k; ++s) {
-                const uint32_t at = st * (kWStage >> 4);
-#pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {
-                    // (both polls at once, by lane)
-                    ok = __all_sync(0xFFFFFFFFu,
-                                    mbar_wait_for(h == 0 && lane == 0 ? &full[st] : &acc_empty[2 * ab + h],
-                                                  h == 0 && lane == 0 ? phase : acc_phase, kWait));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (leader) {
-                        const uint32_t d = tmem + ab * kWN + h * (kWN / 2);
-                        const uint64_t bh = b0 + at + h * (kWHalf >> 4);
-#pragma unroll
-                        for (uint32_t q = 0; q < 4; ++q)
-                            umma_f8(d, a0 + at + q * 2, bh + q * kBStep, id, q);
-                        umma_commit(h == 0 ? &acc_full[ab] : &empty[st]);
-                    }
-                    __syncwarp();
-                }
+                // (both polls at once, by lane)
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait_for(lane == 0 ? &full[st] : &acc_empty[2 * ab + h],
+                                              lane == 0 ? phase : acc_phase, kWait));
                 if (!ok) break;
-                if (++st == kWStages) {
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t at = st * (S::kStage >> 4);
+                    const uint32_t d = tmem + ab * kWN + h * (kWN / 2);
+#pragma unroll
+                    for (uint32_t q = 0; q < 4; ++q)
+                        wide_umma<kPair>(d, a0 + at + q * 2, b0 + at + q * kBStep, id, q);
+                    wide_commit<kPair>(&acc_full[2 * ab + h]);
+                    wide_commit<kPair>(&empty[st]);
+                }
+                __syncwarp();
+                if (++st == S::kStages) {
                     st = 0;
                     phase ^= 1u;
                 }
@@ -746,7 +800,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         if (!ok) {
             fail();
-            if (leader) umma_commit(&drain);
+            if (leader) wide_commit<kPair>(&drain);
             mbar_wait_for(&drain, 0u, kWait);
         }
         __syncwarp();
@@ -756,56 +810,55 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int quarter = warp & 3, group = (warp - kWEpiWarp) >> 2;
         const uint32_t src =
             tmem + group * kWCols + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t done =
+            kPair ? leader_addr(&acc_empty[group]) : smem_u32(&acc_empty[group]);
         const bool aligned =
             (reinterpret_cast<uintptr_t>(Y) | static_cast<size_t>(a.n_out) * sizeof(T)) % 32 == 0;
         float* patch = patches + (warp - kWEpiWarp) * kWPatch;
-        uint32_t ab = 0, acc_phase = 0, st = 0, phase = 0, slot = 0, fac_phase = 0;
+        uint32_t ab = 0, acc_phase = 0, slot = 0, fac_phase = 0;
         int j = 0;
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step, ++j) {
             const Tile t = tile_at(tile, j);
-            const int row0 = t.t0 + quarter * 32, c0 = t.r0 + group * kWCols;
+            const int row0 = t.t0 + rank * kM + quarter * 32, c0 = t.r0 + group * kWCols;
             const int rows = min(t.t1 - row0, 32);   // of this warp's (may be none)
             float2 sum[kWCols / 2];
 #pragma unroll
             for (int i = 0; i < kWCols / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
             for (int s = 0; s < a.n_k; ++s) {
                 // (both polls at once, by lane)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(lane != 0 ? &fac_full[slot] : group == 0 ? &acc_full[ab] : &empty[st],
-                                                           lane != 0 ? fac_phase : group == 0 ? acc_phase : phase, kWait));
+                ok = __all_sync(0xFFFFFFFFu,
+                                mbar_wait_for(lane == 0 ? &acc_full[2 * ab + group]
+                                                        : &fac_full[slot],
+                                              lane == 0 ? acc_phase : fac_phase, kWait));
                 if (!ok) break;
                 tc_fence_after();
                 const float f = fac[slot][quarter * 32 + lane] * fac[slot][kM + group];
-
-                constexpr int kC = 64;
 #pragma unroll
-                for (int c = 0; c < kWCols; c += kC) {
-                    uint32_t u[kC];
+                for (int c = 0; c < kWCols; c += 64) {
+                    uint32_t u[64];
                     if (rows > 0) {
                         tmem_ld<32>(src + ab * kWN + c, u);
                         tmem_ld<32>(src + ab * kWN + c + 32, u + 32);
                     }
                     tmem_ld_wait();
-                    if (c + kC >= kWCols) {
+                    if (c + 64 == kWCols) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            mbar_arrive_m(&acc_empty[2 * ab + group]);
+                            if constexpr (kPair) pair_arrive(done + ab * 16);
+                            else mbar_arrive_m(&acc_empty[2 * ab + group]);
                             mbar_arrive_m(&fac_empty[slot]);
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < kC / 2; ++i)
+                    for (int i = 0; i < 32; ++i)
                         sum[c / 2 + i] = __ffma2_rn(make_float2(__uint_as_float(u[2 * i]),
                                                                 __uint_as_float(u[2 * i + 1])),
                                                     make_float2(f, f), sum[c / 2 + i]);
                 }
-                acc_phase ^= ab;
                 ab ^= 1u;
-                if (++st == kWStages) {
-                    st = 0;
-                    phase ^= 1u;
-                }
+                acc_phase ^= ab ^ 1u;
                 if (++slot == kWFac) {
                     slot = 0;
                     fac_phase ^= 1u;
@@ -849,10 +902,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
         for (const long long t0 = clock64(); clock64() - t0 < kDrain;) __nanosleep(1000);
     }
     tc_fence_before();
-    __syncthreads();
+    sync_all();   // neither of a pair leaves while the other still multiplies from its memory
     if (warp == 1) {
         tc_fence_after();
-        tmem_give(tmem, 2 * kWN);
+        if constexpr (kPair) pair_tmem_give(tmem, 2 * kWN);
+        else tmem_give(tmem, 2 * kWN);
     }
 }
 
@@ -917,11 +971,11 @@ cudaError_t launch_k(const F8Product& p, F8Args a, int split, int per_sm, unsign
                         xmap, a, static_cast<T*>(p.y));
 }
 
-template <typename T, bool kGrad>
-cudaError_t launch_wide(const F8Product& p, F8Args a, cudaStream_t s) {
-    constexpr size_t kSmem = kWStages * kWStage + kWEpiWarps * kWPatch * 4 + 1024;
+template <typename T, bool kGrad, bool kPair>
+cudaError_t launch_wide(const F8Product& p, const F8Args& a, cudaStream_t s) {
+    using S = Wide<kPair>;
     const size_t extra = p.offsets != nullptr ? static_cast<size_t>(p.n_experts + 1) * 8 : 0;
-    auto kernel = k_f8_wide<T, kGrad>;
+    auto kernel = k_f8_wide<T, kGrad, kPair>;
     static PerDevice memo;
     const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([&] {
         return static_cast<int>(
@@ -930,14 +984,15 @@ cudaError_t launch_wide(const F8Product& p, F8Args a, cudaStream_t s) {
     }));
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap wmap, xmap;
-    const int k = p.grad ? p.rows : p.cols;
-    if (!code_map(&wmap, p.bank, p.cols, p.rows, p.n_experts, kM) ||
-        !code_map(&xmap, p.x, k, p.n_rows, 0, kM))
+    if (!code_map(&wmap, p.bank, p.cols, p.rows, p.n_experts, kGrad ? kF8Block : S::kBox,
+                  kGrad ? S::kBox : kF8Block) ||
+        !code_map(&xmap, p.x, kGrad ? p.rows : p.cols, p.n_rows, 0, kM))
         return cudaErrorNotSupported;
-    const long tiles = static_cast<long>(a.n_rt) * a.n_tt, sms = sm_count();
+    constexpr unsigned kCtas = kPair ? 2 : 1;
+    const long tiles = static_cast<long>(a.n_rt) * a.n_tt, most = sm_count() / kCtas;
     const unsigned grid =
-        static_cast<unsigned>(p.offsets != nullptr || tiles > sms ? sms : tiles);
-    return launch_after(kernel, dim3(grid), kWThreads, kSmem + extra, s, 1, wmap, xmap, a,
+        kCtas * static_cast<unsigned>(p.offsets != nullptr || tiles > most ? most : tiles);
+    return launch_after(kernel, dim3(grid), kWThreads, S::kSmem + extra, s, kCtas, wmap, xmap, a,
                         static_cast<T*>(p.y));
 }
 
@@ -989,12 +1044,21 @@ cudaError_t launch_f8_mm(const F8Product& p, cudaStream_t s) {
         wide = a.tn == 128 && split == 1;
     }
     if (wide) {
-        a.tn = kM;
         a.n_rt = (a.n_out + kWN - 1) / kWN;
-        a.n_tt = p.offsets != nullptr ? 0 : (p.n_rows + kM - 1) / kM;
-        auto go = [&](auto one) {
+        auto rounds = [&](int tokens, int at_once) {   // of tiles over the SMs
+            return (static_cast<long>(a.n_rt) * ((p.n_rows + tokens - 1) / tokens) + at_once - 1) /
+                   at_once;
+        };
+        const bool pair = p.offsets == nullptr && rounds(2 * kM, sms / 2) <= rounds(kM, sms);
+        a.tn = pair ? 2 * kM : kM;
+        a.n_tt = p.offsets != nullptr ? 0 : (p.n_rows + a.tn - 1) / a.tn;
+        auto by_pair = [&](auto one, auto grad) {
             using T = decltype(one);
-            return p.grad ? launch_wide<T, true>(p, a, s) : launch_wide<T, false>(p, a, s);
+            return pair ? launch_wide<T, grad(), true>(p, a, s)
+                        : launch_wide<T, grad(), false>(p, a, s);
+        };
+        auto go = [&](auto one) {
+            return p.grad ? by_pair(one, std::true_type{}) : by_pair(one, std::false_type{});
         };
         return p.y_type == kTypeF32 ? go(float{}) : go(__nv_bfloat16{});
     }

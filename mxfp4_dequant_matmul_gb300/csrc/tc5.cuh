@@ -100,6 +100,13 @@ __device__ __forceinline__ uint64_t operand_desc_mn(uint32_t saddr, uint32_t nex
            (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
 
+// The same in rows of 64 bytes with 64-byte swizzle (64 bytes of the side in all).
+__device__ __forceinline__ uint64_t operand_desc_mn64(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
+           (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(4) << 61);
+}
+
 // --- pairs of CTAs that share their MMAs (cta_group::2): rank 0 issues them ------------------
 
 // The address of rank 0's copy of a shared variable.
@@ -115,6 +122,14 @@ __device__ __forceinline__ void pair_tma2d(uint32_t dst, const CUtensorMap* map,
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
         "bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void pair_tma3d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                           int z, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "l"(policy)
         : "memory");
 }
 __device__ __forceinline__ void pair_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
