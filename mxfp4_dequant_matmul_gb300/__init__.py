@@ -691,21 +691,48 @@ def mxfp4_f8_quant_weight(w, n_matrices, rows, cols, codes, scales, values=None,
 
 def _f8_product(fn, bank, bank_scales, n_experts, rows, cols, xq, x_scales, n_rows, offsets, Y,
                 y_type, stream, k, n_out):
-    if _F8 is None:
-        _f8_types()
-    _need(fn, (bank, _F8, max(n_experts or 1, 1) * rows * cols),
-          (bank_scales, (_FLOAT32,), max(n_experts or 1, 1) * _blocks(rows) * _blocks(cols)),
-          (xq, _F8, n_rows * k), (x_scales, (_FLOAT32,), _blocks(k) * n_rows),
-          (Y, _TYPE_OF, n_rows * n_out),
-          (offsets, (_INT32,), 0 if n_experts is None else n_experts + 1))
-    y_type = _type(y_type, Y)
-    call = getattr(lib(), fn)
-    if n_experts is None:
-        status = call(_addr(bank), _addr(bank_scales), rows, cols, _addr(xq), _addr(x_scales),
-                      n_rows, _addr(Y), y_type, _stream(stream))
-    else:
-        status = call(_addr(bank), _addr(bank_scales), n_experts, rows, cols, _addr(xq),
-                      _addr(x_scales), n_rows, _addr(offsets), _addr(Y), y_type, _stream(stream))
+    n = 1 if n_experts is None else n_experts
+    try:   # (the plain case, as above)
+        here = _current_device()
+        if (bank.dtype not in _F8 or xq.dtype not in _F8 or bank_scales.dtype is not _FLOAT32 or
+                x_scales.dtype is not _FLOAT32 or bank.get_device() != here or
+                xq.get_device() != here or bank_scales.get_device() != here or
+                x_scales.get_device() != here or Y.get_device() != here or
+                bank.numel() < n * rows * cols or xq.numel() < n_rows * k or
+                bank_scales.numel() < n * ((rows + 127) // 128) * ((cols + 127) // 128) or
+                x_scales.numel() < (k + 127) // 128 * n_rows or Y.numel() < n_rows * n_out or
+                not (bank.is_contiguous() and xq.is_contiguous() and bank_scales.is_contiguous() and
+                     x_scales.is_contiguous() and Y.is_contiguous())):
+            raise TypeError
+        code = _TYPE_OF[Y.dtype] if y_type is None else y_type
+        on = _current_stream() if stream is None else _stream(stream)
+        if n_experts is None:
+            status = getattr(_lib, fn)(
+                bank.data_ptr(), bank_scales.data_ptr(), rows, cols, xq.data_ptr(),
+                x_scales.data_ptr(), n_rows, Y.data_ptr(), code, on)
+        else:
+            if (offsets.dtype is not _INT32 or offsets.numel() <= n or
+                    offsets.get_device() != here or not offsets.is_contiguous()):
+                raise TypeError
+            status = getattr(_lib, fn)(
+                bank.data_ptr(), bank_scales.data_ptr(), n, rows, cols, xq.data_ptr(),
+                x_scales.data_ptr(), n_rows, offsets.data_ptr(), Y.data_ptr(), code, on)
+    except _NOT_PLAIN:
+        if _F8 is None:
+            _f8_types()
+        _need(fn, (bank, _F8, n * rows * cols),
+              (bank_scales, (_FLOAT32,), n * _blocks(rows) * _blocks(cols)),
+              (xq, _F8, n_rows * k), (x_scales, (_FLOAT32,), _blocks(k) * n_rows),
+              (Y, _TYPE_OF, n_rows * n_out), (offsets, (_INT32,), n + 1))
+        y_type = _type(y_type, Y)
+        call = getattr(lib(), fn)
+        if n_experts is None:
+            status = call(_addr(bank), _addr(bank_scales), rows, cols, _addr(xq), _addr(x_scales),
+                          n_rows, _addr(Y), y_type, _stream(stream))
+        else:
+            status = call(_addr(bank), _addr(bank_scales), n, rows, cols, _addr(xq),
+                          _addr(x_scales), n_rows, _addr(offsets), _addr(Y), y_type,
+                          _stream(stream))
     if status:
         _check(fn, status)
 

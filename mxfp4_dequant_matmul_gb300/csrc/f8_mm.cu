@@ -971,6 +971,34 @@ cudaError_t launch_k(const F8Product& p, F8Args a, int split, int per_sm, unsign
                         xmap, a, static_cast<T*>(p.y));
 }
 
+// Clusters of `split` CTAs, per_sm (1 or 2) on an SM, that the device holds at once (its SMs come
+// in groups that a cluster does not cross), 0 where it cannot say.
+int clusters_at_once(int split, int per_sm) {
+    static PerDevice memo[2][3];
+    return memo[per_sm - 1][split / 4].get([&] {
+        auto kernel = per_sm == 1 ? k_f8_mm<float, 128, true, false> : k_f8_mm<float, 32, true, false>;
+        const size_t smem = kSmemMax / per_sm - kSmemSlack;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(split));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(split);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSmemMax - kSmemSlack)) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        return n;
+    });
+}
+
 template <typename T, bool kGrad, bool kPair>
 cudaError_t launch_wide(const F8Product& p, const F8Args& a, cudaStream_t s) {
     using S = Wide<kPair>;
@@ -1029,18 +1057,20 @@ cudaError_t launch_f8_mm(const F8Product& p, cudaStream_t s) {
         a.box = std::min(a.tn, (p.n_rows + 15) / 16 * 16);
         a.n_tt = (p.n_rows + a.tn - 1) / a.tn;
         // tiles for less than two thirds of the SMs: slices of the sum over a cluster, as many as
-        // fit at once (us: 4096x14336, one token 23.1 unsplit, 15.0 by 2, 13.6 by 4; 4096x4096, 128
-        // tokens 21.1, 18.3 and 12.8; with 112 tiles, 14336x4096, one token, 12.8, by 2 13.6)
+        // there is room for at once (us: 4096x14336, one token 23.1 unsplit, 15.0 by 2, 13.3 by 4;
+        // 4096x4096, 128 tokens 21.1, 18.3 and 11.5; 2048x4096, 128 tokens by 4 10.5, by 8, whose
+        // clusters are not all there at once, 17.8; with 112 tiles, 14336x4096, one token, 12.7
+        // unsplit, by 2 13.6)
         const int fit = a.tn <= 32 ? 2 : 1;   // CTAs whose registers an SM holds
         const long tiles = static_cast<long>(a.n_rt) * a.n_tt;
-        while (split < kMaxSplit && 3 * tiles < 2 * sms && tiles * split * 2 <= fit * sms &&
-               split * 2 <= a.n_k)
+        while (split < kMaxSplit && 3 * tiles < 2 * sms && split * 2 <= a.n_k &&
+               tiles <= clusters_at_once(split * 2, fit))
             split *= 2;
-        if (split > 1) per_sm = static_cast<int>((tiles * split + sms - 1) / sms);
+        if (split > 1) per_sm = tiles <= clusters_at_once(split, 1) ? 1 : 2;
         // Past 64 tokens either kernel takes about as long for a block of its tile (1000 cycles),
         // and the other one's tiles are twice as large: it is slower only where this one is split
-        // (us: 4096x4096, 256 tokens 18.4 by 2, 21.8 the other; 512 tokens, not split, 22.0 the
-        // other; 2303x2880, 333 tokens 15.9 by 2 and 21.5).
+        // (us: 4096x4096, 256 tokens 14.9 by 2, 21.8 the other; 512 tokens, not split, 20.4 the
+        // other; 2303x2880, 333 tokens 12.8 by 2 and 21.5).
         wide = a.tn == 128 && split == 1;
     }
     if (wide) {

@@ -16,8 +16,10 @@
 // shared memory (in both operands: zero times whatever lies there may be NaN).  That last stage
 // lands on a barrier of its own CTA, a warp of which writes the zeros before it reports the stage.
 //
-// Warps: copies, MMAs (rank 0), those zeros, eight for the sums.  Persistent: pair c takes tiles
-// c, c + pairs, ...
+// Warps: copies, MMAs (even ranks), those zeros, eight for the sums.  Persistent: pair c takes tiles
+// c, c + pairs, ...  With few tiles and long sums (kSplit) a cluster of two or four pairs shares a
+// tile, each a slice of the stages, and adds the partial sums through distributed shared memory
+// in rank order.
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land, frees its
 // tensor memory and returns.
@@ -43,6 +45,7 @@ constexpr int kBox = 64;                      // elements of a copied row (128 b
 constexpr uint32_t kBoxBytes = kBox * kK * 2;
 constexpr uint32_t kABytes = 2 * kBoxBytes, kStageBytes = 2 * kABytes;   // of dY; and of X
 constexpr int kStages = 6, kChunk = 4;        // ring; stages an accumulator takes
+constexpr int kMaxSplit = 4;                  // pairs that share a tile
 constexpr int kPatch = 32 * 64;               // bytes a warp turns round
 constexpr int kThreads = 384, kEpiWarp = 4, kEpiWarps = 8, kCols = 128;
 constexpr int kMaxExperts = 1024;
@@ -107,7 +110,7 @@ __device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const
     __syncwarp();
 }
 
-template <typename T>
+template <typename T, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grad_w(const __grid_constant__ CUtensorMap dymap, const __grid_constant__ CUtensorMap xmap,
              const WArgs a, T* __restrict__ dw) {
@@ -122,7 +125,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int* abort_flag = &abort_word;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank());
+    const int cluster_rank = static_cast<int>(cluster.block_rank());
+    const int rank = cluster_rank & 1, lead = kSplit ? cluster_rank & ~1 : 0;   // of the pair
+    const int n_split = kSplit ? static_cast<int>(cluster.num_blocks()) / 2 : 1;
 
     if (warp == 1) pair_tmem_take(&tmem_base, 2 * kN);
     if (tid == 0) {
@@ -156,9 +161,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     struct Tile {
         int e, r0, c0, i0, m;
+        int lo, hi;   // this pair's rows of the m, from a multiple of kK on
     };
     const int per_e = a.n_rt * a.n_ct, n_tiles = per_e * a.n_experts;
-    const int tile0 = static_cast<int>(blockIdx.x >> 1), tile_step = static_cast<int>(gridDim.x >> 1);
+    const int tile0 = static_cast<int>(blockIdx.x) / (2 * n_split);
+    const int tile_step = static_cast<int>(gridDim.x) / (2 * n_split);   // (split: one tile each)
     auto tile_at = [&](int tile) {
         Tile t;
         t.e = tile / per_e;
@@ -167,6 +174,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         t.c0 = (local - rt * a.n_ct) * kN;
         t.i0 = off[t.e];
         t.m = max(off[t.e + 1] - t.i0, 0);
+        t.lo = 0;
+        t.hi = t.m;
+        if constexpr (kSplit) {
+            const int stages = (t.m + kK - 1) / kK, q = lead / 2;
+            t.lo = static_cast<int>(static_cast<long long>(stages) * q / n_split) * kK;
+            t.hi = min(static_cast<int>(static_cast<long long>(stages) * (q + 1) / n_split) * kK,
+                       t.m);
+        }
         return t;
     };
     auto fail = [&]() {
@@ -180,13 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // --- copies
         const bool leader = elect_one();
         const uint64_t policy = l2_evict_normal();
-        const uint32_t ring = smem_u32(smem), full0 = leader_addr(&full[0]);
+        const uint32_t ring = smem_u32(smem), full0 = leader_addr(&full[0], lead);
         uint32_t st = 0, phase = 1;   // the first round of the ring passes at once
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             const Tile t = tile_at(tile);
             const int r = t.r0 + rank * kM, c = t.c0 + rank * (kN / 2);
-            for (int i = 0; i < t.m; i += kK) {
+            for (int i = t.lo; i < t.hi; i += kK) {
                 ok = mbar_wait_for(&empty[st], phase, kWait);
                 if (!ok) break;
                 if (leader) {
@@ -232,12 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             const Tile t = tile_at(tile);
             int in_chunk = 0;
-            for (int i = 0; i < t.m; i += kK) {
+            for (int i = t.lo; i < t.hi; i += kK) {
                 ok = in_chunk > 0 || mbar_wait_for(&acc_empty[ab], acc_phase, kWait);
                 ok = ok && mbar_wait_for(&full[st], phase, kWait);
                 if (!ok) break;
                 const int steps = min(kK, t.m - i + 15) >> 4;   // of 16 rows
-                const bool done = in_chunk + 1 == kChunk || i + kK >= t.m;
+                const bool done = in_chunk + 1 == kChunk || i + kK >= t.hi;
                 tc_fence_after();
                 if (leader) {
                     const uint32_t at = st * (kStageBytes >> 4);
@@ -246,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (q < steps)
                             pair_umma_f16(tmem + ab * kN, a0 + at + q * 128, b0 + at + q * 128,
                                           a.idesc, in_chunk + q);
-                    pair_commit(&empty[st]);
-                    if (done) pair_commit(&acc_full[ab]);
+                    pair_commit(&empty[st], lead);
+                    if (done) pair_commit(&acc_full[ab], lead);
                 }
                 __syncwarp();
                 ++in_chunk;
@@ -265,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) {
             fail();
-            if (leader) pair_commit(&drain);
+            if (leader) pair_commit(&drain, lead);
             mbar_wait_for(&drain, 0u, kWait);
         }
         __syncwarp();
@@ -275,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             const Tile t = tile_at(tile);
-            st = (st + static_cast<uint32_t>((t.m + kK - 1) / kK)) % kStages;
-            if ((t.m & 15) == 0) continue;
+            st = (st + static_cast<uint32_t>((t.hi - t.lo + kK - 1) / kK)) % kStages;
+            if ((t.m & 15) == 0 || t.hi < t.m || t.hi <= t.lo) continue;
             const uint32_t last = (st + kStages - 1) % kStages;
             ok = __all_sync(0xFFFFFFFFu,
                             mbar_wait_for(&last_full[last], (phases >> last) & 1u, kWait));
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) pair_arrive_release(leader_addr(&full[last]));
+            if (lane == 0) pair_arrive_release(leader_addr(&full[last], lead));
             ok = !*abort_flag;
         }
         if (!ok) fail();
@@ -301,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int quarter = warp & 3, half = (warp - kEpiWarp) >> 2;
         const uint32_t src = tmem + half * kCols + (static_cast<uint32_t>(quarter * 32) << 16);
-        const uint32_t done = leader_addr(&acc_empty[0]);
+        const uint32_t done = leader_addr(&acc_empty[0], lead);
         uint8_t* patch = smem + kStages * kStageBytes + (warp - kEpiWarp) * kPatch;
         uint32_t ab = 0, acc_phase = 0;
         bool ok = true;
@@ -310,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float2 sum[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
-            for (int i = 0; i < t.m; i += kK * kChunk) {
+            for (int i = t.lo; i < t.hi; i += kK * kChunk) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(&acc_full[ab], acc_phase, kWait));
                 if (!ok) break;
                 tc_fence_after();
@@ -338,6 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fail();
                 break;
             }
+            if constexpr (kSplit) {
+                // [row][column] partial sums of this CTA, over the ring: every copy and MMA of the
+                // pair is done once its last accumulator was handed over
+                float4* part = reinterpret_cast<float4*>(smem) + (quarter * 32 + lane) * (kN / 4);
+#pragma unroll
+                for (int c = 0; c < kCols / 4; ++c)
+                    part[(half * (kCols / 4) + c) ^ lane] = make_float4(
+                        sum[2 * c].x, sum[2 * c].y, sum[2 * c + 1].x, sum[2 * c + 1].y);
+                continue;   // (its one tile)
+            }
             const int r = t.r0 + rank * kM + quarter * 32, c0 = t.c0 + half * kCols;
             T* dst = dw + (static_cast<size_t>(t.e) * a.rows + r) * a.cols + c0;
             constexpr int kE = 64 / sizeof(T);
@@ -354,6 +379,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*abort_flag && tid == 0) {
         // a CTA that gave up: its copies in flight land long before this
         for (const long long t0 = clock64(); clock64() - t0 < kDrain;) __nanosleep(1000);
+    }
+    if constexpr (kSplit) {
+        cluster.sync();   // every pair's partial sums are written
+        const Tile t = tile_at(tile0);
+        const int q = lead / 2, row_lo = kM * q / n_split, row_hi = kM * (q + 1) / n_split;
+        for (int i = row_lo * (kN / 4) + tid; i < row_hi * (kN / 4) && !*abort_flag; i += kThreads) {
+            const int row = i / (kN / 4), c4 = i % (kN / 4);
+            const int at = row * (kN / 4) + (c4 ^ (row & 31));
+            float4 v[kMaxSplit];   // all loads on their way before the first sum
+#pragma unroll
+            for (int s = 0; s < kMaxSplit; ++s)
+                if (s < n_split)
+                    v[s] = cluster.map_shared_rank(reinterpret_cast<const float4*>(smem),
+                                                   2 * s + rank)[at];
+            float f[4] = {};
+#pragma unroll
+            for (int s = 0; s < kMaxSplit; ++s)
+                if (s < n_split) {
+                    f[0] += v[s].x;
+                    f[1] += v[s].y;
+                    f[2] += v[s].z;
+                    f[3] += v[s].w;
+                }
+            const int r = t.r0 + rank * kM + row, c = t.c0 + c4 * 4;
+            Pack<T, 4> p;
+            p.set(f);
+            if (r < a.rows && c < a.cols)
+                store_pack(reinterpret_cast<Pack<T, 4>*>(
+                               dw + (static_cast<size_t>(t.e) * a.rows + r) * a.cols + c),
+                           p);
+        }
     }
     tc_fence_before();
     cluster.sync();   // neither leaves while the other still multiplies from its memory
@@ -378,21 +434,55 @@ bool row_map(CUtensorMap* map, const void* base, int width, int n_rows, int type
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T>
-cudaError_t launch_t(const CUtensorMap& dymap, const CUtensorMap& xmap, WArgs a, void* dw,
-                     cudaStream_t s) {
-    constexpr size_t kSmem = kStages * kStageBytes + kEpiWarps * kPatch + 1024;
+constexpr size_t kSmem = kStages * kStageBytes + kEpiWarps * kPatch + 1024;
+
+template <typename T, bool kSplit>
+cudaError_t allow_smem() {
     static PerDevice memo;
-    const cudaError_t attr_err = static_cast<cudaError_t>(memo.get([] {
-        return static_cast<int>(cudaFuncSetAttribute(
-            k_grad_w<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)));
+    return static_cast<cudaError_t>(memo.get([] {
+        return static_cast<int>(cudaFuncSetAttribute(k_grad_w<T, kSplit>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     static_cast<int>(kSmem)));
     }));
+}
+
+// Clusters of 2 * split CTAs that the device holds at once (its SMs come in groups that a cluster
+// does not cross), 0 where it cannot say.
+template <typename T>
+int clusters_at_once(int split) {
+    static PerDevice memo[2];
+    return memo[split / 4].get([&] {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2u * static_cast<unsigned>(split));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2u * static_cast<unsigned>(split);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (allow_smem<T, true>() != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, k_grad_w<T, true>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+        return n;
+    });
+}
+
+template <typename T, bool kSplit>
+cudaError_t launch_t(const CUtensorMap& dymap, const CUtensorMap& xmap, WArgs a, int split,
+                     void* dw, cudaStream_t s) {
+    const cudaError_t attr_err = allow_smem<T, kSplit>();
     if (attr_err != cudaSuccess) return attr_err;
     a.wide = (reinterpret_cast<uintptr_t>(dw) | static_cast<uintptr_t>(a.cols) * sizeof(T)) % 32 == 0;
     const int tiles = a.n_rt * a.n_ct * a.n_experts;
-    return launch_after(k_grad_w<T>,
-                        dim3(2u * static_cast<unsigned>(std::min(tiles, sm_count() / 2))), kThreads,
-                        kSmem, s, 2, dymap, xmap, a, static_cast<T*>(dw));
+    const unsigned ctas = 2u * static_cast<unsigned>(split);
+    return launch_after(k_grad_w<T, kSplit>,
+                        dim3(ctas * static_cast<unsigned>(std::min(tiles, sm_count() / 2))),
+                        kThreads, kSmem, s, ctas, dymap, xmap, a, static_cast<T*>(dw));
 }
 
 }  // namespace
@@ -415,8 +505,19 @@ cudaError_t launch_mm_grad_w(const void* dy, const void* x, int type, int n_expe
     CUtensorMap dymap, xmap;
     if (!row_map(&dymap, dy, rows, n_rows, type) || !row_map(&xmap, x, cols, n_rows, type))
         return cudaErrorNotSupported;
-    return dw_type == kTypeF32 ? launch_t<float>(dymap, xmap, a, dw, s)
-                               : launch_t<__nv_bfloat16>(dymap, xmap, a, dw, s);
+    const long tiles = static_cast<long>(a.n_rt) * a.n_ct * n_experts;
+    auto go = [&](auto one) {
+        using T = decltype(one);
+        // slices of a tile's rows where their clusters are all there at once, and the mean
+        // expert has four stages a slice
+        int split = 1;
+        while (split < kMaxSplit && n_rows / n_experts >= split * 2 * 4 * kK &&
+               tiles <= clusters_at_once<T>(split * 2))
+            split *= 2;
+        return split > 1 ? launch_t<T, true>(dymap, xmap, a, split, dw, s)
+                         : launch_t<T, false>(dymap, xmap, a, 1, dw, s);
+    };
+    return dw_type == kTypeF32 ? go(float{}) : go(__nv_bfloat16{});
 }
 
 cudaError_t read_fault_grad_w(int* value, bool reset) {

@@ -107,12 +107,12 @@ __device__ __forceinline__ uint64_t operand_desc_mn64(uint32_t saddr) {
            (static_cast<uint64_t>(4) << 61);
 }
 
-// --- pairs of CTAs that share their MMAs (cta_group::2): rank 0 issues them ------------------
+// --- pairs of CTAs that share their MMAs (cta_group::2): the even rank issues them -----------
 
-// The address of rank 0's copy of a shared variable.
-__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+// The address of CTA `leader`'s copy of a shared variable (the pair's even rank in its cluster).
+__device__ __forceinline__ uint32_t leader_addr(const void* p, int leader = 0) {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(leader));
     return r;
 }
 // A copy into this CTA that completes on a barrier of either.
@@ -148,11 +148,11 @@ __device__ __forceinline__ void pair_arrive_release(uint32_t bar) {
                  : "memory");
 }
 // Arrives on both CTAs' barrier once the MMAs so far are done.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+__device__ __forceinline__ void pair_commit(uint64_t* bar, int leader = 0) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)),
-        "h"(static_cast<uint16_t>(3))
+        "h"(static_cast<uint16_t>(3 << leader))
         : "memory");
 }
 __device__ __forceinline__ void pair_tmem_take(uint32_t* dst, uint32_t columns) {

@@ -223,7 +223,8 @@ def test_many_tiles_a_block(mx, n, rows, cols, mean, grad):
 
 
 @pytest.mark.parametrize("t", ["bf16", "f16"])
-@pytest.mark.parametrize("rows,cols,counts", [(520, 776, [1000, 0, 3, 257, 256, 64]), (2056, 264, [513, 5000]), (24, 2040, [17] * 40)])
+@pytest.mark.parametrize("rows,cols,counts", [(520, 776, [1000, 0, 3, 257, 256, 64]), (2056, 264, [513, 5000]), (24, 2040, [17] * 40),
+                                              (264, 136, [5001]), (256, 256, [2100, 3]), (248, 520, [0, 4099, 2, 4000]), (8, 8, [8192])])
 def test_grad_w_of_long_sums_and_many_tiles(mx, rows, cols, counts, t):
     off = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
     g = torch.Generator(device="cuda").manual_seed(rows)
