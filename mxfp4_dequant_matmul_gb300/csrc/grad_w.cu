@@ -16,6 +16,11 @@
 // shared memory (in both operands: zero times whatever lies there may be NaN).  That last stage
 // lands on a barrier of its own CTA, a warp of which writes the zeros before it reports the stage.
 //
+// What bounds it: 4096 tokens top-4 of 16 experts 2880x2880 bf16 into f32, 243 us, 1.1 PFLOP/s: 182
+// without the stores, in which a stage takes about 700 cycles (the MMAs 512), as either CTA's 32 KB
+// come from L2 at some 50 bytes a cycle; the stores are as much again as a fifth of those copies.
+// One matrix 2048x2048, 8192 rows: 46 us, 1.5 PFLOP/s.
+//
 // Warps: copies, MMAs (even ranks), those zeros, eight for the sums.  Persistent: pair c takes tiles
 // c, c + pairs, ...  With few tiles and long sums (kSplit) a cluster of two or four pairs shares a
 // tile, each a slice of the stages, and adds the partial sums through distributed shared memory
@@ -44,9 +49,9 @@ constexpr int kM = 128, kN = 256, kK = 64;    // a CTA's rows, a tile's columns,
 constexpr int kBox = 64;                      // elements of a copied row (128 bytes)
 constexpr uint32_t kBoxBytes = kBox * kK * 2;
 constexpr uint32_t kABytes = 2 * kBoxBytes, kStageBytes = 2 * kABytes;   // of dY; and of X
-constexpr int kStages = 6, kChunk = 4;        // ring; stages an accumulator takes
+constexpr int kStages = 5, kChunk = 4;        // ring; stages an accumulator takes
 constexpr int kMaxSplit = 4;                  // pairs that share a tile
-constexpr int kPatch = 32 * 64;               // bytes a warp turns round
+constexpr int kPatch = 32 * 128;               // bytes a warp turns round
 constexpr int kThreads = 384, kEpiWarp = 4, kEpiWarps = 8, kCols = 128;
 constexpr int kMaxExperts = 1024;
 constexpr long long kWait = 1ll << 32, kDrain = 1ll << 24;   // SM cycles: about 2 s and 8 ms
@@ -70,32 +75,32 @@ __device__ __forceinline__ void pair_umma_f16(uint32_t d, uint64_t a, uint64_t b
         : "memory");
 }
 
-// 64 bytes of outputs of each lane's row (n elements of them exist, a multiple of 8) for `rows`
-// rows, turned round in shared memory, so that a store is 64 bytes of 16 rows and not 32 of 32:
-// the stores of a tile are waited for by the next tile's sums.  Rows are 16-byte aligned, or 32
-// (wide).
+// 128 bytes of outputs of each lane's row (n elements of them exist, a multiple of 8) for `rows`
+// rows, turned round in shared memory, so that a store is whole lines of 8 rows and not 32 bytes of
+// 32 (4096 tokens top-4 of 16 experts 2880x2880: 274 us with those, 252 with 64 bytes of 16 rows,
+// 243).  Rows are 16-byte aligned, or 32 (wide).
 template <typename T>
 __device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const float2* sum,
                                              int n, uint8_t* patch, int lane, bool wide) {
     constexpr int kE = 16 / sizeof(T);   // elements of a 16-byte unit
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 8; ++q) {
         float f[kE];
 #pragma unroll
         for (int i = 0; i < kE; ++i)
             f[i] = i % 2 ? sum[(q * kE + i) / 2].y : sum[(q * kE + i) / 2].x;
         Pack<T, kE> p;
         p.set(f);
-        *reinterpret_cast<uint4*>(patch + lane * 64 + (q ^ (lane >> 1 & 3)) * 16) = p.raw;
+        *reinterpret_cast<uint4*>(patch + lane * 128 + (q ^ (lane & 7)) * 16) = p.raw;
     }
     __syncwarp();
-    const int c = lane % 2 * 2;          // this lane's first unit of a row
+    const int c = lane % 4 * 2;          // this lane's first unit of a row
 #pragma unroll
-    for (int r = lane / 2; r < 32; r += 16) {
+    for (int r = lane / 4; r < 32; r += 8) {
         const uint4 lo =
-            *reinterpret_cast<const uint4*>(patch + r * 64 + (c ^ (r >> 1 & 3)) * 16);
+            *reinterpret_cast<const uint4*>(patch + r * 128 + (c ^ (r & 7)) * 16);
         const uint4 hi =
-            *reinterpret_cast<const uint4*>(patch + r * 64 + ((c + 1) ^ (r >> 1 & 3)) * 16);
+            *reinterpret_cast<const uint4*>(patch + r * 128 + ((c + 1) ^ (r & 7)) * 16);
         if (r >= rows) break;
         uint4* dst = reinterpret_cast<uint4*>(y + static_cast<size_t>(r) * pitch + c * kE);
         if (wide && (c + 2) * kE <= n) {
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const int r = t.r0 + rank * kM + quarter * 32, c0 = t.c0 + half * kCols;
             T* dst = dw + (static_cast<size_t>(t.e) * a.rows + r) * a.cols + c0;
-            constexpr int kE = 64 / sizeof(T);
+            constexpr int kE = 128 / sizeof(T);
 #pragma unroll
             for (int c = 0; c < kCols; c += kE)
                 if (c0 + c < a.cols && r < a.rows)
