@@ -83,6 +83,48 @@ __device__ __forceinline__ void store_pack(P* p, const P& v) {
         p->raw = v.raw;
 }
 
+// kBytes (64 or 128) of outputs of each lane's row (n of their elements exist, whole 16-byte units)
+// for `rows` rows of a warp, turned round in kBytes * 32 bytes of shared memory (patch), so that a
+// store is kBytes of several rows and not 32 bytes of 32.  Rows are 16-byte aligned, or 32 (wide).
+template <typename T, int kBytes>
+__device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const float2* sum,
+                                             int n, uint8_t* patch, int lane, bool wide) {
+    constexpr int kE = 16 / sizeof(T);     // elements of a 16-byte unit
+    constexpr int kUnits = kBytes / 16, kLanes = kUnits / 2;   // of a row; lanes that store one
+    // (8 lanes' units in 8 different groups of 4 banks, both ways)
+    auto unit = [&](int row, int q) {
+        const int x = kBytes == 128 ? row & 7 : (row >> 1) & 3;
+        return reinterpret_cast<uint4*>(patch + row * kBytes + (q ^ x) * 16);
+    };
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+        float f[kE];
+#pragma unroll
+        for (int i = 0; i < kE; ++i)
+            f[i] = i % 2 ? sum[(q * kE + i) / 2].y : sum[(q * kE + i) / 2].x;
+        Pack<T, kE> p;
+        p.set(f);
+        *unit(lane, q) = p.raw;
+    }
+    __syncwarp();
+    const int c = lane % kLanes * 2;       // this lane's first unit of a row
+#pragma unroll
+    for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
+        const uint4 lo = *unit(r, c), hi = *unit(r, c + 1);
+        if (r >= rows) break;
+        uint4* dst = reinterpret_cast<uint4*>(y + static_cast<size_t>(r) * pitch + c * kE);
+        if (wide && (c + 2) * kE <= n) {
+            Pack<T, 2 * kE> p;
+            p.raw = Raw32{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+            store_pack(reinterpret_cast<Pack<T, 2 * kE>*>(dst), p);
+        } else {
+            if (c * kE < n) dst[0] = lo;
+            if ((c + 1) * kE < n) dst[1] = hi;
+        }
+    }
+    __syncwarp();
+}
+
 // i / d for 0 <= i < 2^32 as one multiplication (Granlund & Montgomery 1994): m =
 // ceil(2^(32 + s) / d) with s = ceil(log2 d), one bit more than 32 bits hold.
 struct FastDiv {

@@ -551,11 +551,11 @@ struct Wide {
     static constexpr size_t kSmem = kStages * kStage + kWEpiWarps * kWPatch * 4 + 1024;
 };
 
-// 16 of a lane's sums (its row's outputs c0 .. c0 + 15, of which n exist) for rows of any
-// alignment: turned round in shared memory, so that a store is two rows' 16 outputs.
+// 16 of a lane's sums (n of them exist) for rows of any alignment: as store_turned, element by
+// element, two rows' 16 outputs a store.
 template <typename T>
-__device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const float2* sum,
-                                             int n, float* patch, int lane) {
+__device__ __forceinline__ void store_any(T* y, size_t pitch, int rows, const float2* sum, int n,
+                                          float* patch, int lane) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         patch[lane * 16 + ((2 * i) ^ (lane >> 1 & 15))] = sum[i].x;
@@ -812,8 +812,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
             tmem + group * kWCols + (static_cast<uint32_t>(quarter * 32) << 16);
         const uint32_t done =
             kPair ? leader_addr(&acc_empty[group]) : smem_u32(&acc_empty[group]);
-        const bool aligned =
-            (reinterpret_cast<uintptr_t>(Y) | static_cast<size_t>(a.n_out) * sizeof(T)) % 32 == 0;
+        const uint32_t align = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(Y) |
+                                                     static_cast<size_t>(a.n_out) * sizeof(T));
         float* patch = patches + (warp - kWEpiWarp) * kWPatch;
         uint32_t ab = 0, acc_phase = 0, slot = 0, fac_phase = 0;
         int j = 0;
@@ -869,28 +869,21 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 break;
             }
             T* dst = Y + static_cast<size_t>(row0) * a.n_out + c0;
-            if (aligned && a.n_out - c0 >= kWCols) {
-                constexpr int kN = 32 / sizeof(T);
-                Pack<T, kN>* out =
-                    reinterpret_cast<Pack<T, kN>*>(dst + static_cast<size_t>(lane) * a.n_out);
-                if (lane < rows) {
+            if (align % 16 == 0) {
+                constexpr int kE = 64 / sizeof(T);
 #pragma unroll
-                    for (int q = 0; q < kWCols / kN; ++q) {
-                        float f[kN];
-#pragma unroll
-                        for (int i = 0; i < kN; ++i)
-                            f[i] = i % 2 ? sum[(q * kN + i) / 2].y : sum[(q * kN + i) / 2].x;
-                        Pack<T, kN> p;
-                        p.set(f);
-                        store_pack(out + q, p);
-                    }
-                }
+                for (int c = 0; c < kWCols; c += kE)
+                    if (c0 + c < a.n_out)
+                        store_turned<T, 64>(dst + c, static_cast<size_t>(a.n_out), rows,
+                                            &sum[c / 2], a.n_out - c0 - c,
+                                            reinterpret_cast<uint8_t*>(patch), lane,
+                                            align % 32 == 0);
             } else {
 #pragma unroll
                 for (int c = 0; c < kWCols; c += 16)
                     if (c0 + c < a.n_out)
-                        store_turned(dst + c, static_cast<size_t>(a.n_out), rows, &sum[c / 2],
-                                     a.n_out - c0 - c, patch, lane);
+                        store_any(dst + c, static_cast<size_t>(a.n_out), rows, &sum[c / 2],
+                                  a.n_out - c0 - c, patch, lane);
             }
             ok = !*abort_flag;
         }

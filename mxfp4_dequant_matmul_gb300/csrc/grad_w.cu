@@ -75,46 +75,6 @@ __device__ __forceinline__ void pair_umma_f16(uint32_t d, uint64_t a, uint64_t b
         : "memory");
 }
 
-// 128 bytes of outputs of each lane's row (n elements of them exist, a multiple of 8) for `rows`
-// rows, turned round in shared memory, so that a store is whole lines of 8 rows and not 32 bytes of
-// 32 (4096 tokens top-4 of 16 experts 2880x2880: 274 us with those, 252 with 64 bytes of 16 rows,
-// 243).  Rows are 16-byte aligned, or 32 (wide).
-template <typename T>
-__device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const float2* sum,
-                                             int n, uint8_t* patch, int lane, bool wide) {
-    constexpr int kE = 16 / sizeof(T);   // elements of a 16-byte unit
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        float f[kE];
-#pragma unroll
-        for (int i = 0; i < kE; ++i)
-            f[i] = i % 2 ? sum[(q * kE + i) / 2].y : sum[(q * kE + i) / 2].x;
-        Pack<T, kE> p;
-        p.set(f);
-        *reinterpret_cast<uint4*>(patch + lane * 128 + (q ^ (lane & 7)) * 16) = p.raw;
-    }
-    __syncwarp();
-    const int c = lane % 4 * 2;          // this lane's first unit of a row
-#pragma unroll
-    for (int r = lane / 4; r < 32; r += 8) {
-        const uint4 lo =
-            *reinterpret_cast<const uint4*>(patch + r * 128 + (c ^ (r & 7)) * 16);
-        const uint4 hi =
-            *reinterpret_cast<const uint4*>(patch + r * 128 + ((c + 1) ^ (r & 7)) * 16);
-        if (r >= rows) break;
-        uint4* dst = reinterpret_cast<uint4*>(y + static_cast<size_t>(r) * pitch + c * kE);
-        if (wide && (c + 2) * kE <= n) {
-            Pack<T, 2 * kE> p;
-            p.raw = Raw32{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-            store_pack(reinterpret_cast<Pack<T, 2 * kE>*>(dst), p);
-        } else {
-            if (c * kE < n) dst[0] = lo;
-            if ((c + 1) * kE < n) dst[1] = hi;
-        }
-    }
-    __syncwarp();
-}
-
 template <typename T, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grad_w(const __grid_constant__ CUtensorMap dymap, const __grid_constant__ CUtensorMap xmap,
@@ -371,10 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int r = t.r0 + rank * kM + quarter * 32, c0 = t.c0 + half * kCols;
             T* dst = dw + (static_cast<size_t>(t.e) * a.rows + r) * a.cols + c0;
             constexpr int kE = 128 / sizeof(T);
+            // (4096 tokens top-4 of 16 experts 2880x2880: 243 us, with 64 bytes of 16 rows a store
+            // 252, with 32 bytes of 32 rows 274)
 #pragma unroll
             for (int c = 0; c < kCols; c += kE)
                 if (c0 + c < a.cols && r < a.rows)
-                    store_turned(dst + c, static_cast<size_t>(a.cols), a.rows - r, &sum[c / 2],
+                    store_turned<T, 128>(dst + c, static_cast<size_t>(a.cols), a.rows - r, &sum[c / 2],
                                  a.cols - c0 - c, patch, lane, a.wide != 0);
             ok = !*abort_flag;
         }
