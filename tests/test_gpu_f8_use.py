@@ -421,3 +421,72 @@ def test_gradients_against_differences(mx, nb):
     bound += (np.abs(step) * ref.sum_bound(nb, 16, 0) * ref.grad_w(dyv, xv, [0, nb])[1][0]).sum()
     got, want = (dw.double().cpu().numpy() * step).sum(), (dyv * (z[1] - z[0])).sum()
     assert abs(got - want) <= bound
+
+
+# --- streams and captures ----------------------------------------------------------------------
+
+
+def test_a_stream_given_by_the_caller(mx):
+    """Calls on a stream of the caller's, while torch's current one does something else."""
+    layer = Layer(mx, 32, 4, 16, 400, 160)
+    b, want = layer.fresh(1)
+    s, xq, xs = torch.cuda.Stream(), torch.zeros_like(b["xq"]), torch.zeros_like(b["xs"])
+    o, dW = torch.zeros_like(b["o"]), torch.zeros_like(want["dW"])
+    torch.cuda.synchronize()
+    mx.mxfp4_f8_quant(layer.x[1], 32, 400, 400, b["token_at"], 128, xq, xs, stream=s)
+    mx.mxfp4_f8_moe_mm(layer.bank, layer.bs, 16, 160, 400, xq, xs, 128, b["offsets"], o, stream=s)
+    mx.mxfp4_moe_mm_grad_w(b["d_o"], b["xv"], 16, 160, 400, 128, b["offsets"], dW, stream=s.cuda_stream)
+    s.synchronize()
+    m = int(b["offsets"][-1])
+    assert torch.equal(o[:m], b["o"][:m]) and torch.equal(dW, want["dW"])
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import mxfp4_dequant_matmul_gb300 as mx
+torch.zeros(1, device="cuda")
+g = torch.Generator(device="cuda").manual_seed(1)
+code = lambda *s: torch.randint(0, 120, s, generator=g, device="cuda", dtype=torch.uint8)
+num = lambda *s: torch.rand(s, generator=g, device="cuda")
+new = lambda *s, **k: torch.zeros(s, device="cuda", **k)
+off = torch.tensor([0, 3, 700], dtype=torch.int32, device="cuda")
+w, ws, x, xs, d, ds = code(2, 1040, 528), num(2, 9, 5), code(700, 528), num(5, 700), code(700, 1040), num(9, 700)
+h, k = num(4000, 1040).bfloat16(), num(4000, 528).bfloat16()
+def calls():
+    out = [new(700, 528, dtype=torch.uint8), new(5, 700), new(2, 1040, 528, dtype=torch.uint8), new(2, 9, 5)]
+    mx.mxfp4_f8_quant(k, 700, 528, 528, None, 700, out[0], out[1])
+    mx.mxfp4_f8_quant_weight(w.bfloat16(), 2, 1040, 528, out[2], out[3])
+    for nb in (1, 100, 700):
+        out += [new(nb, 1040), new(nb, 528)]
+        mx.mxfp4_f8_mm(w, ws, 1040, 528, x, xs.flatten()[:5 * nb], nb, out[-2])
+        mx.mxfp4_f8_mm_grad(w, ws, 1040, 528, d, ds.flatten()[:9 * nb], nb, out[-1])
+    out += [new(700, 1040), new(700, 528), new(2, 1040, 528), new(1040, 528)]
+    mx.mxfp4_f8_moe_mm(w, ws, 2, 1040, 528, x, xs, 700, off, out[-4])
+    mx.mxfp4_f8_moe_mm_grad(w, ws, 2, 1040, 528, d, ds, 700, off, out[-3])
+    mx.mxfp4_moe_mm_grad_w(h, k, 2, 1040, 528, 700, off, out[-2])
+    mx.mxfp4_mm_grad_w(h, k, 1040, 528, 4000, out[-1])
+    return out
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    first = calls()
+graph.replay()
+torch.cuda.synchronize()
+again = calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, again)) and all(a.float().abs().sum() > 0 for a in first)
+assert mx.mxfp4_device_faults() == 0
+print("captured")
+"""
+
+
+def test_first_calls_under_capture(mx):
+    """Nothing that a first call sets up (attributes, occupancies, modules) stops a capture."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALL.format(root=os.path.dirname(tests), tests=tests)],
+                         capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stdout + run.stderr
