@@ -83,21 +83,19 @@ __device__ __forceinline__ void store_pack(P* p, const P& v) {
         p->raw = v.raw;
 }
 
-// kBytes (64 or 128) of outputs of each lane's row (n of their elements exist, whole 16-byte units)
-// for `rows` rows of a warp, turned round in kBytes * 32 bytes of shared memory (patch), so that a
-// store is kBytes of several rows and not 32 bytes of 32.  Rows are 16-byte aligned, or 32 (wide).
-template <typename T, int kBytes>
+// 64 bytes of outputs of each lane's row (n of their elements exist, whole 16-byte units) for `rows`
+// rows of a warp, turned round in 2 KB of shared memory (patch), so that a store is 64 bytes of
+// 16 rows and not 32 bytes of 32.  Rows are 16-byte aligned, or 32 (wide).
+template <typename T>
 __device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const float2* sum,
                                              int n, uint8_t* patch, int lane, bool wide) {
     constexpr int kE = 16 / sizeof(T);     // elements of a 16-byte unit
-    constexpr int kUnits = kBytes / 16, kLanes = kUnits / 2;   // of a row; lanes that store one
     // (8 lanes' units in 8 different groups of 4 banks, both ways)
     auto unit = [&](int row, int q) {
-        const int x = kBytes == 128 ? row & 7 : (row >> 1) & 3;
-        return reinterpret_cast<uint4*>(patch + row * kBytes + (q ^ x) * 16);
+        return reinterpret_cast<uint4*>(patch + row * 64 + (q ^ ((row >> 1) & 3)) * 16);
     };
 #pragma unroll
-    for (int q = 0; q < kUnits; ++q) {
+    for (int q = 0; q < 4; ++q) {
         float f[kE];
 #pragma unroll
         for (int i = 0; i < kE; ++i)
@@ -107,9 +105,9 @@ __device__ __forceinline__ void store_turned(T* y, size_t pitch, int rows, const
         *unit(lane, q) = p.raw;
     }
     __syncwarp();
-    const int c = lane % kLanes * 2;       // this lane's first unit of a row
+    const int c = lane % 2 * 2;            // this lane's first unit of a row
 #pragma unroll
-    for (int r = lane / kLanes; r < 32; r += 32 / kLanes) {
+    for (int r = lane / 2; r < 32; r += 16) {
         const uint4 lo = *unit(r, c), hi = *unit(r, c + 1);
         if (r >= rows) break;
         uint4* dst = reinterpret_cast<uint4*>(y + static_cast<size_t>(r) * pitch + c * kE);

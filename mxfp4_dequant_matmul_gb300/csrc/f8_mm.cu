@@ -13,11 +13,12 @@
 // rows), MMAs, scales (asynchronous copies of 4 bytes, several blocks ahead: fetched when they
 // are needed, their latency bounded a block), and eight warps for the sums.
 //
-// What bounds them: few tokens, HBM (64 experts 2880x2880, 32 tokens, top-4: 69 us, 6.6 TB/s; one
-// token 14336x4096 12.8 us, of which the stream of the weights is 8.8); many tokens, about 1000 cycles a
-// block of 128 x 256 sums: copies and MMAs without the sums take 935, as either brings 48 KB of
-// operands through shared memory a block (2048 tokens 4096x14336: 123 us, 1.95 PFLOP/s; 4096 tokens
-// 4096x4096 by its rows' gradient 78 us).
+// What bounds them: few tokens, HBM (64 experts 2880x2880, 32 tokens, top-4: 66 us, 6.6 TB/s; one
+// token 14336x4096 12.7 us, of which the stream of the weights is 8.8); many tokens, about 900 to
+// 1000 cycles a block of 128 x 256 sums, of which the MMAs are 512: by single CTAs copies and MMAs
+// take 935, as 48 KB of operands go through shared memory, by pairs the accumulators' way
+// round (2048 tokens 4096x14336 107 us, 2.2 PFLOP/s; 4096 tokens 4096x4096 by the rows 65 us, 2.1;
+// 2048 tokens, top-4 of 64 experts 2880x2880, 123 us).
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land, frees its
 // tensor memory and returns.
@@ -536,19 +537,21 @@ __global__ void __launch_bounds__(kThreads, NC <= 32 ? 2 : 1)
 // kPair: two CTAs share each MMA (256 tokens; either brings its 128 and half of the outputs'
 // rows), so that an operand byte is fetched for twice the products.  Then the hand-over crosses the
 // pair, and tiles are coarser: better for one matrix with many tokens, not for experts (us: 2048
-// tokens 4096x14336 110, single CTAs 123; a prompt's experts 147 and 131).
+// tokens 4096x14336 108, single CTAs 123; a prompt's experts 147 and 131).  Results leave by copies
+// from shared memory where rows are 16-byte aligned (4096 tokens 8192x2048 into f32 72 us, by stores
+// 79); an expert's last tile must not write past its rows, so there by stores.
 constexpr int kWN = 256;
 constexpr uint32_t kWHalf = kM * kF8Block;   // 128 rows of a stage
 constexpr int kWThreads = 384, kWEpiWarp = 4, kWEpiWarps = 8, kWCols = 128;
 constexpr int kWFac = 8;           // blocks whose scales are held
-constexpr int kWPatch = 32 * 16;   // floats a warp turns round for rows that are not aligned
 template <bool kPair>
 struct Wide {
     static constexpr uint32_t kWRows = kPair ? kM : kWN;   // outputs that a CTA brings
     static constexpr uint32_t kStage = kWHalf + kWRows * kF8Block;
-    static constexpr int kStages = kPair ? 6 : 4;
+    static constexpr int kStages = kPair ? 5 : 4;
+    static constexpr int kPatch = kPair ? 4096 : 2048;     // bytes a warp stores at a time
     static constexpr int kBox = kPair ? 64 : 128;          // outputs of a copy: a CTA's of a half
-    static constexpr size_t kSmem = kStages * kStage + kWEpiWarps * kWPatch * 4 + 1024;
+    static constexpr size_t kSmem = kStages * kStage + kWEpiWarps * kPatch + 1024;
 };
 
 // 16 of a lane's sums (n of them exist) for rows of any alignment: as store_turned, element by
@@ -590,7 +593,7 @@ __device__ __forceinline__ void wide_commit(uint64_t* bar) {
 template <typename T, bool kGrad, bool kPair>
 __global__ void __launch_bounds__(kWThreads, 1)
     k_f8_wide(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-              const F8Args a, T* __restrict__ Y) {
+              const __grid_constant__ CUtensorMap ymap, const F8Args a, T* __restrict__ Y) {
     using S = Wide<kPair>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -602,8 +605,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     __shared__ int abort_word, n_tiles_sh;
     __shared__ Tile table[kTileTable];
     volatile int* abort_flag = &abort_word;
-    float* patches = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
-    int32_t* off = reinterpret_cast<int32_t*>(patches + kWEpiWarps * kWPatch);
+    uint8_t* patches = smem + S::kStages * S::kStage;
+    int32_t* off = reinterpret_cast<int32_t*>(patches + kWEpiWarps * S::kPatch);
     int32_t* first = off + a.n_experts + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = kPair ? static_cast<int>(cg::this_cluster().block_rank()) : 0;
@@ -814,7 +817,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             kPair ? leader_addr(&acc_empty[group]) : smem_u32(&acc_empty[group]);
         const uint32_t align = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(Y) |
                                                      static_cast<size_t>(a.n_out) * sizeof(T));
-        float* patch = patches + (warp - kWEpiWarp) * kWPatch;
+        uint8_t* patch = patches + (warp - kWEpiWarp) * S::kPatch;
         uint32_t ab = 0, acc_phase = 0, slot = 0, fac_phase = 0;
         int j = 0;
         bool ok = true;
@@ -869,23 +872,54 @@ __global__ void __launch_bounds__(kWThreads, 1)
                 break;
             }
             T* dst = Y + static_cast<size_t>(row0) * a.n_out + c0;
-            if (align % 16 == 0) {
+            if (kPair && align % 16 == 0) {
+                // 128 bytes of the 32 rows at a time, by copies from shared memory (which cut off
+                // at the matrix's edges): the warp goes on while they run
+                constexpr int kE = 128 / sizeof(T), kUnit = 16 / sizeof(T);
+#pragma unroll
+                for (int c = 0; c < kWCols; c += kE) {
+                    if (lane == 0) bulk_wait_read<0>();   // the last copy has read the patch
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        float f[kUnit];
+#pragma unroll
+                        for (int i = 0; i < kUnit; ++i) {
+                            const float2 v = sum[(c + q * kUnit + i) / 2];
+                            f[i] = i % 2 ? v.y : v.x;
+                        }
+                        Pack<T, kUnit> p;
+                        p.set(f);
+                        *reinterpret_cast<uint4*>(patch + lane * 128 + (q ^ (lane & 7)) * 16) =
+                            p.raw;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (c0 + c < a.n_out && rows > 0)
+                            tma2d_store(&ymap, c0 + c, row0, smem_u32(patch));
+                        bulk_commit();
+                    }
+                }
+            } else if (align % 16 == 0) {
                 constexpr int kE = 64 / sizeof(T);
 #pragma unroll
                 for (int c = 0; c < kWCols; c += kE)
                     if (c0 + c < a.n_out)
-                        store_turned<T, 64>(dst + c, static_cast<size_t>(a.n_out), rows,
-                                            &sum[c / 2], a.n_out - c0 - c,
-                                            reinterpret_cast<uint8_t*>(patch), lane,
-                                            align % 32 == 0);
+                        store_turned(dst + c, static_cast<size_t>(a.n_out), rows, &sum[c / 2],
+                                     a.n_out - c0 - c, patch, lane, align % 32 == 0);
             } else {
 #pragma unroll
                 for (int c = 0; c < kWCols; c += 16)
                     if (c0 + c < a.n_out)
                         store_any(dst + c, static_cast<size_t>(a.n_out), rows, &sum[c / 2],
-                                  a.n_out - c0 - c, patch, lane);
+                                  a.n_out - c0 - c, reinterpret_cast<float*>(patch), lane);
             }
             ok = !*abort_flag;
+        }
+        if constexpr (kPair) {
+            if (lane == 0) bulk_wait_all();
+            __syncwarp();
         }
     }
 
@@ -921,6 +955,22 @@ bool code_map(CUtensorMap* map, const void* base, int cols, int rows, int n, int
               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               box_cols == kF8Block ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Y [n_rows][n_out], copies of 128 bytes x 32 rows.
+template <typename T>
+bool out_map(CUtensorMap* map, void* y, int n_out, int n_rows) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n_out), static_cast<cuuint64_t>(n_rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(n_out) * sizeof(T)};
+    const cuuint32_t box[2] = {128 / sizeof(T), 32};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map,
+              sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1009,11 +1059,16 @@ cudaError_t launch_wide(const F8Product& p, const F8Args& a, cudaStream_t s) {
                   kGrad ? S::kBox : kF8Block) ||
         !code_map(&xmap, p.x, kGrad ? p.rows : p.cols, p.n_rows, 0, kM))
         return cudaErrorNotSupported;
+    CUtensorMap ymap = xmap;
+    if (kPair && (reinterpret_cast<uintptr_t>(p.y) | static_cast<size_t>(a.n_out) * sizeof(T)) % 16 ==
+                     0 &&
+        !out_map<T>(&ymap, p.y, a.n_out, p.n_rows))
+        return cudaErrorNotSupported;
     constexpr unsigned kCtas = kPair ? 2 : 1;
     const long tiles = static_cast<long>(a.n_rt) * a.n_tt, most = sm_count() / kCtas;
     const unsigned grid =
         kCtas * static_cast<unsigned>(p.offsets != nullptr || tiles > most ? most : tiles);
-    return launch_after(kernel, dim3(grid), kWThreads, S::kSmem + extra, s, kCtas, wmap, xmap, a,
+    return launch_after(kernel, dim3(grid), kWThreads, S::kSmem + extra, s, kCtas, wmap, xmap, ymap, a,
                         static_cast<T*>(p.y));
 }
 

@@ -16,10 +16,10 @@
 // shared memory (in both operands: zero times whatever lies there may be NaN).  That last stage
 // lands on a barrier of its own CTA, a warp of which writes the zeros before it reports the stage.
 //
-// What bounds it: 4096 tokens top-4 of 16 experts 2880x2880 bf16 into f32, 243 us, 1.1 PFLOP/s: 182
+// What bounds it: 4096 tokens top-4 of 16 experts 2880x2880 bf16 into f32, 235 us, 1.16 PFLOP/s: 182
 // without the stores, in which a stage takes about 700 cycles (the MMAs 512), as either CTA's 32 KB
 // come from L2 at some 50 bytes a cycle; the stores are as much again as a fifth of those copies.
-// One matrix 2048x2048, 8192 rows: 46 us, 1.5 PFLOP/s.
+// One matrix 2048x2048, 8192 rows: 47 us, 1.45 PFLOP/s.
 //
 // Warps: copies, MMAs (even ranks), those zeros, eight for the sums.  Persistent: pair c takes tiles
 // c, c + pairs, ...  With few tiles and long sums (kSplit) a cluster of two or four pairs shares a
@@ -51,7 +51,7 @@ constexpr uint32_t kBoxBytes = kBox * kK * 2;
 constexpr uint32_t kABytes = 2 * kBoxBytes, kStageBytes = 2 * kABytes;   // of dY; and of X
 constexpr int kStages = 5, kChunk = 4;        // ring; stages an accumulator takes
 constexpr int kMaxSplit = 4;                  // pairs that share a tile
-constexpr int kPatch = 32 * 128;               // bytes a warp turns round
+constexpr int kPatch = 32 * 128;               // bytes a warp stores at a time
 constexpr int kThreads = 384, kEpiWarp = 4, kEpiWarps = 8, kCols = 128;
 constexpr int kMaxExperts = 1024;
 constexpr long long kWait = 1ll << 32, kDrain = 1ll << 24;   // SM cycles: about 2 s and 8 ms
@@ -63,7 +63,6 @@ struct WArgs {
     int n_experts, rows, cols, n_rows;
     int n_rt, n_ct;           // tiles down and across a matrix
     uint32_t idesc;
-    int wide;                 // rows of dW are 32-byte aligned
 };
 
 __device__ __forceinline__ void pair_umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -78,7 +77,7 @@ __device__ __forceinline__ void pair_umma_f16(uint32_t d, uint64_t a, uint64_t b
 template <typename T, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_grad_w(const __grid_constant__ CUtensorMap dymap, const __grid_constant__ CUtensorMap xmap,
-             const WArgs a, T* __restrict__ dw) {
+             const __grid_constant__ CUtensorMap dwmap, const WArgs a, T* __restrict__ dw) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -112,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 32 * 2) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&dymap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&xmap) : "memory");
+        if (!kSplit) asm volatile("prefetch.tensormap [%0];" ::"l"(&dwmap) : "memory");
     }
     tc_fence_before();
     cluster.sync();   // both CTAs' barriers and tensor memory are there
@@ -328,18 +328,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[2 * c].x, sum[2 * c].y, sum[2 * c + 1].x, sum[2 * c + 1].y);
                 continue;   // (its one tile)
             }
+            // 128 bytes of the 32 rows at a time, by copies from shared memory (which cut off at
+            // the matrix's edges): the warp goes on while they run (16 experts as above 235 us, by
+            // stores of whole lines 243, of 32 bytes of 32 rows 274; top-4 of 64 experts, 2048 tokens,
+            // into bf16 249, 280 and 314)
             const int r = t.r0 + rank * kM + quarter * 32, c0 = t.c0 + half * kCols;
-            T* dst = dw + (static_cast<size_t>(t.e) * a.rows + r) * a.cols + c0;
-            constexpr int kE = 128 / sizeof(T);
-            // (4096 tokens top-4 of 16 experts 2880x2880: 243 us, with 64 bytes of 16 rows a store
-            // 252, with 32 bytes of 32 rows 274)
+            constexpr int kE = 128 / sizeof(T), kUnit = 16 / sizeof(T);
 #pragma unroll
-            for (int c = 0; c < kCols; c += kE)
-                if (c0 + c < a.cols && r < a.rows)
-                    store_turned<T, 128>(dst + c, static_cast<size_t>(a.cols), a.rows - r, &sum[c / 2],
-                                 a.cols - c0 - c, patch, lane, a.wide != 0);
+            for (int c = 0; c < kCols; c += kE) {
+                uint8_t* to = patch;
+                if (lane == 0) bulk_wait_read<0>();   // the last copy has read it
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float f[kUnit];
+#pragma unroll
+                    for (int i = 0; i < kUnit; ++i) {
+                        const float2 v = sum[(c + q * kUnit + i) / 2];
+                        f[i] = i % 2 ? v.y : v.x;
+                    }
+                    Pack<T, kUnit> p;
+                    p.set(f);
+                    *reinterpret_cast<uint4*>(to + lane * 128 + (q ^ (lane & 7)) * 16) = p.raw;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (c0 + c < a.cols && r < a.rows)
+                        tma3d_store(&dwmap, c0 + c, r, t.e, smem_u32(to));
+                    bulk_commit();
+                }
+            }
             ok = !*abort_flag;
         }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
 
     __syncthreads();
@@ -401,6 +424,24 @@ bool row_map(CUtensorMap* map, const void* base, int width, int n_rows, int type
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// dW, copies of 128 bytes x 32 rows.
+template <typename T>
+bool out_map(CUtensorMap* map, void* dw, const WArgs& a) {
+    auto fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(a.cols) * sizeof(T);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.cols), static_cast<cuuint64_t>(a.rows),
+                                static_cast<cuuint64_t>(a.n_experts)};
+    const cuuint64_t strides[2] = {row, row * a.rows};
+    const cuuint32_t box[3] = {128 / sizeof(T), 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map,
+              sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              dw, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr size_t kSmem = kStages * kStageBytes + kEpiWarps * kPatch + 1024;
 
 template <typename T, bool kSplit>
@@ -440,16 +481,17 @@ int clusters_at_once(int split) {
 }
 
 template <typename T, bool kSplit>
-cudaError_t launch_t(const CUtensorMap& dymap, const CUtensorMap& xmap, WArgs a, int split,
+cudaError_t launch_t(const CUtensorMap& dymap, const CUtensorMap& xmap, const WArgs& a, int split,
                      void* dw, cudaStream_t s) {
     const cudaError_t attr_err = allow_smem<T, kSplit>();
     if (attr_err != cudaSuccess) return attr_err;
-    a.wide = (reinterpret_cast<uintptr_t>(dw) | static_cast<uintptr_t>(a.cols) * sizeof(T)) % 32 == 0;
+    CUtensorMap dwmap;
+    if (!out_map<T>(&dwmap, dw, a)) return cudaErrorNotSupported;
     const int tiles = a.n_rt * a.n_ct * a.n_experts;
     const unsigned ctas = 2u * static_cast<unsigned>(split);
     return launch_after(k_grad_w<T, kSplit>,
                         dim3(ctas * static_cast<unsigned>(std::min(tiles, sm_count() / 2))),
-                        kThreads, kSmem, s, ctas, dymap, xmap, a, static_cast<T*>(dw));
+                        kThreads, kSmem, s, ctas, dymap, xmap, dwmap, a, static_cast<T*>(dw));
 }
 
 }  // namespace
