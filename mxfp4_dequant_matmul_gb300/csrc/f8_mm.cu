@@ -314,9 +314,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 32 ? 2 : 1)
             const uint32_t id =
                 idesc_f8<kGrad>(__shfl_sync(0xFFFFFFFFu, (t.t1 - t.t0 + 15) & ~15, 0));
             for (int s0 = s_lo; s0 < s_hi; s0 += S::kU) {
-                // (both polls at once, by lane)
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(lane == 0 ? &full[st] : &acc_empty[ab],
-                                                           lane == 0 ? phase : acc_phase, kWait));
+                ok = warp_wait_both(&full[st], phase, &acc_empty[ab], acc_phase, kWait);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -401,10 +399,7 @@ __global__ void __launch_bounds__(kThreads, NC <= 32 ? 2 : 1)
 #pragma unroll
             for (int i = 0; i < S::kHalf / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
             for (int s0 = s_lo; s0 < s_hi; s0 += S::kU) {
-                // (both polls at once, by lane)
-                ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait_for(lane == 0 ? &acc_full[ab] : &fac_full[f],
-                                              lane == 0 ? acc_phase : fac_phase, kWait));
+                ok = warp_wait_both(&acc_full[ab], acc_phase, &fac_full[f], fac_phase, kWait);
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t v[S::kU][S::kHalf];
@@ -776,10 +771,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tile_step) {
             for (int s = 0; s < a.n_k; ++s) {
-                // (both polls at once, by lane)
-                ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait_for(lane == 0 ? &full[st] : &acc_empty[2 * ab + h],
-                                              lane == 0 ? phase : acc_phase, kWait));
+                ok = warp_wait_both(&full[st], phase, &acc_empty[2 * ab + h], acc_phase, kWait);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -829,11 +821,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
             for (int i = 0; i < kWCols / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
             for (int s = 0; s < a.n_k; ++s) {
-                // (both polls at once, by lane)
-                ok = __all_sync(0xFFFFFFFFu,
-                                mbar_wait_for(lane == 0 ? &acc_full[2 * ab + group]
-                                                        : &fac_full[slot],
-                                              lane == 0 ? acc_phase : fac_phase, kWait));
+                ok = warp_wait_both(&acc_full[2 * ab + group], acc_phase, &fac_full[slot], fac_phase,
+                                    kWait);
                 if (!ok) break;
                 tc_fence_after();
                 const float f = fac[slot][quarter * 32 + lane] * fac[slot][kM + group];

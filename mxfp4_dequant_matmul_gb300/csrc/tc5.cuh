@@ -118,6 +118,18 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, lo
     return false;
 }
 
+// Two barriers at once, so that their polls overlap: lane 0 asks one, the other lanes the other.  A
+// lane has acquired only the barrier that it asked, and the vote orders no memory between lanes;
+// __syncwarp does, so after this any lane may read what either barrier guards (the whole warp calls).
+__device__ __forceinline__ bool warp_wait_both(uint64_t* a, uint32_t parity_a, uint64_t* b,
+                                               uint32_t parity_b, long long cycles) {
+    const bool first = (threadIdx.x & 31) == 0;
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_for(first ? a : b,
+                                                          first ? parity_a : parity_b, cycles));
+    __syncwarp();
+    return ok;
+}
+
 // An operand that lies with its M or N side contiguous (rows of 128 bytes along that side, one
 // for each k, 128-byte swizzle): 8-k groups 1024 bytes apart, the next 128 bytes of the side
 // `next` bytes on.
