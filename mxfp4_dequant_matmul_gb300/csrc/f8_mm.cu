@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ uint64_t full[S::kStages], empty[S::kStages], acc_full[4], acc_empty[4];
-    __shared__ uint64_t fac_full[kWFac], fac_empty[kWFac], drain;
+    __shared__ uint64_t fac_full[kWFac], fac_empty[kWFac], drain[2];
     __shared__ float fac[kWFac][kM + 4];   // a block's scales: X's, then W's two
     __shared__ uint32_t tmem_base;
     __shared__ int abort_word, n_tiles_sh;
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             mbar_init(&fac_full[i], 32);
             mbar_init(&fac_empty[i], kWEpiWarps);
         }
-        mbar_init(&drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);   // one for each warp that multiplies
         abort_word = 0;
         n_tiles_sh = a.n_rt * a.n_tt;
         fence_mbar_init();
@@ -795,8 +795,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         if (!ok) {
             fail();
-            if (leader) wide_commit<kPair>(&drain);
-            mbar_wait_for(&drain, 0u, kWait);
+            if (leader) wide_commit<kPair>(&drain[h]);
+            mbar_wait_for(&drain[h], 0u, kWait);
         }
         __syncwarp();
     } else if (warp >= kWEpiWarp) {
