@@ -376,6 +376,7 @@ def q4k_mm(w, rows, cols, X, nb, Y, stream=None):
 # other ones as something else, or past their end.
 
 _TYPE_OF = {}
+_CODE_OF = {}                  # (type given or None, dtype) -> type, where the two agree
 _INT32 = _FLOAT32 = None       # torch's, from the first call on
 _NOT_PLAIN = (AttributeError, KeyError, TypeError, ctypes.ArgumentError)   # before the call
 
@@ -385,6 +386,8 @@ def _dtypes():
     import torch
     _TYPE_OF.update({torch.float32: TYPE_F32, torch.bfloat16: TYPE_BF16,
                      torch.float16: TYPE_F16})
+    _CODE_OF.update({(given, dtype): code for dtype, code in _TYPE_OF.items()
+                     for given in (None, code)})
     _INT32, _FLOAT32 = torch.int32, torch.float32
 
 
@@ -598,10 +601,10 @@ def mxfp4_moe_combine_grad(dy, o, n_tokens, top_k, width, pos_of, route_w, d_o, 
 
 # --- 8-bit codes with a scale for each block of 128 (include/f8.h) -----------------
 #
-# Codes are torch.float8_e4m3fn (or uint8) tensors.  A tensor of another dtype, on another device
-# than the current one, too small, or with strides where the library takes contiguous rows (a
-# transposed table of scales) is refused (status 1): the kernels would read it as something else
-# or past its end.  Addresses pass, as everywhere.
+# Codes are torch.float8_e4m3fn (or uint8) tensors.  A tensor of another dtype (or of another than
+# an explicit type says), on another device than the current one, too small, or with strides where
+# the library takes contiguous rows (a transposed table of scales) is refused (status 1): the
+# kernels would read or write it as something else or past its end.  Addresses pass, as everywhere.
 
 _F8 = None       # torch's dtypes of codes, from the first call on
 _current_device = None
@@ -636,6 +639,15 @@ def _need(fn, *wanted):
             raise Mxfp4Error(fn, 1)
 
 
+def _own_type(given, *tensors):
+    """_type, and refused where a tensor is not of the type given."""
+    if given is not None:
+        for t in tensors:
+            if t is not None and t.__class__ is not int and _TYPE_OF.get(t.dtype) != given:
+                return -1
+    return _type(given, *tensors)
+
+
 def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None, type=None,
                    stream=None):
     """x (x_rows rows, ld elements apart) or its rows row_of -> codes [rows, cols] and scales
@@ -655,7 +667,7 @@ def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None
                                         not row_of.is_contiguous())):
             raise TypeError
         status = _lib.mxfp4_f8_quant(
-            x.data_ptr(), _TYPE_OF[dtype] if type is None else type, x_rows, cols, ld,
+            x.data_ptr(), _CODE_OF[type, dtype], x_rows, cols, ld,
             None if row_of is None else row_of.data_ptr(), rows, codes.data_ptr(),
             scales.data_ptr(), None if values is None else values.data_ptr(),
             _current_stream() if stream is None else _stream(stream))
@@ -664,11 +676,12 @@ def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None
             _f8_types()
         _need("mxfp4_f8_quant", (codes, _F8, n), (scales, (_FLOAT32,), _blocks(cols) * rows),
               (row_of, (_INT32,), rows), (values, _TYPE_OF, n))
-        if x.__class__ is not int and x is not None and x.get_device() != _current_device():
+        if x.__class__ is not int and x is not None and (x.dtype not in _TYPE_OF or
+                                                         x.get_device() != _current_device()):
             raise Mxfp4Error("mxfp4_f8_quant", 1)
         status = lib().mxfp4_f8_quant(
-            _addr(x), _type(type, x, values), x_rows, cols, ld, _addr(row_of), rows, _addr(codes),
-            _addr(scales), _addr(values), _stream(stream))
+            _addr(x), _own_type(type, x, values), x_rows, cols, ld, _addr(row_of), rows,
+            _addr(codes), _addr(scales), _addr(values), _stream(stream))
     if status:
         _check("mxfp4_f8_quant", status)
 
@@ -682,8 +695,8 @@ def mxfp4_f8_quant_weight(w, n_matrices, rows, cols, codes, scales, values=None,
     n = n_matrices * rows * cols
     _need("mxfp4_f8_quant_weight", (w, _TYPE_OF, n), (codes, _F8, n), (values, _TYPE_OF, n),
           (scales, (_FLOAT32,), n_matrices * _blocks(rows) * _blocks(cols)))
-    status = lib().mxfp4_f8_quant_weight(_addr(w), _type(type, w, values), n_matrices, rows, cols,
-                                         _addr(codes), _addr(scales), _addr(values),
+    status = lib().mxfp4_f8_quant_weight(_addr(w), _own_type(type, w, values), n_matrices, rows,
+                                         cols, _addr(codes), _addr(scales), _addr(values),
                                          _stream(stream))
     if status:
         _check("mxfp4_f8_quant_weight", status)
@@ -704,7 +717,7 @@ def _f8_product(fn, bank, bank_scales, n_experts, rows, cols, xq, x_scales, n_ro
                 not (bank.is_contiguous() and xq.is_contiguous() and bank_scales.is_contiguous() and
                      x_scales.is_contiguous() and Y.is_contiguous())):
             raise TypeError
-        code = _TYPE_OF[Y.dtype] if y_type is None else y_type
+        code = _CODE_OF[y_type, Y.dtype]
         on = _current_stream() if stream is None else _stream(stream)
         if n_experts is None:
             status = getattr(_lib, fn)(
@@ -724,7 +737,7 @@ def _f8_product(fn, bank, bank_scales, n_experts, rows, cols, xq, x_scales, n_ro
               (bank_scales, (_FLOAT32,), n * _blocks(rows) * _blocks(cols)),
               (xq, _F8, n_rows * k), (x_scales, (_FLOAT32,), _blocks(k) * n_rows),
               (Y, _TYPE_OF, n_rows * n_out), (offsets, (_INT32,), n + 1))
-        y_type = _type(y_type, Y)
+        y_type = _own_type(y_type, Y)
         call = getattr(lib(), fn)
         if n_experts is None:
             status = call(_addr(bank), _addr(bank_scales), rows, cols, _addr(xq), _addr(x_scales),
@@ -769,8 +782,8 @@ def mxfp4_mm_grad_w(dy, x, rows, cols, n_rows, dW, type=None, dw_type=None, stre
         _f8_types()
     _need("mxfp4_mm_grad_w", (dy, _TYPE_OF, n_rows * rows), (x, _TYPE_OF, n_rows * cols),
           (dW, _TYPE_OF, rows * cols))
-    status = lib().mxfp4_mm_grad_w(_addr(dy), _addr(x), _type(type, dy, x), rows, cols, n_rows,
-                                   _addr(dW), _type(dw_type, dW), _stream(stream))
+    status = lib().mxfp4_mm_grad_w(_addr(dy), _addr(x), _own_type(type, dy, x), rows, cols, n_rows,
+                                   _addr(dW), _own_type(dw_type, dW), _stream(stream))
     if status:
         _check("mxfp4_mm_grad_w", status)
 
@@ -782,8 +795,8 @@ def mxfp4_moe_mm_grad_w(dy, x, n_experts, rows, cols, n_rows, offsets, dW, type=
         _f8_types()
     _need("mxfp4_moe_mm_grad_w", (dy, _TYPE_OF, n_rows * rows), (x, _TYPE_OF, n_rows * cols),
           (offsets, (_INT32,), n_experts + 1), (dW, _TYPE_OF, n_experts * rows * cols))
-    status = lib().mxfp4_moe_mm_grad_w(_addr(dy), _addr(x), _type(type, dy, x), n_experts, rows,
+    status = lib().mxfp4_moe_mm_grad_w(_addr(dy), _addr(x), _own_type(type, dy, x), n_experts, rows,
                                        cols, n_rows, _addr(offsets), _addr(dW),
-                                       _type(dw_type, dW), _stream(stream))
+                                       _own_type(dw_type, dW), _stream(stream))
     if status:
         _check("mxfp4_moe_mm_grad_w", status)

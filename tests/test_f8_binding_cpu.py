@@ -1,0 +1,140 @@
+"""The binding of include/f8.h without a GPU, on host tensors that pass for the current device's and a
+library that records its calls: what the kernels would read or write past a tensor's end, or as
+something else, is refused (status 1) before the library is asked, or by it (type -1)."""
+import pytest
+
+torch = pytest.importorskip("torch")
+F32, BF16, F16 = 0, 1, 2
+TYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+ROWS, COLS, NB, N = 32, 48, 4, 2
+
+
+class Recorder:
+    """Each entry point: notes its arguments; refuses a type that is none, as the library does."""
+
+    def __init__(self, mx):
+        self.mx, self.calls = mx, []
+
+    def __getattr__(self, name):
+        if name == "mxfp4_status_string":
+            return lambda status: b"refused"
+        types = [i for i, (got, arg) in enumerate(zip(self.mx._SIG[name][1], ARGS[name])) if arg in ("type", "y_type", "dw_type")]
+
+        def call(*args):
+            if any(args[i] not in (F32, BF16, F16) for i in types):
+                return 1
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+ARGS = {"mxfp4_f8_quant": ("x", "type", "x_rows", "cols", "ld", "row_of", "rows", "codes", "scales", "values", "s"),
+        "mxfp4_f8_quant_weight": ("w", "type", "n", "rows", "cols", "codes", "scales", "values", "s"),
+        "mxfp4_mm_grad_w": ("dy", "x", "type", "rows", "cols", "n_rows", "dw", "dw_type", "s"),
+        "mxfp4_moe_mm_grad_w": ("dy", "x", "type", "n", "rows", "cols", "n_rows", "off", "dw", "dw_type", "s")}
+for _f in ("mxfp4_f8_mm", "mxfp4_f8_mm_grad"):
+    ARGS[_f] = ("w", "ws", "rows", "cols", "x", "xs", "nb", "y", "y_type", "s")
+for _f in ("mxfp4_f8_moe_mm", "mxfp4_f8_moe_mm_grad"):
+    ARGS[_f] = ("w", "ws", "n", "rows", "cols", "x", "xs", "nb", "off", "y", "y_type", "s")
+
+
+@pytest.fixture
+def mx(monkeypatch):
+    import mxfp4_dequant_matmul_gb300 as m
+    m._f8_types()
+    rec = Recorder(m)
+    monkeypatch.setattr(m, "_lib", rec)
+    monkeypatch.setattr(m, "_current_device", lambda: -1)   # a host tensor's get_device()
+    monkeypatch.setattr(m, "_current_stream", lambda: 0)
+    m.rec = rec
+    return m
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def f32(*shape):
+    return torch.zeros(shape)
+
+
+OFF = torch.zeros(N + 1, dtype=torch.int32)
+PRODUCTS = {"mxfp4_f8_mm": lambda mx, y, t: mx.mxfp4_f8_mm(u8(ROWS, COLS), f32(1, 1), ROWS, COLS, u8(NB, COLS), f32(1, NB), NB, y(NB, ROWS), y_type=t),
+            "mxfp4_f8_mm_grad": lambda mx, y, t: mx.mxfp4_f8_mm_grad(u8(ROWS, COLS), f32(1, 1), ROWS, COLS, u8(NB, ROWS), f32(1, NB), NB,
+                                                                     y(NB, COLS), dx_type=t),
+            "mxfp4_f8_moe_mm": lambda mx, y, t: mx.mxfp4_f8_moe_mm(u8(N, ROWS, COLS), f32(N, 1, 1), N, ROWS, COLS, u8(NB, COLS), f32(1, NB), NB, OFF,
+                                                                   y(NB, ROWS), y_type=t),
+            "mxfp4_f8_moe_mm_grad": lambda mx, y, t: mx.mxfp4_f8_moe_mm_grad(u8(N, ROWS, COLS), f32(N, 1, 1), N, ROWS, COLS, u8(NB, ROWS), f32(1, NB),
+                                                                             NB, OFF, y(NB, COLS), dx_type=t),
+            "mxfp4_mm_grad_w": lambda mx, y, t: mx.mxfp4_mm_grad_w(f32(NB, ROWS).bfloat16(), f32(NB, COLS).bfloat16(), ROWS, COLS, NB, y(ROWS, COLS),
+                                                                   dw_type=t),
+            "mxfp4_moe_mm_grad_w": lambda mx, y, t: mx.mxfp4_moe_mm_grad_w(f32(NB, ROWS).bfloat16(), f32(NB, COLS).bfloat16(), N, ROWS, COLS, NB, OFF,
+                                                                           y(N, ROWS, COLS), dw_type=t)}
+
+
+def refused(mx, call, *args):
+    with pytest.raises(mx.Mxfp4Error) as e:
+        call(*args)
+    assert e.value.status == 1 and not mx.rec.calls
+
+
+@pytest.mark.parametrize("fn", list(PRODUCTS))
+@pytest.mark.parametrize("dtype", list(TYPE))
+@pytest.mark.parametrize("given", [None, F32, BF16, F16])
+def test_the_results_type_is_the_tensors(mx, fn, dtype, given):
+    """A type that is not the result's would be written past its end, or as other values."""
+    def y(*shape):
+        return torch.zeros(shape, dtype=dtype)
+    if given is None or given == TYPE[dtype]:
+        PRODUCTS[fn](mx, y, given)
+        (name, args), = mx.rec.calls
+        assert name == fn and args[len(ARGS[fn]) - 2] == TYPE[dtype]
+    else:
+        refused(mx, PRODUCTS[fn], mx, y, given)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("dy,x,given", [(torch.bfloat16, torch.bfloat16, F16), (torch.float16, torch.float16, BF16), (torch.bfloat16, torch.float16, BF16),
+                                        (torch.bfloat16, torch.float16, F16), (torch.float32, torch.float32, BF16)])
+def test_the_operands_type_is_the_tensors(mx, grouped, dy, x, given):
+    a, b = torch.zeros(NB, ROWS, dtype=dy), torch.zeros(NB, COLS, dtype=x)
+    if grouped:
+        refused(mx, lambda: mx.mxfp4_moe_mm_grad_w(a, b, N, ROWS, COLS, NB, OFF, f32(N, ROWS, COLS), type=given))
+    else:
+        refused(mx, lambda: mx.mxfp4_mm_grad_w(a, b, ROWS, COLS, NB, f32(ROWS, COLS), type=given))
+
+
+@pytest.mark.parametrize("dtype", list(TYPE))
+@pytest.mark.parametrize("given", [None, F32, BF16, F16])
+@pytest.mark.parametrize("weight", [False, True])
+def test_what_is_quantised_has_the_given_type(mx, weight, dtype, given):
+    x, codes, values = torch.zeros(NB, COLS, dtype=dtype), u8(NB, COLS), torch.zeros(NB, COLS, dtype=dtype)
+
+    def call(x, values):
+        if weight:
+            mx.mxfp4_f8_quant_weight(x, 1, NB, COLS, codes, f32(1, 1, 1), values, type=given)
+        else:
+            mx.mxfp4_f8_quant(x, NB, COLS, COLS, None, NB, codes, f32(1, NB), values, type=given)
+    if given is None or given == TYPE[dtype]:
+        call(x, values)
+        call(x, None)
+        assert [c[1][1] for c in mx.rec.calls] == [TYPE[dtype]] * 2
+        mx.rec.calls.clear()
+    else:
+        refused(mx, call, x, values)
+        refused(mx, call, x, None)
+        refused(mx, call, 1 << 20, values)      # an address with values of another type
+    other = torch.zeros(NB, COLS, dtype=torch.float16 if dtype is not torch.float16 else torch.bfloat16)
+    refused(mx, call, x, other)
+
+
+def test_addresses_take_the_given_type(mx):
+    a = 1 << 20
+    mx.mxfp4_f8_mm(a, a, ROWS, COLS, a, a, NB, a, y_type=BF16)
+    mx.mxfp4_f8_quant(a, NB, COLS, COLS, None, NB, a, a, a, type=F16)
+    mx.mxfp4_mm_grad_w(a, a, ROWS, COLS, NB, a, type=BF16, dw_type=F32)
+    assert len(mx.rec.calls) == 3
+    refused_before = len(mx.rec.calls)
+    with pytest.raises(mx.Mxfp4Error):
+        mx.mxfp4_f8_mm(a, a, ROWS, COLS, a, a, NB, a)          # no type at all
+    assert len(mx.rec.calls) == refused_before
