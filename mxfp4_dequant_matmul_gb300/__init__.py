@@ -648,6 +648,25 @@ def _own_type(given, *tensors):
     return _type(given, *tensors)
 
 
+def _outside(x, x_rows, cols, ld):
+    """Whether x_rows rows of cols elements, ld apart, are not all in x: a contiguous tensor is flat
+    memory; of another one they are its rows (or every so many of them), along its last side."""
+    if x.is_contiguous():
+        return x.numel() < (x_rows - 1) * ld + cols
+    shape, step = x.shape, x.stride()
+    if cols > shape[-1] or step[-1] != 1:
+        return True
+    n, pitch = 1, 0                # its rows, and how far apart they are
+    for size, stride in zip(shape[-2::-1], step[-2::-1]):
+        if size != 1:
+            if n != 1 and stride != n * pitch:
+                return True        # not equally far
+            if n == 1:
+                pitch = stride
+            n *= size
+    return x_rows > 1 and (pitch == 0 or ld % pitch != 0 or (x_rows - 1) * (ld // pitch) >= n)
+
+
 def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None, type=None,
                    stream=None):
     """x (x_rows rows, ld elements apart) or its rows row_of -> codes [rows, cols] and scales
@@ -658,6 +677,7 @@ def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None
         if (codes.dtype not in _F8 or scales.dtype is not _FLOAT32 or codes.numel() < n or
                 scales.numel() < (cols + 127) // 128 * rows or not codes.is_contiguous() or
                 not scales.is_contiguous() or x.get_device() != here or
+                _outside(x, x_rows, cols, ld) or
                 codes.get_device() != here or scales.get_device() != here or
                 values is not None and (values.dtype is not dtype or values.numel() < n or
                                         values.get_device() != here or
@@ -676,8 +696,9 @@ def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None
             _f8_types()
         _need("mxfp4_f8_quant", (codes, _F8, n), (scales, (_FLOAT32,), _blocks(cols) * rows),
               (row_of, (_INT32,), rows), (values, _TYPE_OF, n))
-        if x.__class__ is not int and x is not None and (x.dtype not in _TYPE_OF or
-                                                         x.get_device() != _current_device()):
+        if x.__class__ is not int and x is not None and (
+                x.dtype not in _TYPE_OF or x.get_device() != _current_device() or
+                _outside(x, x_rows, cols, ld)):
             raise Mxfp4Error("mxfp4_f8_quant", 1)
         status = lib().mxfp4_f8_quant(
             _addr(x), _own_type(type, x, values), x_rows, cols, ld, _addr(row_of), rows,

@@ -138,3 +138,52 @@ def test_addresses_take_the_given_type(mx):
     with pytest.raises(mx.Mxfp4Error):
         mx.mxfp4_f8_mm(a, a, ROWS, COLS, a, a, NB, a)          # no type at all
     assert len(mx.rec.calls) == refused_before
+
+
+# --- the extent and the rows of what is quantised -------------------------------------------
+
+
+def quantise(mx, x, x_rows, cols, ld, row_of=None, rows=None):
+    rows = x_rows if rows is None else rows
+    mx.mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, u8(rows, cols), f32((cols + 127) // 128, rows))
+
+
+FLAT = torch.zeros(1000, dtype=torch.bfloat16)
+PICK = torch.zeros(9, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("x,x_rows,cols,ld", [
+    (FLAT[:4 * 48].view(4, 48), 4, 48, 48), (FLAT[:4 * 48].view(4, 48), 3, 48, 48), (FLAT[:192], 4, 48, 48), (FLAT[:48], 1, 48, 1000),
+    (FLAT[:960].view(10, 96)[:, 16:64], 10, 48, 96), (FLAT[:960].view(10, 96)[:, :48], 7, 48, 96), (FLAT[:960].view(10, 96)[3:, 48:], 7, 48, 96),
+    (FLAT[:960].view(10, 96), 20, 48, 48), (FLAT[:960].view(10, 96), 5, 96, 192), (FLAT[:960].view(2, 5, 96)[:, :, 32:80], 10, 48, 96),
+    (FLAT[3:3 + 9 * 97 + 48], 10, 48, 97), (torch.as_strided(FLAT, (10, 48), (97, 1), 3), 10, 48, 97), (FLAT[:960].view(20, 48)[::2], 10, 48, 96),
+    (FLAT[:960].view(20, 48)[4:5, 16:32], 1, 16, 16), (FLAT[:960].view(20, 1, 48), 20, 48, 48), (FLAT[:960].view(10, 96)[:, None, :48], 10, 48, 96),
+    (FLAT[:960].view(10, 96)[:, :48], 5, 48, 192), (FLAT[:960].view(10, 96)[1:2, :48], 1, 48, 48), (FLAT[:960].view(2, 5, 96)[:1, :, :48], 5, 32, 96)])
+def test_rows_within_the_tensor_pass(mx, x, x_rows, cols, ld):
+    quantise(mx, x, x_rows, cols, ld)
+    (_, args), = mx.rec.calls
+    assert args[0] == x.data_ptr() and args[2:5] == (x_rows, cols, ld)
+    quantise(mx, x, x_rows, cols, ld, PICK, 9)
+    assert len(mx.rec.calls) == 2
+
+
+@pytest.mark.parametrize("x,x_rows,cols,ld", [
+    (FLAT[:192].view(4, 48), 5, 48, 48), (FLAT[:192].view(4, 48), 4, 48, 49), (FLAT[:192].view(4, 48), 4, 64, 64), (FLAT[:191], 4, 48, 48),
+    (FLAT[:47], 1, 48, 48), (FLAT[:960].view(10, 96)[:, :48], 11, 48, 96), (FLAT[:960].view(10, 96)[:, :48], 10, 64, 96),
+    (FLAT[:960].view(10, 96)[:4, :48], 5, 48, 96), (FLAT[:0], 1, 48, 48), (FLAT[:960].view(48, 20).T, 20, 48, 48), (FLAT[:96:2], 1, 48, 48),
+    (FLAT[:48].expand(5, 48), 5, 48, 48), (FLAT[:960].view(2, 10, 48).transpose(0, 1), 20, 48, 48), (FLAT[:960].view(10, 96)[:, :48], 10, 48, 48),
+    (FLAT[:960].view(2, 5, 96)[:, :4, 32:80], 8, 48, 96),
+    (FLAT[:960].view(10, 96)[:, :48], 9, 64, 96), (FLAT[:960].view(10, 96)[:, :48], 6, 48, 192)])
+def test_rows_past_the_tensor_or_elsewhere_are_refused(mx, x, x_rows, cols, ld):
+    """Too few elements, another unit than 1 along a row, rows that are not ld apart."""
+    refused(mx, quantise, mx, x, x_rows, cols, ld)
+    refused(mx, lambda: quantise(mx, x, x_rows, cols, ld, PICK, 9))
+
+
+def test_sizes_the_library_refuses_reach_it(mx):
+    """Numbers that are wrong whatever the tensor is are the library's to refuse."""
+    for x_rows, cols, ld in ((0, 48, 48), (4, 48, -48), (4, 0, 48), (4, -48, 48)):
+        quantise_none = (x_rows, cols, ld)
+        mx.rec.calls.clear()
+        mx.mxfp4_f8_quant(FLAT[:192].view(4, 48), x_rows, cols, ld, None, 4, u8(4, 48), f32(1, 4))
+        assert len(mx.rec.calls) == 1, quantise_none
