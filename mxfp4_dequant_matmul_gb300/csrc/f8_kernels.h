@@ -12,7 +12,8 @@ namespace mxk {
 
 constexpr int kF8Block = 128;   // elements that share a scale
 
-inline int f8_blocks(int n) { return (n + kF8Block - 1) / kF8Block; }
+// (n + 127 would overflow for the last sides that an int holds.)
+inline int f8_blocks(int n) { return n / kF8Block + (n % kF8Block != 0); }
 
 // f8_quant.cu
 cudaError_t launch_f8_quant(const void* x, int type, int x_rows, int cols, long long ld,
