@@ -677,7 +677,8 @@ def mxfp4_f8_quant(x, x_rows, cols, ld, row_of, rows, codes, scales, values=None
         if (codes.dtype not in _F8 or scales.dtype is not _FLOAT32 or codes.numel() < n or
                 scales.numel() < (cols + 127) // 128 * rows or not codes.is_contiguous() or
                 not scales.is_contiguous() or x.get_device() != here or
-                _outside(x, x_rows, cols, ld) or
+                (x.numel() < (x_rows - 1) * ld + cols if x.is_contiguous() else
+                 _outside(x, x_rows, cols, ld)) or
                 codes.get_device() != here or scales.get_device() != here or
                 values is not None and (values.dtype is not dtype or values.numel() < n or
                                         values.get_device() != here or
