@@ -158,7 +158,9 @@ PICK = torch.zeros(9, dtype=torch.int32)
     (FLAT[:960].view(10, 96), 20, 48, 48), (FLAT[:960].view(10, 96), 5, 96, 192), (FLAT[:960].view(2, 5, 96)[:, :, 32:80], 10, 48, 96),
     (FLAT[3:3 + 9 * 97 + 48], 10, 48, 97), (torch.as_strided(FLAT, (10, 48), (97, 1), 3), 10, 48, 97), (FLAT[:960].view(20, 48)[::2], 10, 48, 96),
     (FLAT[:960].view(20, 48)[4:5, 16:32], 1, 16, 16), (FLAT[:960].view(20, 1, 48), 20, 48, 48), (FLAT[:960].view(10, 96)[:, None, :48], 10, 48, 96),
-    (FLAT[:960].view(10, 96)[:, :48], 5, 48, 192), (FLAT[:960].view(10, 96)[1:2, :48], 1, 48, 48), (FLAT[:960].view(2, 5, 96)[:1, :, :48], 5, 32, 96)])
+    (FLAT[:960].view(10, 96)[:, :48], 5, 48, 192), (FLAT[:960].view(10, 96)[1:2, :48], 1, 48, 48), (FLAT[:960].view(2, 5, 96)[:1, :, :48], 5, 32, 96),
+    (FLAT[:960].view(2, 5, 3, 4, 8)[:, :, 1], 10, 32, 96), (FLAT[:960].view(10, 2, 3, 16)[:, 1], 10, 48, 96), (FLAT[:960].view(2, 5, 96)[:, :4], 4, 96, 96),
+    (FLAT[:960].view(2, 10, 48)[:, :9], 2, 144, 480), (FLAT[:960].view(2, 10, 48)[:, :9], 3, 144, 144)])
 def test_rows_within_the_tensor_pass(mx, x, x_rows, cols, ld):
     quantise(mx, x, x_rows, cols, ld)
     (_, args), = mx.rec.calls
@@ -173,7 +175,9 @@ def test_rows_within_the_tensor_pass(mx, x, x_rows, cols, ld):
     (FLAT[:960].view(10, 96)[:4, :48], 5, 48, 96), (FLAT[:0], 1, 48, 48), (FLAT[:960].view(48, 20).T, 20, 48, 48), (FLAT[:96:2], 1, 48, 48),
     (FLAT[:48].expand(5, 48), 5, 48, 48), (FLAT[:960].view(2, 10, 48).transpose(0, 1), 20, 48, 48), (FLAT[:960].view(10, 96)[:, :48], 10, 48, 48),
     (FLAT[:960].view(2, 5, 96)[:, :4, 32:80], 8, 48, 96),
-    (FLAT[:960].view(10, 96)[:, :48], 9, 64, 96), (FLAT[:960].view(10, 96)[:, :48], 6, 48, 192)])
+    (FLAT[:960].view(10, 96)[:, :48], 9, 64, 96), (FLAT[:960].view(10, 96)[:, :48], 6, 48, 192),
+    (FLAT[:960].view(2, 5, 3, 4, 8)[:, :, 1], 10, 48, 96), (FLAT[:960].view(2, 5, 3, 4, 8)[:, :, 1], 11, 32, 96),
+    (FLAT[:960].view(2, 5, 3, 4, 8)[..., 1, :], 10, 32, 96), (FLAT[:960].view(2, 5, 96)[:, :4], 5, 96, 96)])
 def test_rows_past_the_tensor_or_elsewhere_are_refused(mx, x, x_rows, cols, ld):
     """Too few elements, another unit than 1 along a row, rows that are not ld apart."""
     refused(mx, quantise, mx, x, x_rows, cols, ld)
@@ -187,3 +191,35 @@ def test_sizes_the_library_refuses_reach_it(mx):
         mx.rec.calls.clear()
         mx.mxfp4_f8_quant(FLAT[:192].view(4, 48), x_rows, cols, ld, None, 4, u8(4, 48), f32(1, 4))
         assert len(mx.rec.calls) == 1, quantise_none
+
+
+def test_what_passes_is_read_within_the_tensor():
+    """Random views and rows: those that pass read elements of the view alone, and of a view with rows
+    at one distance every such choice passes."""
+    import random
+    import mxfp4_dequant_matmul_gb300 as m
+    rng, flat, passed = random.Random(5), torch.arange(720), 0
+    for _ in range(20000):
+        x = flat.view(rng.choice([(720,), (45, 16), (9, 5, 16), (3, 15, 16), (5, 3, 3, 16), (15, 48), (5, 3, 48), (720, 1)]))
+        for d in range(x.dim()):
+            if rng.random() < 0.5:
+                a = rng.randrange(x.shape[d])
+                x = x.narrow(d, a, rng.randint(1, x.shape[d] - a))
+        if rng.random() < 0.2 and x.dim() > 1:
+            x = x.transpose(0, rng.randrange(x.dim()))
+        if rng.random() < 0.1:
+            x = x[::2]
+        if rng.random() < 0.1:
+            x = x.select(rng.randrange(x.dim()), 0) if x.dim() > 1 else x
+        held = set(x.reshape(-1).tolist())
+        cols = rng.choice([1, 8, 16, 32, 48])
+        plain = x.dim() == 2 and x.shape[0] > 1 and x.stride(1) == 1 and x.stride(0) >= cols
+        ld = x.stride(0) * rng.choice([1, 1, 2]) if plain and rng.random() < 0.7 else cols + rng.choice([0, 0, 0, 8, 16, 32, 96])
+        x_rows = rng.randint(1, 12)
+        inside = all(x.storage_offset() + i * ld + c in held for i in range(x_rows) for c in range(cols))
+        out = m._outside(x, x_rows, cols, ld)
+        assert inside or out, (x.shape, x.stride(), x_rows, cols, ld)
+        if plain and inside and cols <= x.shape[1] and ld % x.stride(0) == 0:
+            assert not out, (x.shape, x.stride(), x_rows, cols, ld)
+        passed += not out
+    assert passed > 2000
