@@ -10,7 +10,8 @@
  *
  * Codes are E4M3 bytes (sign, 4 bits of exponent with bias 7, 3 of fraction; largest
  * 448, 0x7F and 0xFF NaN, no infinities), row-major without padding, cols % 16 == 0,
- * 16-byte aligned.  Scales are FP32 multipliers, of any value (a checkpoint's need be
+ * 16-byte aligned.  (What is quantised, its rows and the values are read and written fastest where
+ * they are 32-byte aligned.)  Scales are FP32 multipliers, of any value (a checkpoint's need be
  * no powers of two):
  *   matrix [rows, cols]      one for each 128x128 block: [ceil(rows/128)][ceil(cols/128)],
  *                            the matrices of a bank one after the other
@@ -21,7 +22,8 @@
  *
  * A routed layer with its gradients, in this order:
  *   mxfp4_moe_sort, mxfp4_f8_quant (rows gathered into expert order)
- *   mxfp4_f8_moe_mm ..., mxfp4_moe_combine
+ *   mxfp4_f8_moe_mm (the act between two of them is the caller's, as is its gradient),
+ *   mxfp4_moe_combine
  *   mxfp4_moe_combine_grad, mxfp4_f8_quant of the gradient's rows
  *   mxfp4_f8_moe_mm_grad (by the rows), mxfp4_moe_mm_grad_w (by the matrices)
  *   mxfp4_moe_dispatch_grad
@@ -95,11 +97,11 @@ int mxfp4_f8_moe_mm_grad(const void* bank, const float* bank_scales, int n_exper
 /* Gradient of a product by its matrices: dW_e[r*cols + c] = sum over offsets[e] <= i <
  * offsets[e+1] of dY[i][r] * X[i][c], dY [n_rows, rows] and X [n_rows, cols] both of
  * `type` (BF16 or F16), dW [n_experts][rows][cols] of dw_type (F32 or BF16; the FP32 sum
- * rounded once).  In 16 bits, since the scales of 8-bit codes change along this sum.  An
- * expert without rows gets zeros; rows of dY and X that belong to no expert are not used,
- * whatever they hold.  rows % 8 == 0 and cols % 8 == 0.  Products of two elements are exact;
- * error bound (ceil(m/16) + 8) * 2^-23 * sum_i |dY X| for an expert of m rows, before the
- * rounding to BF16.  mxfp4_mm_grad_w: one matrix, all n_rows rows. */
+ * rounded once; written, never added to).  In 16 bits, since the scales of 8-bit codes change
+ * along this sum.  An expert without rows gets zeros; rows of dY and X that belong to no expert
+ * are not used, whatever they hold.  rows % 8 == 0 and cols % 8 == 0.  Products of two elements
+ * are exact; error bound (ceil(m/16) + 8) * 2^-23 * sum_i |dY X| for an expert of m rows, before
+ * the rounding to BF16.  mxfp4_mm_grad_w: one matrix, all n_rows rows. */
 int mxfp4_mm_grad_w(const void* dy, const void* x, int type, int rows, int cols, int n_rows,
                     void* dW, int dw_type, cudaStream_t stream);
 int mxfp4_moe_mm_grad_w(const void* dy, const void* x, int type, int n_experts, int rows, int cols,

@@ -13,12 +13,12 @@
 // rows), MMAs, scales (asynchronous copies of 4 bytes, several blocks ahead: fetched when they
 // are needed, their latency bounded a block), and eight warps for the sums.
 //
-// What bounds them: few tokens, HBM (64 experts 2880x2880, 32 tokens, top-4: 66 us, 6.6 TB/s; one
-// token 14336x4096 12.7 us, of which the stream of the weights is 8.8); many tokens, about 900 to
+// What bounds them: few tokens, HBM (64 experts 2880x2880, 32 tokens, top-4: 65 to 71 us, 6.6 TB/s;
+// one token 14336x4096 12.8 us, of which the stream of the weights is 8.8); many tokens, about 900 to
 // 1000 cycles a block of 128 x 256 sums, of which the MMAs are 512: by single CTAs copies and MMAs
 // take 935, as 48 KB of operands go through shared memory, by pairs the accumulators' way
-// round (2048 tokens 4096x14336 107 us, 2.2 PFLOP/s; 4096 tokens 4096x4096 by the rows 65 us, 2.1;
-// 2048 tokens, top-4 of 64 experts 2880x2880, 123 us).
+// round (2048 tokens 4096x14336 109 to 114 us, 2.1 to 2.2 PFLOP/s; 4096 tokens 4096x4096 by the rows
+// 65 to 68 us, 2.1; 2048 tokens, top-4 of 64 experts 2880x2880, 123 to 135 us).
 //
 // Every wait is bounded; a CTA that gives up sets the fault word, lets its copies land, frees its
 // tensor memory and returns.
@@ -175,6 +175,8 @@ struct Shape {
     static constexpr int kFacRow = NC + 4;    // floats of a block's scales: X's, then W's
 };
 
+// Two CTAs an SM: for the split form, whose clusters share SMs.  (The unsplit one asks for all of the
+// shared memory and is alone on its SM; under the same bound it spills 36 bytes a thread at 32 tokens.)
 template <typename T, int NC, bool kSplit, bool kGrad>
 __global__ void __launch_bounds__(kThreads, NC <= 32 ? 2 : 1)
     k_f8_mm(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -531,10 +533,11 @@ __global__ void __launch_bounds__(kThreads, NC <= 32 ? 2 : 1)
 //
 // kPair: two CTAs share each MMA (256 tokens; either brings its 128 and half of the outputs'
 // rows), so that an operand byte is fetched for twice the products.  Then the hand-over crosses the
-// pair, and tiles are coarser: better for one matrix with many tokens, not for experts (us: 2048
-// tokens 4096x14336 108, single CTAs 123; a prompt's experts 147 and 131).  Results leave by copies
-// from shared memory where rows are 16-byte aligned (4096 tokens 8192x2048 into f32 72 us, by stores
-// 79); an expert's last tile must not write past its rows, so there by stores.
+// pair, and tiles are coarser: better for one matrix with many tokens, not for experts (us, one after
+// the other on one GPU: 2048 tokens 4096x14336 108, single CTAs 123; a prompt's experts 147 and 131).
+// Results leave by copies from shared memory where rows are 16-byte aligned (4096 tokens 8192x2048
+// into f32 72 us, by stores 79); an expert's last tile must not write past its rows, so there by
+// stores.
 constexpr int kWN = 256;
 constexpr uint32_t kWHalf = kM * kF8Block;   // 128 rows of a stage
 constexpr int kWThreads = 384, kWEpiWarp = 4, kWEpiWarps = 8, kWCols = 128;
@@ -1107,7 +1110,9 @@ cudaError_t launch_f8_mm(const F8Product& p, cudaStream_t s) {
         // Past 64 tokens either kernel takes about as long for a block of its tile (1000 cycles),
         // and the other one's tiles are twice as large: it is slower only where this one is split
         // (us: 4096x4096, 256 tokens 14.9 by 2, 21.8 the other; 512 tokens, not split, 20.4 the
-        // other; 2303x2880, 333 tokens 12.8 by 2 and 21.5).
+        // other; 2303x2880, 333 tokens 12.8 by 2 and 21.5).  Up to 128 tokens its tiles are not full:
+        // a pair's second CTA then brings outputs but has no token (14336x4096: 64 tokens 15.5, 65 to
+        // 128 as long as 256, 21; this kernel unsplit was not timed there).
         wide = a.tn == 128 && split == 1;
     }
     if (wide) {

@@ -7,7 +7,9 @@
 // the code is the only rounding and the maximum of the block in integers is all that is reduced.
 //
 // Bound by HBM: each element is read once, its code (and rounded value) written.  A thread takes 16
-// elements, eight lanes a block.
+// elements, eight lanes a block: 32 bytes a load where x, its rows and the values are all 32-byte
+// aligned, else an element a load ([7996, 2880] bf16 with values 19 us; rows 2888 apart 35, values 16
+// bytes off 33.  Matrix [14336, 4096] f32 76 us, 16 bytes off 138; bf16 44 and 69).
 #include <cstdint>
 #include <type_traits>
 

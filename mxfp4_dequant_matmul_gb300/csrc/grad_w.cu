@@ -16,10 +16,10 @@
 // shared memory (in both operands: zero times whatever lies there may be NaN).  That last stage
 // lands on a barrier of its own CTA, a warp of which writes the zeros before it reports the stage.
 //
-// What bounds it: 4096 tokens top-4 of 16 experts 2880x2880 bf16 into f32, 235 us, 1.16 PFLOP/s: 182
-// without the stores, in which a stage takes about 700 cycles (the MMAs 512), as either CTA's 32 KB
-// come from L2 at some 50 bytes a cycle; the stores are as much again as a fifth of those copies.
-// One matrix 2048x2048, 8192 rows: 47 us, 1.45 PFLOP/s.
+// What bounds it: 4096 tokens top-4 of 16 experts 2880x2880 bf16 into f32, 235 to 255 us, 1.07 to 1.16
+// PFLOP/s: 182 without the stores, in which a stage takes about 700 cycles (the MMAs 512), as either
+// CTA's 32 KB come from L2 at some 50 bytes a cycle; the stores are as much again as a fifth of those
+// copies.  One matrix 2048x2048, 8192 rows: 47 us, 1.45 PFLOP/s; 4096x4096, 4096 rows 94 us, 1.46.
 //
 // Warps: copies, MMAs (even ranks), those zeros, eight for the sums.  Persistent: pair c takes tiles
 // c, c + pairs, ...  With few tiles and long sums (kSplit) a cluster of two or four pairs shares a
@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;   // (its one tile)
             }
             // 128 bytes of the 32 rows at a time, by copies from shared memory (which cut off at
-            // the matrix's edges): the warp goes on while they run (16 experts as above 235 us, by
-            // stores of whole lines 243, of 32 bytes of 32 rows 274; top-4 of 64 experts, 2048 tokens,
-            // into bf16 249, 280 and 314)
+            // the matrix's edges): the warp goes on while they run (one after the other on one GPU:
+            // 16 experts as above 235 us, by stores of whole lines 243, of 32 bytes of 32 rows 274;
+            // top-4 of 64 experts, 2048 tokens, into bf16 249, 280 and 314)
             const int r = t.r0 + rank * kM + quarter * 32, c0 = t.c0 + half * kCols;
             constexpr int kE = 128 / sizeof(T), kUnit = 16 / sizeof(T);
 #pragma unroll
